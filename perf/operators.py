@@ -233,7 +233,7 @@ def _run_own(s):
                                     cu_seqlens_k_host=s["cuk_host"], want_lse=True, **more)
         return {"o": o, "lse": lse, **({"kc": s["kc"], "vc": s["vc"]} if c["cache"] else {})}
     o = kda.window_decode(s["q"], s["k"], s["v"], s["kc"], s["vc"], s["pos"], window=c["window"], sinks=c["sinks"],
-                          slots=s["slots"], workspace="cache")
+                          slots=s["slots"])
     return {"o": o, "kc": s["kc"], "vc": s["vc"]}
 
 
