@@ -402,6 +402,211 @@ kda_status kda_short_conv_step(const kda_short_conv_step_args* args, void* strea
 kda_status kda_kcp_apply(const float* M, float* X, const float* add, int H, int d, int n, void* stream);
 
 /*
+ * The hybrid stack's other token mixers.  A model that interleaves linear
+ * attention with local softmax attention needs, beside KDA, the delta rule with
+ * one decay per head, the norm and rotation of its attention queries and keys,
+ * and attention through a window whose cache, like the delta rule's state, has
+ * a fixed size per sequence and is addressed by the same kind of slot table.
+ * The conventions at the top of this file hold for all of them.
+ */
+
+/*
+ * Gated delta rule with a SCALAR decay per value head and grouped heads, per
+ * sequence and value head h (key head h / (Hv / Hk)):
+ *   S_t = e^{g_t} (I - beta_t k_t k_t^T) S_{t-1} + beta_t k_t v_t^T,
+ *   o_t = scale * S_t^T q_t,
+ * g_t = -exp(A_h) Softplus(z_t)  (KDA_GATE_SOFTPLUS)  or
+ * g_t = g_min Sigmoid(exp(A_h) z_t)  (KDA_GATE_BOUNDED).  Any decay in (0, 1]
+ * is representable: nothing relies on the bound.
+ *
+ *   q, k  [T_total, Hk, 128]  dtype qkv_dtype;  v, o [T_total, Hv, 128] the same
+ *   z     [T_total, Hv] float32 decay logits (bias included)
+ *   beta  [T_total, Hv] float32;  A [Hv] float32
+ *   S0, S_T [num_seqs, Hv, 128, 128] float32 or NULL; S_T may equal S0
+ *   o may be NULL when only the final states are wanted.
+ * Hv a multiple of Hk.  cu_seqlens / cu_seqlens_host as for kda_prefill.
+ *
+ * kda_gdn_prefill, bf16: the chunked form (128-token chunks, tensor cores); the
+ * workspace must hold kda_gdn_prefill_workspace_size() bytes, else
+ * KDA_ERR_WORKSPACE.  Its first 4 bytes are the call's error word, read with
+ * kda_get_last_device_error.  Final states carry float32 precision: every
+ * product that reaches them splits its float32 operand into two bf16 parts.
+ * float32: the per-token recurrence on CUDA cores, no workspace.
+ * kda_gdn_prefill_recurrent: the per-token recurrence for either type.
+ * Rows of o outside every sequence do not exist (cu_seqlens ends at T_total);
+ * non-finite values of one sequence never reach another.
+ */
+typedef struct {
+    int num_seqs;
+    int T_total;
+    int Hk, Hv, dk, dv;
+    kda_dtype qkv_dtype;
+    const int32_t* cu_seqlens;       /* device */
+    const int32_t* cu_seqlens_host;  /* host   */
+    const void* q;
+    const void* k;
+    const void* v;
+    const float* z;
+    const float* beta;
+    const float* A;
+    float g_min;
+    float scale;
+    int qk_l2norm;        /* 1: L2-normalise q and k in FP32 (eps 1e-6) */
+    const float* S0;
+    void* o;
+    float* S_T;
+    void* workspace;
+    size_t workspace_bytes;
+    int gate_mode;        /* kda_gate */
+} kda_gdn_prefill_args;
+
+size_t kda_gdn_prefill_workspace_size(const kda_gdn_prefill_args* args);
+kda_status kda_gdn_prefill(const kda_gdn_prefill_args* args, void* stream);
+kda_status kda_gdn_prefill_recurrent(const kda_gdn_prefill_args* args, void* stream);
+
+/*
+ * One decode token per sequence of the same rule, states updated IN PLACE:
+ *   q, k [N, Hk, 128], v, o [N, Hv, 128] bf16; z, beta [N, Hv] float32;
+ *   state [num_slots, Hv, 128, 128] float32; slots [N] int32 or NULL (row n),
+ *   distinct.  A sequence whose slot lies outside [0, num_slots) is skipped:
+ *   its o row and every state row are left as they were.
+ */
+typedef struct {
+    int N, Hk, Hv, dk, dv, num_slots;
+    const void* q;
+    const void* k;
+    const void* v;
+    const float* z;
+    const float* beta;
+    const float* A;
+    float g_min;
+    float scale;
+    int qk_l2norm;
+    float* state;
+    const int32_t* slots;
+    void* o;
+    int gate_mode;        /* kda_gate */
+} kda_gdn_decode_args;
+
+kda_status kda_gdn_decode_step(const kda_gdn_decode_args* args, void* stream);
+
+/*
+ * RMSNorm of each query and key head with the position rotation in the same
+ * pass, for x a head of d channels at position p = positions[t]:
+ *   n = w (.) x / sqrt(mean(x^2) + eps)
+ *   (y_a, y_b) = (n_a cos - n_b sin, n_b cos + n_a sin),  cos, sin = row p, column i
+ * over the pairs i < rot/2 of the first rot channels, (a, b) = (i, i + rot/2), or
+ * (2i, 2i + 1) when interleaved; the channels from rot on are only normalised.
+ * All arithmetic in float32, rounded once.
+ *   q [T, Hq, d], k [T, Hkv, d] dtype (bf16 or float32), q_stride / k_stride
+ *     elements between tokens (a slice of a packed projection), heads dense;
+ *   q_out [T, Hq, d], k_out [T, Hkv, d] dense, same dtype (q_out may equal q,
+ *     k_out may equal k, when that tensor is dense too; no other overlap);
+ *   q_weight, k_weight [d] float32 or NULL (ones); cos, sin [num_pos, rot/2]
+ *     float32; positions [T] int32.
+ * A token whose position lies outside [0, num_pos) is skipped: its output rows
+ * are left as they were.
+ * Supported: d a multiple of 8 up to 256; rot a multiple of 16, 16 <= rot <= d;
+ * Hq, Hkv >= 0, not both 0; strides multiples of 16 bytes and >= heads * d.
+ */
+typedef struct {
+    int T, Hq, Hkv, d, rot, num_pos;
+    kda_dtype dtype;
+    const void* q;
+    const void* k;
+    long q_stride, k_stride;
+    const float* q_weight;
+    const float* k_weight;
+    float eps;
+    const float* cos;
+    const float* sin;
+    const int32_t* positions;
+    int interleaved;
+    void* q_out;
+    void* k_out;
+} kda_qk_norm_rope_args;
+
+kda_status kda_qk_norm_rope(const kda_qk_norm_rope_args* args, void* stream);
+
+/*
+ * Causal softmax attention through a sliding window with sinks, grouped heads
+ * (query head h reads key head h / (Hq / Hkv)): the query at position p of its
+ * sequence sees the keys at positions j <= p with j > p - window or j < sinks,
+ *   o = sum_j softmax_j(scale q.k_j) v_j,   lse = log sum_j exp(scale q.k_j).
+ *
+ *   q, o [T_total, Hq, d] bf16; k, v [Tk_total, Hkv, d] bf16, d = 64 or 128;
+ *   q_stride, k_stride, v_stride: elements between tokens (heads dense), o dense;
+ *   lse [T_total, Hq] float32 or NULL.
+ * Sequence n owns query rows [cu_seqlens[n], cu_seqlens[n+1]) and key rows
+ * [cu_seqlens_k[n], cu_seqlens_k[n+1]); its queries are the last of its keys
+ * (a prompt resumed after earlier tokens has more keys than queries), so it has
+ * at least as many keys as queries, else KDA_ERR_SEQLENS.  Keys and values that
+ * no query sees are never used, whatever they hold.
+ *
+ * Caches (optional, k_cache and v_cache together): [num_slots, cache_rows, Hkv, d]
+ * bf16, cache_rows >= sinks + window.  Position p of a sequence lives in row
+ *   p                                        for p < sinks,
+ *   sinks + (p - sinks) mod (cache_rows - sinks)  otherwise;
+ * sequence n writes the rows that kda_window_decode will read: its first
+ * min(sinks, len) and its last `window` positions, into slot slots[n] (or n).  Other
+ * rows keep what they held.  A slot outside [0, num_slots) is skipped.
+ * The caches must not overlap any other argument.
+ */
+typedef struct {
+    int num_seqs;
+    int T_total, Tk_total;
+    int Hq, Hkv, d;
+    int window, sinks;
+    kda_dtype dtype;
+    const int32_t* cu_seqlens;         /* device */
+    const int32_t* cu_seqlens_host;    /* host   */
+    const int32_t* cu_seqlens_k;       /* device */
+    const int32_t* cu_seqlens_k_host;  /* host   */
+    const void* q;
+    const void* k;
+    const void* v;
+    long q_stride, k_stride, v_stride;
+    float scale;
+    void* o;
+    float* lse;
+    void* k_cache;
+    void* v_cache;
+    const int32_t* slots;
+    int num_slots, cache_rows;
+} kda_window_prefill_args;
+
+kda_status kda_window_prefill(const kda_window_prefill_args* args, void* stream);
+
+/*
+ * One decode token per sequence of the same attention: the token's key and value
+ * are written into the caches at its position, and its query attends over them.
+ *   q, o [N, Hq, d], k, v [N, Hkv, d] bf16 with strides as above;
+ *   positions [N] int32: the position of the new token (= tokens before it);
+ *   caches as above, the rows of earlier visible positions already written;
+ *   slots [N] int32 or NULL (row n), distinct.
+ * A sequence whose slot lies outside [0, num_slots), or whose position is
+ * negative, is skipped: its o row and the caches are left as they were.
+ */
+typedef struct {
+    int N, Hq, Hkv, d;
+    int window, sinks;
+    kda_dtype dtype;
+    const void* q;
+    const void* k;
+    const void* v;
+    long q_stride, k_stride, v_stride;
+    float scale;
+    void* k_cache;
+    void* v_cache;
+    const int32_t* positions;
+    const int32_t* slots;
+    int num_slots, cache_rows;
+    void* o;
+} kda_window_decode_args;
+
+kda_status kda_window_decode(const kda_window_decode_args* args, void* stream);
+
+/*
  * Device-side error report of the tensor-core prefill (library plumbing: the
  * KDA pages have no counterpart).  Every wait of a prefill kernel on an
  * asynchronous copy, a tensor-core operation or a peer CTA is bounded; a wait

@@ -9,6 +9,7 @@ there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -28,7 +29,9 @@ EXPORTED = ["kda_prefill", "kda_prefill_recurrent", "kda_prefill_workspace_size"
             "kda_version", "kda_launch_count", "kda_prefill_noalloc", "kda_prefill_snapshot_count",
             "kda_short_conv", "kda_short_conv_step", "kda_kcp_apply", "kda_prefill_records",
             "kda_prefill_scan", "kda_get_last_device_error", "kda_debug_set_wait_limit",
-            "kda_prefill_from_host", "kda_prefill_from_host_staging_size"]
+            "kda_prefill_from_host", "kda_prefill_from_host_staging_size",
+            "kda_gdn_prefill", "kda_gdn_prefill_recurrent", "kda_gdn_prefill_workspace_size",
+            "kda_gdn_decode_step", "kda_qk_norm_rope", "kda_window_prefill", "kda_window_decode"]
 
 _vp = ctypes.c_void_p
 
@@ -79,6 +82,64 @@ class ShortConvStepArgs(ctypes.Structure):
         ("dtype", ctypes.c_int),
         ("x", _vp), ("weight", _vp), ("bias", _vp), ("state", _vp), ("slots", _vp),
         ("y", _vp), ("activation", ctypes.c_int),
+    ]
+
+
+class GdnPrefillArgs(ctypes.Structure):
+    _fields_ = [
+        ("num_seqs", ctypes.c_int), ("T_total", ctypes.c_int),
+        ("Hk", ctypes.c_int), ("Hv", ctypes.c_int), ("dk", ctypes.c_int), ("dv", ctypes.c_int),
+        ("qkv_dtype", ctypes.c_int),
+        ("cu_seqlens", _vp), ("cu_seqlens_host", _vp),
+        ("q", _vp), ("k", _vp), ("v", _vp), ("z", _vp), ("beta", _vp), ("A", _vp),
+        ("g_min", ctypes.c_float), ("scale", ctypes.c_float), ("qk_l2norm", ctypes.c_int),
+        ("S0", _vp), ("o", _vp), ("S_T", _vp),
+        ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t), ("gate_mode", ctypes.c_int),
+    ]
+
+
+class GdnDecodeArgs(ctypes.Structure):
+    _fields_ = [
+        ("N", ctypes.c_int), ("Hk", ctypes.c_int), ("Hv", ctypes.c_int), ("dk", ctypes.c_int), ("dv", ctypes.c_int),
+        ("num_slots", ctypes.c_int),
+        ("q", _vp), ("k", _vp), ("v", _vp), ("z", _vp), ("beta", _vp), ("A", _vp),
+        ("g_min", ctypes.c_float), ("scale", ctypes.c_float), ("qk_l2norm", ctypes.c_int),
+        ("state", _vp), ("slots", _vp), ("o", _vp), ("gate_mode", ctypes.c_int),
+    ]
+
+
+class QkNormRopeArgs(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("d", ctypes.c_int), ("rot", ctypes.c_int),
+        ("num_pos", ctypes.c_int), ("dtype", ctypes.c_int),
+        ("q", _vp), ("k", _vp), ("q_stride", ctypes.c_long), ("k_stride", ctypes.c_long),
+        ("q_weight", _vp), ("k_weight", _vp), ("eps", ctypes.c_float),
+        ("cos", _vp), ("sin", _vp), ("positions", _vp), ("interleaved", ctypes.c_int),
+        ("q_out", _vp), ("k_out", _vp),
+    ]
+
+
+class WindowPrefillArgs(ctypes.Structure):
+    _fields_ = [
+        ("num_seqs", ctypes.c_int), ("T_total", ctypes.c_int), ("Tk_total", ctypes.c_int),
+        ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("d", ctypes.c_int),
+        ("window", ctypes.c_int), ("sinks", ctypes.c_int), ("dtype", ctypes.c_int),
+        ("cu_seqlens", _vp), ("cu_seqlens_host", _vp), ("cu_seqlens_k", _vp), ("cu_seqlens_k_host", _vp),
+        ("q", _vp), ("k", _vp), ("v", _vp),
+        ("q_stride", ctypes.c_long), ("k_stride", ctypes.c_long), ("v_stride", ctypes.c_long),
+        ("scale", ctypes.c_float), ("o", _vp), ("lse", _vp),
+        ("k_cache", _vp), ("v_cache", _vp), ("slots", _vp), ("num_slots", ctypes.c_int), ("cache_rows", ctypes.c_int),
+    ]
+
+
+class WindowDecodeArgs(ctypes.Structure):
+    _fields_ = [
+        ("N", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("d", ctypes.c_int),
+        ("window", ctypes.c_int), ("sinks", ctypes.c_int), ("dtype", ctypes.c_int),
+        ("q", _vp), ("k", _vp), ("v", _vp),
+        ("q_stride", ctypes.c_long), ("k_stride", ctypes.c_long), ("v_stride", ctypes.c_long),
+        ("scale", ctypes.c_float), ("k_cache", _vp), ("v_cache", _vp),
+        ("positions", _vp), ("slots", _vp), ("num_slots", ctypes.c_int), ("cache_rows", ctypes.c_int), ("o", _vp),
     ]
 
 
@@ -136,6 +197,13 @@ def load_library(path: str = LIB_PATH):
     lib.kda_prefill_from_host_staging_size.argtypes = [ctypes.POINTER(PrefillArgs), ctypes.c_int]
     lib.kda_prefill_from_host_staging_size.restype = ctypes.c_size_t
     lib.kda_debug_set_wait_limit.restype = ctypes.c_uint32
+    for name, struct in (("kda_gdn_prefill", GdnPrefillArgs), ("kda_gdn_prefill_recurrent", GdnPrefillArgs),
+                         ("kda_gdn_decode_step", GdnDecodeArgs), ("kda_qk_norm_rope", QkNormRopeArgs),
+                         ("kda_window_prefill", WindowPrefillArgs), ("kda_window_decode", WindowDecodeArgs)):
+        fn = getattr(lib, name)
+        fn.argtypes, fn.restype = [ctypes.POINTER(struct), _vp], ctypes.c_int
+    lib.kda_gdn_prefill_workspace_size.argtypes = [ctypes.POINTER(GdnPrefillArgs)]
+    lib.kda_gdn_prefill_workspace_size.restype = ctypes.c_size_t
     _lib = lib
     return lib
 
@@ -520,3 +588,275 @@ def gate_norm(o, g_in, norm_w=None, eps=1e-6, out=None, stream=None):
                              ctypes.c_long(rows), int(dv), _dtype_code(o), _stream(stream)),
            "kda_gate_norm")
     return y
+
+
+# ---------------------------------------------------------------------------
+# the hybrid stack's other token mixers.  Each takes stream=None (the current
+# stream of its tensors' device) beside the arguments shown.
+# ---------------------------------------------------------------------------
+
+def _dense(name, t, shape, dtype, dev):
+    """``t``'s address, once it is what the entry point reads: ``shape`` (None: any
+    extent), ``dtype``, contiguous, on ``dev``.  None stays None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.device != dev or not t.is_contiguous() or len(t.shape) != len(shape) or \
+            any(e is not None and e != x for e, x in zip(shape, t.shape)):
+        raise KDAError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, "
+                       f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+    return t.data_ptr()
+
+
+def _heads(name, t, shape, dtype, dev):
+    """Address and token stride of a [tokens, heads, d] tensor with dense heads:
+    contiguous, or a slice of a packed projection."""
+    if t.dtype != dtype or t.device != dev or tuple(t.shape) != tuple(shape):
+        raise KDAError(f"{name}: expected {dtype} of shape {tuple(shape)} on {dev}, "
+                       f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    n, h, d = shape
+    st = t.stride()
+    if (d > 1 and st[2] != 1) or (h > 1 and st[1] != d):
+        raise KDAError(f"{name}: the heads of a token must be dense, got strides {st}")
+    return t.data_ptr(), (st[0] if n > 1 else h * d)
+
+
+def _launch(fn, args, dev, what):
+    """The call on the current stream of the tensors' device."""
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            status = fn(ctypes.byref(args), stream)
+    else:
+        status = fn(ctypes.byref(args), stream)
+    if status != 0:
+        _check(status, what)
+
+
+def _on_stream(f):
+    """Runs the call with ``stream`` (when given) current, so that what it allocates
+    belongs to the stream that uses it."""
+    @functools.wraps(f)
+    def call(q, *args, stream=None, **kw):
+        if stream is None:
+            return f(q, *args, **kw)
+        if q.device != stream.device:
+            raise KDAError(f"the stream is on {stream.device}, the tensors on {q.device}")
+        with torch.cuda.stream(stream):
+            return f(q, *args, **kw)
+    return call
+
+
+def _cuda_device(t, name):
+    if t.device.type != "cuda":
+        raise KDAError(f"{name} must be a CUDA tensor, got {t.device}")
+    return t.device
+
+
+def _cu_pair(cu, cu_host, total, dev, name="cu_seqlens"):
+    """Device and host copy of sequence bounds.  cu None: one sequence.  cu_host None:
+    copied from the device (synchronises); a caller who has the lengths on the host
+    passes both and saves that."""
+    if cu is None:
+        if cu_host is None:
+            cu_host = torch.tensor([0, total], dtype=torch.int32)
+        cu = cu_host.to(dev)
+    elif cu_host is None:
+        cu_host = cu.to("cpu")
+    _dense(name, cu, (None,), torch.int32, dev)
+    if cu_host.device.type != "cpu" or cu_host.dtype != torch.int32 or not cu_host.is_contiguous() or \
+            cu_host.shape != cu.shape or cu.shape[0] < 1:
+        raise KDAError(f"{name}_host must be the contiguous int32 host copy of {name}")
+    return cu, cu_host
+
+
+def _gate_code(gate):
+    if gate not in GATES:
+        raise KDAError(f"gate must be one of {sorted(GATES)}, got {gate!r}")
+    return GATES[gate]
+
+
+def _cached_workspace(dev, need):
+    key = (dev.type, dev.index)
+    ws = _WS_CACHE.get(key)
+    if ws is None or ws.numel() < need:
+        _WS_CACHE[key] = ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    return ws
+
+
+@_on_stream
+def gdn_prefill(q, k, v, z, beta, A, cu_seqlens=None, cu_seqlens_host=None, S0=None, g_min=-5.0, scale=1.0,
+                qk_l2norm=True, want_o=True, want_state=True, out=None, recurrent=False, workspace=None,
+                gate="softplus"):
+    """Gated delta rule with one decay per value head, over packed sequences, through
+    ``kda_gdn_prefill`` (``recurrent=True``: ``kda_gdn_prefill_recurrent``).
+
+    q, k: [T, Hk, 128]; v: [T, Hv, 128], Hv a multiple of Hk (bf16, or float32: the
+    per-token recurrence); z, beta: [T, Hv] f32; A: [Hv] f32; cu_seqlens int32 [N+1]
+    on the device (None = one sequence) and its host copy; S0 [N, Hv, 128, 128] f32
+    or None.  out: {"o": ..., "S_T": ...} to write into.  workspace as for ``prefill``
+    (a uint8 tensor, None, or "cache": one buffer per device, for calls that follow
+    one another on one stream).  Returns (o, S_T).
+    """
+    dev = _cuda_device(q, "q")
+    T, Hk, dk = q.shape
+    Hv, dv = v.shape[1], v.shape[2]
+    cu, cu_host = _cu_pair(cu_seqlens, cu_seqlens_host, T, dev)
+    N = cu_host.shape[0] - 1
+    o = (out["o"] if out else torch.empty((T, Hv, dv), dtype=q.dtype, device=dev)) if want_o else None
+    S_T = (out["S_T"] if out else torch.empty((N, Hv, dk, dv), dtype=torch.float32, device=dev)) if want_state else None
+    f32 = torch.float32
+    a = GdnPrefillArgs(
+        N, T, Hk, Hv, dk, dv, _dtype_code(q), cu.data_ptr(), cu_host.data_ptr(),
+        _dense("q", q, (T, Hk, dk), q.dtype, dev), _dense("k", k, (T, Hk, dk), q.dtype, dev),
+        _dense("v", v, (T, Hv, dv), q.dtype, dev), _dense("z", z, (T, Hv), f32, dev),
+        _dense("beta", beta, (T, Hv), f32, dev), _dense("A", A, (Hv,), f32, dev),
+        g_min, scale, 1 if qk_l2norm else 0, _dense("S0", S0, (N, Hv, dk, dv), f32, dev),
+        _dense("o", o, (T, Hv, dv), q.dtype, dev), _dense("S_T", S_T, (N, Hv, dk, dv), f32, dev),
+        None, 0, _gate_code(gate))
+    lib = load_library()
+    if recurrent:
+        _launch(lib.kda_gdn_prefill_recurrent, a, dev, "kda_gdn_prefill_recurrent")
+        return o, S_T
+    need = lib.kda_gdn_prefill_workspace_size(ctypes.byref(a))
+    if need:
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        elif isinstance(workspace, str):
+            if workspace != "cache":
+                raise KDAError(f"workspace must be a tensor, None or 'cache', got {workspace!r}")
+            workspace = _cached_workspace(dev, need)
+        elif workspace.device != dev or not workspace.is_contiguous():
+            raise KDAError(f"the workspace must be a contiguous tensor on {dev}")
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _launch(lib.kda_gdn_prefill, a, dev, "kda_gdn_prefill")
+    return o, S_T
+
+
+@_on_stream
+def gdn_decode_step(q, k, v, z, beta, A, state, slots=None, g_min=-5.0, scale=1.0, qk_l2norm=True, out=None,
+                    gate="softplus"):
+    """One decode token per sequence of the scalar-gated delta rule through
+    ``kda_gdn_decode_step``; ``state`` [slots, Hv, 128, 128] f32 is updated in place.
+
+    q, k: [N, Hk, 128], v: [N, Hv, 128] bf16; z, beta: [N, Hv] f32; A: [Hv] f32;
+    slots int32 [N] or None (row n).  Returns o [N, Hv, 128].
+    """
+    dev = _cuda_device(q, "q")
+    N, Hk, dk = q.shape
+    Hv, dv = v.shape[1], v.shape[2]
+    bf, f32 = torch.bfloat16, torch.float32
+    o = torch.empty((N, Hv, dv), dtype=bf, device=dev) if out is None else out
+    a = GdnDecodeArgs(
+        N, Hk, Hv, dk, dv, state.shape[0],
+        _dense("q", q, (N, Hk, dk), bf, dev), _dense("k", k, (N, Hk, dk), bf, dev),
+        _dense("v", v, (N, Hv, dv), bf, dev), _dense("z", z, (N, Hv), f32, dev),
+        _dense("beta", beta, (N, Hv), f32, dev), _dense("A", A, (Hv,), f32, dev),
+        g_min, scale, 1 if qk_l2norm else 0, _dense("state", state, (None, Hv, dk, dv), f32, dev),
+        _dense("slots", slots, (N,), torch.int32, dev), _dense("out", o, (N, Hv, dv), bf, dev), _gate_code(gate))
+    _launch(load_library().kda_gdn_decode_step, a, dev, "kda_gdn_decode_step")
+    return o
+
+
+@_on_stream
+def qk_norm_rope(q, k, cos, sin, positions, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, out=None):
+    """RMSNorm of each query and key head and the rotation by position, in one pass,
+    through ``kda_qk_norm_rope``.
+
+    q: [T, Hq, d], k: [T, Hkv, d] (bf16 or f32; contiguous, or slices of a packed
+    projection), cos, sin: [positions, rot/2] f32, positions: int32 [T];
+    q_weight, k_weight: [d] f32 or None.  out: (q_out, k_out) to write into (q and k
+    themselves when they are contiguous).  Returns (q_out, k_out), contiguous.
+    """
+    dev = _cuda_device(q, "q")
+    T, Hq, d = q.shape
+    Hkv, half = k.shape[1], cos.shape[1]
+    dt, f32 = q.dtype, torch.float32
+    qo, ko = (torch.empty((T, Hq, d), dtype=dt, device=dev), torch.empty((T, Hkv, d), dtype=dt, device=dev)) \
+        if out is None else out
+    qp, qs = _heads("q", q, (T, Hq, d), dt, dev)
+    kp, ks = _heads("k", k, (T, Hkv, d), dt, dev)
+    a = QkNormRopeArgs(
+        T, Hq, Hkv, d, 2 * half, cos.shape[0], _dtype_code(q), qp, kp, qs, ks,
+        _dense("q_weight", q_weight, (d,), f32, dev), _dense("k_weight", k_weight, (d,), f32, dev), eps,
+        _dense("cos", cos, (None, half), f32, dev), _dense("sin", sin, (cos.shape[0], half), f32, dev),
+        _dense("positions", positions, (T,), torch.int32, dev), 1 if interleaved else 0,
+        _dense("q_out", qo, (T, Hq, d), dt, dev), _dense("k_out", ko, (T, Hkv, d), dt, dev))
+    _launch(load_library().kda_qk_norm_rope, a, dev, "kda_qk_norm_rope")
+    return qo, ko
+
+
+def _caches(k_cache, v_cache, Hkv, d, dev):
+    if (k_cache is None) != (v_cache is None):
+        raise KDAError("k_cache and v_cache are given together")
+    if k_cache is None:
+        return None, None, 0, 0
+    shape = (k_cache.shape[0], k_cache.shape[1], Hkv, d) if len(k_cache.shape) == 4 else (None, None, Hkv, d)
+    return (_dense("k_cache", k_cache, shape, torch.bfloat16, dev), _dense("v_cache", v_cache, shape, torch.bfloat16, dev),
+            k_cache.shape[0], k_cache.shape[1])
+
+
+@_on_stream
+def window_prefill(q, k, v, window, sinks=0, cu_seqlens=None, cu_seqlens_host=None, cu_seqlens_k=None,
+                   cu_seqlens_k_host=None, scale=None, want_lse=False, k_cache=None, v_cache=None, slots=None, out=None):
+    """Causal attention through a sliding window with sinks over packed sequences,
+    through ``kda_window_prefill``.
+
+    q: [T, Hq, d] bf16, k, v: [Tk, Hkv, d] bf16 (contiguous, or slices of a packed
+    projection), d = 64 or 128, Hq a multiple of Hkv; the query at position p sees
+    the keys j <= p with j > p - window or j < sinks.  cu_seqlens bounds the
+    queries, cu_seqlens_k the keys (None: the same bounds; a sequence's queries are
+    the last of its keys).  scale: d ** -0.5 by default.  k_cache, v_cache
+    [num_slots, rows >= sinks + window, Hkv, d] bf16 receive the rows that
+    ``window_decode`` goes on from, in slot slots[n] (or n).
+    Returns o, or (o, lse [T, Hq] f32) with want_lse.
+    """
+    dev = _cuda_device(q, "q")
+    T, Hq, d = q.shape
+    Tk, Hkv = k.shape[0], k.shape[1]
+    bf = torch.bfloat16
+    cu, cu_host = _cu_pair(cu_seqlens, cu_seqlens_host, T, dev)
+    if cu_seqlens_k is not None or cu_seqlens_k_host is not None:
+        cuk, cuk_host = _cu_pair(cu_seqlens_k, cu_seqlens_k_host, Tk, dev, "cu_seqlens_k")
+    elif cu_seqlens is None and cu_seqlens_host is None and Tk != T:
+        cuk, cuk_host = _cu_pair(None, None, Tk, dev, "cu_seqlens_k")
+    else:
+        cuk, cuk_host = cu, cu_host
+    if cuk_host.shape != cu_host.shape:
+        raise KDAError("cu_seqlens and cu_seqlens_k bound the same sequences")
+    N = cu_host.shape[0] - 1
+    o = torch.empty((T, Hq, d), dtype=bf, device=dev) if out is None else out
+    lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if want_lse else None
+    qp, qs = _heads("q", q, (T, Hq, d), bf, dev)
+    kp, ks = _heads("k", k, (Tk, Hkv, d), bf, dev)
+    vp, vs = _heads("v", v, (Tk, Hkv, d), bf, dev)
+    kc, vc, num_slots, rows = _caches(k_cache, v_cache, Hkv, d, dev)
+    a = WindowPrefillArgs(
+        N, T, Tk, Hq, Hkv, d, window, sinks, KDA_BF16, cu.data_ptr(), cu_host.data_ptr(), cuk.data_ptr(),
+        cuk_host.data_ptr(), qp, kp, vp, qs, ks, vs, d ** -0.5 if scale is None else scale,
+        _dense("out", o, (T, Hq, d), bf, dev), lse.data_ptr() if want_lse else None, kc, vc,
+        _dense("slots", slots, (N,), torch.int32, dev), num_slots, rows)
+    _launch(load_library().kda_window_prefill, a, dev, "kda_window_prefill")
+    return (o, lse) if want_lse else o
+
+
+@_on_stream
+def window_decode(q, k, v, k_cache, v_cache, positions, window, sinks=0, slots=None, scale=None, out=None):
+    """One decode token per sequence of the windowed attention through
+    ``kda_window_decode``: k, v [N, Hkv, d] are written into the ring caches at
+    ``positions`` (int32 [N], the tokens before the new one), q [N, Hq, d] attends
+    over them.  Returns o [N, Hq, d]; the caches are updated in place.
+    """
+    dev = _cuda_device(q, "q")
+    N, Hq, d = q.shape
+    Hkv, bf = k.shape[1], torch.bfloat16
+    o = torch.empty((N, Hq, d), dtype=bf, device=dev) if out is None else out
+    qp, qs = _heads("q", q, (N, Hq, d), bf, dev)
+    kp, ks = _heads("k", k, (N, Hkv, d), bf, dev)
+    vp, vs = _heads("v", v, (N, Hkv, d), bf, dev)
+    kc, vc, num_slots, rows = _caches(k_cache, v_cache, Hkv, d, dev)
+    a = WindowDecodeArgs(
+        N, Hq, Hkv, d, window, sinks, KDA_BF16, qp, kp, vp, qs, ks, vs, d ** -0.5 if scale is None else scale, kc, vc,
+        _dense("positions", positions, (N,), torch.int32, dev), _dense("slots", slots, (N,), torch.int32, dev),
+        num_slots, rows, _dense("out", o, (N, Hq, d), bf, dev))
+    _launch(load_library().kda_window_decode, a, dev, "kda_window_decode")
+    return o
