@@ -617,8 +617,9 @@ kda_status kda_window_decode(const kda_window_decode_args* args, void* stream);
  *
  * kda_get_last_device_error waits for the work queued on `stream`, then reads
  * and clears the error word of `workspace` (the workspace the prefill calls
- * used), or, with workspace == NULL, of the fixed array kda_prefill_noalloc
- * uses on the current device.  Returns KDA_OK when no wait gave up,
+ * used), or, with workspace == NULL, those of the fixed array kda_prefill_noalloc
+ * uses on the current device and of kda_window_prefill (which needs no workspace;
+ * its word stays set until it is read).  Returns KDA_OK when no wait gave up,
  * KDA_ERR_TIMEOUT when one did, KDA_ERR_CUDA when the read failed.  It
  * allocates nothing.  Call it on the stream of the prefill calls (or after
  * synchronising them); calls on other streams that use the same workspace

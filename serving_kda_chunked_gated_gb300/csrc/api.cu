@@ -27,6 +27,9 @@ cudaError_t launch_short_conv(const kda_short_conv_args& a, cudaStream_t s);
 cudaError_t launch_kcp_apply(const float* M, float* X, const float* Add, int H, int d, int n, cudaStream_t s);
 cudaError_t launch_short_conv_step(const kda_short_conv_step_args& a, cudaStream_t s);
 cudaError_t noalloc_scratch_address(void** out);
+namespace win {
+cudaError_t error_word(void** out);
+}
 }  // namespace kda
 
 static thread_local char g_last_error[256] = "no error";
@@ -84,7 +87,15 @@ kda_status kda_get_last_device_error(void* workspace, void* stream) {
     int32_t h = 0;
     if ((e = cudaMemcpyAsync(&h, word, sizeof(h), cudaMemcpyDeviceToHost, s)) != cudaSuccess) return cuda_fail(e);
     if ((e = cudaMemsetAsync(word, 0, sizeof(h), s)) != cudaSuccess) return cuda_fail(e);
+    int32_t w = 0;
+    void* window = nullptr;
+    if (!workspace) {   // the window prefill has no workspace: its word is the library's too
+        if ((e = kda::win::error_word(&window)) != cudaSuccess) return cuda_fail(e);
+        if ((e = cudaMemcpyAsync(&w, window, sizeof(w), cudaMemcpyDeviceToHost, s)) != cudaSuccess) return cuda_fail(e);
+        if ((e = cudaMemsetAsync(window, 0, sizeof(w), s)) != cudaSuccess) return cuda_fail(e);
+    }
     if ((e = cudaStreamSynchronize(s)) != cudaSuccess) return cuda_fail(e);
+    h |= w;
     return h ? KDA_ERR_TIMEOUT : KDA_OK;
 }
 

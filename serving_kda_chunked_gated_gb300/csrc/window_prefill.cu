@@ -1,83 +1,481 @@
-// Sliding-window attention with sinks over packed sequences.
+// Sliding-window attention with sinks over packed sequences, on tcgen05.
 //
-// One warp per (query, query head): 32 visible keys at a time, one per lane, with
-// a running maximum and sum.
-#include "kda_common.cuh"
-
+// Work unit: 256 rows of one key head's attention, two tiles A and B of 128 rows.
+// Row r of a tile is query r / GP and head r % GP, GP the largest power of two that
+// divides the group (at most 16): the heads that share a key head share its tiles,
+// and a unit covers few queries, so its key range is hardly wider than the window
+// itself.  The unit's keys are the window's union [lo, p_last] in tiles of 128 (the
+// last one only as wide as needed, in steps of 32), then the sinks before lo.
+//
+//   S = Q K^T (TMEM, 128 x 128 fp32 per tile), P = exp2(c S - m) in registers with the
+//   running row maximum m and sum l, P back to TMEM as bf16 over S, O += P V (TMEM).
+// A new maximum rescales O only when it exceeds the reference by more than 2^8 (the
+// weights then stay below 2^8, which costs bf16 and fp32 nothing): O is rarely touched.
+//
+// Roles of the 12 warps: 0-3 the softmax of tile A, 4-7 that of tile B (one thread per
+// row), 8 the TMA loads, 9 the MMAs, 10 and 11 only fill the third warpgroup.  While one tile is in its softmax the tensor core
+// works on the other.  CTAs are persistent: the loads and the first S of the next unit
+// run while the softmax warps write this unit's rows.
+//
+// V is the B operand straight from the TMA tile (MN-major), Q and K are K-major; no
+// thread touches an operand but for zeroing the unseen rows of edge tiles (0 x NaN).
 #include <math.h>
+
+#include "kda_common.cuh"
+#include "tcgen05.cuh"
+#include "tma_host.cuh"
 
 namespace kda {
 namespace win {
 
+constexpr int PF_THREADS = 384;
+constexpr int KT = 128;                     // keys per tile
+
 template <int D>
-__global__ void __launch_bounds__(256)
-window_prefill_kernel(kda_window_prefill_args a) {
-    __shared__ float s_q[8][D];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long unit = (long)blockIdx.x * 8 + warp;
-    if (unit >= (long)a.T_total * a.Hq) return;
-    const int t = (int)(unit / a.Hq), h = (int)(unit % a.Hq), hk = h / (a.Hq / a.Hkv);
-    int lo = 0, hi = a.num_seqs;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.cu_seqlens[mid] <= t) lo = mid; else hi = mid;
+struct PF {
+    static constexpr int QB = 128 * D * 2;          // bytes of one Q tile
+    static constexpr int SB = KT * D * 2;           // bytes of one K or V tile (ring slot)
+    static constexpr int SLOTS = D == 128 ? 5 : 10;
+    static constexpr int SMEM = 2 * QB + SLOTS * SB + 1024;   // + alignment slack
+};
+
+__device__ int g_window_error;              // ERR_ bits of calls whose bounded waits gave up (sticky until read)
+
+struct PfParams {
+    kda_window_prefill_args a;
+    int gp, subs;                           // rows' heads per tile; head subgroups per key head
+    int qpt;                                // queries per tile (128 / gp)
+    long units;
+    float c;                                // |scale| log2 e
+    int neg;                                // scale < 0: S = -Q K^T
+    int wide;                               // o is 32-byte aligned
+    uint32_t wait_limit;
+};
+
+// One unit's geometry, from its index; called by whole warps.  Units count down so
+// that a sequence's end, where the windows are full, comes first.
+struct Unit {
+    int q0, q1;        // packed query rows [q0, q1) of the unit
+    int p0;            // position of query q0 in its sequence
+    int k0;            // packed key row of position 0
+    int lo, hi;        // window keys: positions [lo, hi]
+    int nsink;         // sink keys before lo: positions [0, nsink)
+    int nwin, ntiles;  // window tiles, all tiles
+    int hk, h0;        // key head, first query head
+    // tile i: first position and width (a multiple of 32, at most KT)
+    KDA_DEV void tile(int i, int* j0, int* width) const {
+        const bool w = i < nwin;
+        *j0 = w ? lo + i * KT : (i - nwin) * KT;
+        const int left = (w ? hi + 1 : nsink) - *j0;
+        *width = left >= KT ? KT : (left + 31) & ~31;
     }
-    const int k0 = a.cu_seqlens_k[lo], k1 = a.cu_seqlens_k[lo + 1];
-    const int pos = (k1 - k0) - (a.cu_seqlens[lo + 1] - t);
-    const int first = max(a.sinks, pos - a.window + 1), ns = min(a.sinks, pos + 1);
-    const int total = ns + max(0, pos - first + 1);
-    for (int c = lane; c < D; c += 32)
-        s_q[warp][c] = bf16_to_f(reinterpret_cast<const uint16_t*>(a.q)[(size_t)t * a.q_stride + (size_t)h * D + c]);
-    __syncwarp();
-    float m = -INFINITY, l = 0.f, o[D / 32] = {};
-    for (int u0 = 0; u0 < total; u0 += 32) {
-        const int u = u0 + lane, j = u < ns ? u : first + (u - ns);
-        float s = -INFINITY;
-        if (u < total) {
-            s = 0.f;
-            const uint16_t* kr = reinterpret_cast<const uint16_t*>(a.k) + (size_t)(k0 + j) * a.k_stride + (size_t)hk * D;
-            for (int c = 0; c < D; c += 8) {
-                float x[8];
-                load8_bf16(kr + c, x);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) s += x[i] * s_q[warp][c + i];
-            }
-            s *= a.scale * 1.4426950408889634f;
-        }
-        float x = s;
-#pragma unroll
-        for (int i = 16; i > 0; i >>= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, i));
-        const float mn = fmaxf(m, x), b = mn == -INFINITY ? 0.f : mn;
-        const float c = exp2f(m - b), p = exp2f(s - b);
-        l = l * c + p;
-        m = mn;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) o[i] *= c;
-        const int cnt = min(32, total - u0);
-        for (int y = 0; y < cnt; ++y) {
-            const float w = __shfl_sync(~0u, p, y);
-            const int jj = __shfl_sync(~0u, j, y);
-            const uint16_t* vr = reinterpret_cast<const uint16_t*>(a.v) + (size_t)(k0 + jj) * a.v_stride + (size_t)hk * D;
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) o[i] += w * bf16_to_f(vr[lane + 32 * i]);
-        }
+    // rows of tile i that some query of the unit sees
+    KDA_DEV int seen(int i) const {
+        const bool w = i < nwin;
+        const int left = w ? hi + 1 - (lo + i * KT) : nsink - (i - nwin) * KT;
+        return left < KT ? left : KT;
     }
-    l = warp_sum(l);
-    const size_t row = (size_t)t * a.Hq + h;
+};
+
+KDA_DEV Unit unit_at(const PfParams& p, long u) {
+    u = p.units - 1 - u;
+    const int heads = p.a.Hkv * p.subs;
+    const int hs = (int)(u % heads);
+    long b = u / heads;                     // block of 2 qpt queries, counted over the sequences
+    const int lane = threadIdx.x & 31, per = 2 * p.qpt;
+    int n = 0;
+    for (int base = 0;; base += 32) {       // 32 sequences at a time; ends: u < units
+        const int m = base + lane;
+        const int len = m < p.a.num_seqs ? p.a.cu_seqlens[m + 1] - p.a.cu_seqlens[m] : 0;
+        int pre = (len + per - 1) / per;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-        reinterpret_cast<uint16_t*>(a.o)[row * D + lane + 32 * i] = f_to_bf16(o[i] / l);
-    if (a.lse && lane == 0) a.lse[row] = 0.6931471805599453f * m + logf(l);
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(~0u, pre, o);
+            if (lane >= o) pre += x;
+        }
+        const unsigned hit = __ballot_sync(~0u, b < pre);
+        if (hit) {
+            const int f = __ffs(hit) - 1;
+            const int before = __shfl_sync(~0u, pre, f > 0 ? f - 1 : 0);
+            if (f > 0) b -= before;
+            n = base + f;
+            break;
+        }
+        b -= __shfl_sync(~0u, pre, 31);
+        if (base + 32 >= p.a.num_seqs) break;
+    }
+    Unit x;
+    const int c0 = p.a.cu_seqlens[n], c1 = p.a.cu_seqlens[n + 1];
+    x.k0 = p.a.cu_seqlens_k[n];
+    const int lk = p.a.cu_seqlens_k[n + 1] - x.k0;
+    x.q0 = c0 + (int)b * per;
+    x.q1 = min(c1, x.q0 + per);
+    x.p0 = lk - (c1 - c0) + (int)b * per;
+    x.hi = x.p0 + (x.q1 - x.q0) - 1;
+    x.lo = max(0, x.p0 - p.a.window + 1);
+    x.nsink = min(p.a.sinks, x.lo);
+    x.nwin = (x.hi - x.lo + KT) / KT;
+    x.ntiles = x.nwin + (x.nsink + KT - 1) / KT;
+    x.hk = hs / p.subs;
+    x.h0 = x.hk * (p.a.Hq / p.a.Hkv) + (hs % p.subs) * p.gp;
+    return x;
 }
 
-cudaError_t launch_prefill(const kda_window_prefill_args& a, cudaStream_t s) {
-    const long blocks = ((long)a.T_total * a.Hq + 7) / 8;
-    if (blocks == 0) return cudaSuccess;
-    if (a.d == 64) window_prefill_kernel<64><<<(unsigned)blocks, 256, 0, s>>>(a);
-    else window_prefill_kernel<128><<<(unsigned)blocks, 256, 0, s>>>(a);
+// A wait of a whole warp: every lane gets the same answer.
+KDA_DEV bool wait_warp(uint64_t* bar, uint32_t parity, uint32_t limit, volatile int* abort) {
+    return __all_sync(~0u, tc::mbar_wait_role(bar, parity, limit, abort));
+}
+
+template <int D>
+__global__ void __launch_bounds__(PF_THREADS, 1)
+window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant__ CUtensorMap mq,
+                      const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+    using L = PF<D>;
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t full[L::SLOTS], empty[L::SLOTS], edge, q_full, q_empty, s_full[2], p_full[2], o_full[2], drained;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t* sq = sm;
+    uint8_t* ring = sm + 2 * L::QB;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    volatile int* abort = &s_abort;
+
+    if (tid == 0) {
+        for (int i = 0; i < L::SLOTS; ++i) { tc::mbar_init(&full[i], 1); tc::mbar_init(&empty[i], 1); }
+        tc::mbar_init(&edge, 1);
+        tc::mbar_init(&q_full, 1);
+        tc::mbar_init(&q_empty, 1);
+        for (int i = 0; i < 2; ++i) { tc::mbar_init(&s_full[i], 1); tc::mbar_init(&p_full[i], 128); tc::mbar_init(&o_full[i], 1); }
+        tc::mbar_init(&drained, 1);
+        tc::mbar_fence_init();
+        s_abort = 0;
+    }
+    if (warp == 9) {
+        tc::tmem_alloc(&s_tmem, 512);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tm = s_tmem;
+    const uint32_t limit = p.wait_limit;
+    // The launch has 168 registers for each of the 384 threads (64512); a softmax thread
+    // holds a whole row: 2 x 128 x 224 + 128 x 56 = 64512.
+    if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+
+    if (warp == 8) {
+        // ---------------- loads: Q of a unit, then K and V tiles through the ring ----------------
+        uint32_t it = 0, edges = 0, nu = 0;
+        bool ok = true;
+        for (long u = blockIdx.x; u < p.units && ok; u += gridDim.x, ++nu) {
+            const Unit x = unit_at(p, u);
+            for (int i = 0; i < x.ntiles && ok; ++i) {
+                int j0, width;
+                x.tile(i, &j0, &width);
+                const int seen = x.seen(i);
+                if (i == 0) {
+                    if (nu > 0) ok = wait_warp(&q_empty, (nu - 1) & 1, limit, abort);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        tc::mbar_arrive_expect_tx(&q_full, 2 * L::QB);
+                        for (int t = 0; t < 2; ++t)
+                            for (int s = 0; s < D / 64; ++s)
+                                tc::tma_load_3d(sq + t * L::QB + s * 16384, &mq, s * 64, x.h0, x.q0 + t * p.qpt, &q_full);
+                    }
+                }
+                for (int kv = 0; kv < 2; ++kv, ++it) {
+                    const int slot = it % L::SLOTS;
+                    if (it >= L::SLOTS) ok = wait_warp(&empty[slot], (it / L::SLOTS - 1) & 1, limit, abort);
+                    if (!ok) break;
+                    uint8_t* dst = ring + slot * L::SB;
+                    const bool zero = kv == 1 && seen < width;    // V rows that nothing sees are multiplied by 0
+                    uint64_t* bar = zero ? &edge : &full[slot];
+                    if (lane == 0) {
+                        tc::mbar_arrive_expect_tx(bar, L::SB);
+                        for (int s = 0; s < D / 64; ++s)
+                            tc::tma_load_3d(dst + s * 16384, kv ? &mv : &mk, s * 64, x.hk, x.k0 + j0, bar);
+                    }
+                    if (zero) {
+                        ok = wait_warp(&edge, edges & 1, limit, abort);
+                        ++edges;
+                        if (!ok) break;
+                        // 16-byte pieces of rows [seen, width); the swizzle permutes pieces within a row only
+                        for (int e = lane; e < (width - seen) * (D / 8); e += 32) {
+                            const int r = seen + e / (D / 8), c = e % (D / 8);
+                            *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                        tc::fence_proxy_async();
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(&full[slot]);
+                    }
+                }
+            }
+        }
+        if (!ok && lane == 0) {
+            // give up: the copies issued so far land before the CTA leaves
+            bool d = tc::drain_phase(&q_full, nu) && tc::drain_phase(&edge, edges);
+            for (uint32_t s = 0; s < (uint32_t)L::SLOTS; ++s) {
+                const uint32_t n = it / L::SLOTS + (s < it % L::SLOTS ? 1 : 0);
+                d = tc::drain_phase(&full[s], n) && d;
+            }
+            // this unit's Q may have been issued as well: its phase follows the nu counted
+            tc::mbar_wait_bounded(&q_full, nu & 1, 1u << 16);
+            atomicOr(&g_window_error, d ? tc::ERR_WAIT : tc::ERR_WAIT | tc::ERR_DRAIN);
+        }
+    } else if (warp == 9) {
+        // ---------------- MMAs (one thread issues; the warp stays together for unit_at) ----------------
+        uint32_t it = 0, nu = 0, np = 0;       // ring position, units, softmax steps of each tile
+        bool ok = true;
+        const uint32_t sqa = tc::smem_u32(sq), ra = tc::smem_u32(ring);
+        auto qk = [&](int t, uint32_t slot, int width) {
+            const uint32_t id = tc::idesc_bf16(128, width, false, false, p.neg != 0);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
+                tc::mma_f16_ss(tm + t * 128, tc::sw128_desc(sqa + t * L::QB + off), tc::sw128_desc(ra + slot * L::SB + off),
+                               id, k > 0);
+            }
+        };
+        auto pv = [&](int t, uint32_t slot, int width, bool first) {
+            const uint32_t id = tc::idesc_bf16(128, D, false, true);
+            for (int k = 0; k < width / 16; ++k)
+                tc::mma_f16_ts(tm + 256 + t * D, tm + t * 128 + k * 8, tc::sw128_desc_mn(ra + slot * L::SB + k * 2048, 16384),
+                               id, !(first && k == 0));
+        };
+        for (long u = blockIdx.x; u < p.units && ok; u += gridDim.x, ++nu) {
+            const Unit x = unit_at(p, u);
+            int j0, width;
+            x.tile(0, &j0, &width);
+            ok = wait_warp(&q_full, nu & 1, limit, abort) &&
+                 wait_warp(&full[it % L::SLOTS], (it / L::SLOTS) & 1, limit, abort);
+            if (!ok) break;
+            tc::fence_after_sync();
+            if (lane == 0) {
+                for (int t = 0; t < 2; ++t) {
+                    qk(t, it % L::SLOTS, width);
+                    tc::mma_commit(&s_full[t]);
+                }
+                tc::mma_commit(&empty[it % L::SLOTS]);
+                if (x.ntiles == 1) tc::mma_commit(&q_empty);
+            }
+            ++it;
+            for (int i = 0; i < x.ntiles && ok; ++i, ++np) {
+                const uint32_t vs = it % L::SLOTS, vp = (it / L::SLOTS) & 1;
+                const uint32_t ks = (it + 1) % L::SLOTS, kp = ((it + 1) / L::SLOTS) & 1;
+                const bool more = i + 1 < x.ntiles;
+                int nwidth = 0;
+                if (more) x.tile(i + 1, &j0, &nwidth);
+                ok = wait_warp(&full[vs], vp, limit, abort) && (!more || wait_warp(&full[ks], kp, limit, abort));
+                for (int t = 0; t < 2 && ok; ++t) {
+                    ok = wait_warp(&p_full[t], np & 1, limit, abort);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    if (lane == 0) {
+                        pv(t, vs, width, i == 0);
+                        if (more) {
+                            qk(t, ks, nwidth);
+                            tc::mma_commit(&s_full[t]);
+                        } else {
+                            tc::mma_commit(&o_full[t]);
+                        }
+                    }
+                }
+                if (!ok) break;
+                if (lane == 0) {
+                    tc::mma_commit(&empty[vs]);
+                    if (more) tc::mma_commit(&empty[ks]);
+                    if (i + 2 == x.ntiles) tc::mma_commit(&q_empty);
+                }
+                it += more ? 2 : 1;
+                width = nwidth;
+            }
+        }
+        // everything issued has finished before TMEM and shared memory are given back
+        if (lane == 0) {
+            tc::mma_commit(&drained);
+            const bool d = tc::mbar_wait_bounded(&drained, 0, tc::WAIT_POLLS);
+            if (!ok || !d) atomicOr(&g_window_error, d ? tc::ERR_WAIT : tc::ERR_WAIT | tc::ERR_DRAIN);
+        }
+        __syncwarp();
+    } else if (warp < 8) {
+        // ---------------- softmax of tile t, one row per thread ----------------
+        const int t = warp >> 2, r = tid & 127;
+        const uint32_t ts = tm + t * 128 + ((uint32_t)(warp & 3) << 21);        // this warp's 32 lanes of S (and P)
+        const uint32_t to = tm + 256 + t * D + ((uint32_t)(warp & 3) << 21);
+        uint32_t np = 0, nu = 0;
+        bool ok = true;
+        for (long u = blockIdx.x; u < p.units && ok; u += gridDim.x, ++nu) {
+            const Unit x = unit_at(p, u);
+            const int qi = t * p.qpt + r / p.gp;                  // query of this row, counted from q0
+            const int pos = x.p0 + qi;
+            float ref = -INFINITY, l = 0.f;                       // reference (scaled) and sum
+            // the tile's rows see everything between these positions without a mask
+            const int pmin = x.p0 + t * p.qpt, pmax = min(x.hi, pmin + p.qpt - 1);
+            for (int i = 0; i < x.ntiles; ++i, ++np) {
+                int j0, width;
+                x.tile(i, &j0, &width);
+                ok = wait_warp(&s_full[t], np & 1, limit, abort);
+                if (!ok) break;
+                tc::fence_after_sync();
+                float s[KT];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (k * 32 < width) tc::tmem_ld32(ts + k * 32, s + k * 32);
+                tc::tmem_ld_wait();
+                const bool window = i < x.nwin;
+                const bool whole = window && j0 + width - 1 <= pmin && j0 > pmax - p.a.window;
+                if (!whole) {
+                    // columns [a, b] of the window and columns below z of the sinks
+                    const int b = window ? pos - j0 : -1, a = window ? max(0, pos - p.a.window + 1 - j0) : 0;
+                    const int z = window ? min(p.a.sinks - j0, b + 1) : x.nsink - j0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (k * 32 < width) {
+                            // bit c: column 32 k + c is seen
+                            const int hi = min(31, b - 32 * k), lo = max(0, a - 32 * k), zz = min(32, z - 32 * k);
+                            uint32_t seen = hi >= lo && lo < 32 ? (0xffffffffu >> (31 - hi)) & (0xffffffffu << lo) : 0u;
+                            if (zz > 0) seen |= 0xffffffffu >> (32 - zz);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) s[32 * k + c] = (seen >> c) & 1u ? s[32 * k + c] : -INFINITY;
+                        }
+                    }
+                }
+                float m = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (k * 32 < width) {
+                        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) m4[c & 3] = fmaxf(m4[c & 3], s[32 * k + c]);
+                        m = fmaxf(m, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
+                    }
+                }
+                m *= p.c;
+                // Rescale where the maximum outgrew the reference by 2^8 (always from no reference).
+                const bool grow = m > ref + 8.f;
+                if (__any_sync(~0u, grow)) {
+                    const float nref = grow ? m : ref;
+                    const float f = ref == -INFINITY ? 0.f : exp2f(ref - nref);
+                    l *= f;
+                    ref = nref;
+                    if (i > 0) {
+#pragma unroll
+                        for (int k = 0; k < D / 32; ++k) {
+                            float o[32];
+                            tc::tmem_ld32(to + k * 32, o);
+                            tc::tmem_ld_wait();
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) o[c] *= f;
+                            tc::tmem_st32(to + k * 32, reinterpret_cast<const uint32_t*>(o));
+                        }
+                    }
+                }
+                const float base = ref == -INFINITY ? 0.f : -ref;   // nothing seen yet: every weight is exp2(-inf) = 0
+                float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (k * 32 < width) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int c = 0; c < 32; c += 2) {
+                            const float e0 = exp2f(fmaf(s[32 * k + c], p.c, base)), e1 = exp2f(fmaf(s[32 * k + c + 1], p.c, base));
+                            l4[c & 2] += e0;
+                            l4[(c & 2) + 1] += e1;
+                            // weights rounded to bf16 for the product; l keeps float32
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(e0, e1);
+                            w[c >> 1] = *reinterpret_cast<const uint32_t*>(&h);
+                        }
+                        tc::tmem_st16u(ts + k * 16, w);
+                    }
+                }
+                l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                tc::tmem_st_wait();
+                tc::fence_before_sync();
+                tc::mbar_arrive(&p_full[t]);
+            }
+            if (!ok) break;
+            ok = wait_warp(&o_full[t], nu & 1, limit, abort);
+            if (!ok) break;
+            tc::fence_after_sync();
+            const float inv = 1.0f / l;
+            const int q = x.q0 + qi;
+            const bool live = q < x.q1;
+            const size_t row = (size_t)q * p.a.Hq + x.h0 + r % p.gp;
+            uint16_t* out = reinterpret_cast<uint16_t*>(p.a.o) + row * D;
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+                float o[32];
+                tc::tmem_ld32(to + k * 32, o);
+                tc::tmem_ld_wait();
+                if (live) {
+#pragma unroll
+                    for (int c = 0; c < 32; c += 16) {            // 32 bytes, a whole sector, per store where o allows it
+                        float v[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(o[c + 2 * e] * inv, o[c + 2 * e + 1] * inv);
+                            v[e] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&h));
+                        }
+                        if (p.wide) {
+                            st_stream_f8(reinterpret_cast<float*>(out + k * 32 + c), v);
+                        } else {
+                            st_stream_f4(reinterpret_cast<float*>(out + k * 32 + c), make_float4(v[0], v[1], v[2], v[3]));
+                            st_stream_f4(reinterpret_cast<float*>(out + k * 32 + c + 8), make_float4(v[4], v[5], v[6], v[7]));
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+            if (live && p.a.lse) p.a.lse[row] = 0.6931471805599453f * ref + logf(l);
+            tc::fence_before_sync();       // O has been read before the next unit's first product (p_full orders it)
+        }
+    }
+    __syncthreads();
+    if (warp == 9) tc::tmem_dealloc(tm, 512);
+}
+
+template <int D>
+static cudaError_t prefill_d(const kda_window_prefill_args& a, cudaStream_t s) {
+    PfParams p;
+    p.a = a;
+    const int G = a.Hq / a.Hkv;
+    p.gp = G & -G;
+    if (p.gp > 16) p.gp = 16;
+    p.subs = G / p.gp;
+    p.qpt = 128 / p.gp;
+    long blocks = 0;
+    for (int n = 0; n < a.num_seqs; ++n)
+        blocks += (a.cu_seqlens_host[n + 1] - a.cu_seqlens_host[n] + 2 * p.qpt - 1) / (2 * p.qpt);
+    p.units = blocks * a.Hkv * p.subs;
+    if (p.units == 0) return cudaSuccess;
+    // a zero scale keeps exp2(fma(-inf, c, ...)) at 0 for masked scores
+    p.c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-37f);
+    p.neg = a.scale < 0.f;
+    p.wide = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
+    p.wait_limit = wait_limit();
+    CUtensorMap mq, mk, mv;
+    cudaError_t e = make_map_heads(&mq, a.q, D, a.Hq, a.T_total, a.q_stride, p.gp, p.qpt);
+    if (e == cudaSuccess) e = make_map_heads(&mk, a.k, D, a.Hkv, a.Tk_total, a.k_stride, 1, KT);
+    if (e == cudaSuccess) e = make_map_heads(&mv, a.v, D, a.Hkv, a.Tk_total, a.v_stride, 1, KT);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(window_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, PF<D>::SMEM);
+    int dev = 0, sms = 0;
+    if (e == cudaSuccess) e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const long grid = p.units < sms ? p.units : sms;
+    window_prefill_kernel<D><<<(unsigned)grid, PF_THREADS, PF<D>::SMEM, s>>>(p, mq, mk, mv);
     count_launches(1);
     return cudaGetLastError();
 }
+
+cudaError_t launch_prefill(const kda_window_prefill_args& a, cudaStream_t s) {
+    return a.d == 64 ? prefill_d<64>(a, s) : prefill_d<128>(a, s);
+}
+
+cudaError_t error_word(void** out) { return cudaGetSymbolAddress(out, g_window_error); }
 
 }  // namespace win
 }  // namespace kda
