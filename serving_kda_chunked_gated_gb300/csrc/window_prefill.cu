@@ -12,10 +12,12 @@
 // A new maximum rescales O only when it exceeds the reference by more than 2^8 (the
 // weights then stay below 2^8, which costs bf16 and fp32 nothing): O is rarely touched.
 //
-// Roles of the 12 warps: 0-3 the softmax of tile A, 4-7 that of tile B (one thread per
-// row), 8 the TMA loads, 9 the MMAs, 10 and 11 only fill the third warpgroup.  While one tile is in its softmax the tensor core
-// works on the other.  CTAs are persistent: the loads and the first S of the next unit
-// run while the softmax warps write this unit's rows.
+// Roles of the 16 warps: 0-3 the softmax of tile A, 4-7 that of tile B (one thread per
+// row), 8-11 the output rows of both, 12 the TMA loads, 13 the MMAs (14 and 15 only fill
+// their warpgroup).  While one tile is in its softmax the tensor core works on the other;
+// the first half of a tile's P V runs while the second half of its P is being made.  CTAs
+// are persistent: the loads and the first S of the next unit run while this unit's rows
+// are written.
 //
 // V is the B operand straight from the TMA tile (MN-major), Q and K are K-major; no
 // thread touches an operand but for zeroing the unseen rows of edge tiles (0 x NaN).
@@ -28,14 +30,19 @@
 namespace kda {
 namespace win {
 
-constexpr int PF_THREADS = 384;
+constexpr int PF_THREADS = 512;
 constexpr int KT = 128;                     // keys per tile
+// The tiles stream through a ring of slots in the order K0, V0 K1, V1 K2, ..., over all
+// units of a CTA.  Round 0 consumes K0 (the first S), round r >= 1 the values V of the
+// r-th softmax step and the keys K of the next one: one full and one empty barrier per
+// round, ROUNDS of them in turn (more rounds than the ring holds).
+constexpr int ROUNDS = 8;
 
 template <int D>
 struct PF {
     static constexpr int QB = 128 * D * 2;          // bytes of one Q tile
     static constexpr int SB = KT * D * 2;           // bytes of one K or V tile (ring slot)
-    static constexpr int SLOTS = D == 128 ? 5 : 10;
+    static constexpr int SLOTS = D == 128 ? 5 : 9;
     static constexpr int SMEM = 2 * QB + SLOTS * SB + 1024;   // + alignment slack
 };
 
@@ -126,13 +133,32 @@ KDA_DEV bool wait_warp(uint64_t* bar, uint32_t parity, uint32_t limit, volatile 
     return __all_sync(~0u, tc::mbar_wait_role(bar, parity, limit, abort));
 }
 
+// lane 0's value, which the compiler then knows to be the same in every lane
+KDA_DEV uint32_t uniform(uint32_t x) { return __shfl_sync(~0u, x, 0); }
+
+// two float32 operations in one instruction: d = x c + b, and l += e
+KDA_DEV void fma2(float& d0, float& d1, float x0, float x1, float c, float b) {
+    asm("{\n\t.reg .b64 x, c, b, d;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 c, {%4, %4};\n\tmov.b64 b, {%5, %5};\n\t"
+        "fma.rn.ftz.f32x2 d, x, c, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d0), "=f"(d1) : "f"(x0), "f"(x1), "f"(c), "f"(b));
+}
+KDA_DEV void add2(float& l0, float& l1, float e0, float e1) {
+    asm("{\n\t.reg .b64 l, e;\n\t"
+        "mov.b64 l, {%0, %1};\n\tmov.b64 e, {%2, %3};\n\t"
+        "add.rn.ftz.f32x2 l, l, e;\n\tmov.b64 {%0, %1}, l;\n\t}"
+        : "+f"(l0), "+f"(l1) : "f"(e0), "f"(e1));
+}
+
 template <int D>
 __global__ void __launch_bounds__(PF_THREADS, 1)
 window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant__ CUtensorMap mq,
                       const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
     using L = PF<D>;
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t full[L::SLOTS], empty[L::SLOTS], edge, q_full, q_empty, s_full[2], p_full[2], o_full[2], drained;
+    __shared__ __align__(8) uint64_t full[ROUNDS], empty[ROUNDS], edge, q_full, q_empty, s_full[2], p_full[2][2], o_full[2],
+        l_full[2], o_empty[2], drained;
+    __shared__ float s_l[2][128];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
@@ -142,16 +168,23 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
     volatile int* abort = &s_abort;
 
     if (tid == 0) {
-        for (int i = 0; i < L::SLOTS; ++i) { tc::mbar_init(&full[i], 1); tc::mbar_init(&empty[i], 1); }
+        for (int i = 0; i < ROUNDS; ++i) { tc::mbar_init(&full[i], 2); tc::mbar_init(&empty[i], 1); }
         tc::mbar_init(&edge, 1);
         tc::mbar_init(&q_full, 1);
         tc::mbar_init(&q_empty, 1);
-        for (int i = 0; i < 2; ++i) { tc::mbar_init(&s_full[i], 1); tc::mbar_init(&p_full[i], 128); tc::mbar_init(&o_full[i], 1); }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&s_full[i], 1);
+            tc::mbar_init(&p_full[i][0], 128);
+            tc::mbar_init(&p_full[i][1], 128);
+            tc::mbar_init(&o_full[i], 1);
+            tc::mbar_init(&l_full[i], 128);
+            tc::mbar_init(&o_empty[i], 128);
+        }
         tc::mbar_init(&drained, 1);
         tc::mbar_fence_init();
         s_abort = 0;
     }
-    if (warp == 9) {
+    if (warp == 13) {
         tc::tmem_alloc(&s_tmem, 512);
         tc::tmem_relinquish();
     }
@@ -160,146 +193,228 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
     tc::fence_after_sync();
     const uint32_t tm = s_tmem;
     const uint32_t limit = p.wait_limit;
-    // The launch has 168 registers for each of the 384 threads (64512); a softmax thread
-    // holds a whole row: 2 x 128 x 224 + 128 x 56 = 64512.
-    if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-
-    if (warp == 8) {
-        // ---------------- loads: Q of a unit, then K and V tiles through the ring ----------------
-        uint32_t it = 0, edges = 0, nu = 0;
-        bool ok = true;
-        for (long u = blockIdx.x; u < p.units && ok; u += gridDim.x, ++nu) {
-            const Unit x = unit_at(p, u);
-            for (int i = 0; i < x.ntiles && ok; ++i) {
-                int j0, width;
-                x.tile(i, &j0, &width);
-                const int seen = x.seen(i);
-                if (i == 0) {
-                    if (nu > 0) ok = wait_warp(&q_empty, (nu - 1) & 1, limit, abort);
-                    if (!ok) break;
-                    if (lane == 0) {
-                        tc::mbar_arrive_expect_tx(&q_full, 2 * L::QB);
-                        for (int t = 0; t < 2; ++t)
-                            for (int s = 0; s < D / 64; ++s)
-                                tc::tma_load_3d(sq + t * L::QB + s * 16384, &mq, s * 64, x.h0, x.q0 + t * p.qpt, &q_full);
-                    }
-                }
-                for (int kv = 0; kv < 2; ++kv, ++it) {
-                    const int slot = it % L::SLOTS;
-                    if (it >= L::SLOTS) ok = wait_warp(&empty[slot], (it / L::SLOTS - 1) & 1, limit, abort);
-                    if (!ok) break;
-                    uint8_t* dst = ring + slot * L::SB;
-                    const bool zero = kv == 1 && seen < width;    // V rows that nothing sees are multiplied by 0
-                    uint64_t* bar = zero ? &edge : &full[slot];
-                    if (lane == 0) {
-                        tc::mbar_arrive_expect_tx(bar, L::SB);
-                        for (int s = 0; s < D / 64; ++s)
-                            tc::tma_load_3d(dst + s * 16384, kv ? &mv : &mk, s * 64, x.hk, x.k0 + j0, bar);
-                    }
-                    if (zero) {
-                        ok = wait_warp(&edge, edges & 1, limit, abort);
-                        ++edges;
+    // The launch has 128 registers for each of the 512 threads (65536); a softmax thread
+    // holds a whole row: 2 x 128 x 184 + 2 x 128 x 72 = 65536.
+    if (warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == 12) {
+            // ---------------- loads: Q of a unit, then K and V tiles through the ring ----------------
+            uint32_t it = 0, edges = 0, nu = 0, nq = 0;     // items, zeroed tiles, units, Q loads so far
+            bool ok = true;
+            for (long u = blockIdx.x; u < p.units && ok; u += gridDim.x, ++nu) {
+                const Unit x = unit_at(p, u);
+                for (int i = 0; i < x.ntiles && ok; ++i) {
+                    int j0, width;
+                    x.tile(i, &j0, &width);
+                    const int seen = x.seen(i);
+                    if (i == 0) {
+                        if (nu > 0) ok = wait_warp(&q_empty, (nu - 1) & 1, limit, abort);
                         if (!ok) break;
-                        // 16-byte pieces of rows [seen, width); the swizzle permutes pieces within a row only
-                        for (int e = lane; e < (width - seen) * (D / 8); e += 32) {
-                            const int r = seen + e / (D / 8), c = e % (D / 8);
-                            *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        if (lane == 0) {
+                            tc::mbar_arrive_expect_tx(&q_full, 2 * L::QB);
+                            for (int t = 0; t < 2; ++t)
+                                for (int s = 0; s < D / 64; ++s)
+                                    tc::tma_load_3d(sq + t * L::QB + s * 16384, &mq, s * 64, x.h0, x.q0 + t * p.qpt, &q_full);
                         }
-                        tc::fence_proxy_async();
-                        __syncwarp();
-                        if (lane == 0) tc::mbar_arrive(&full[slot]);
+                        ++nq;
+                    }
+                    for (int kv = 0; kv < 2; ++kv) {       // item `it`: even K, odd V, consumed in round ceil(it / 2)
+                        const int slot = it % L::SLOTS;
+                        if (it >= L::SLOTS) {
+                            const uint32_t r = (it - L::SLOTS + 1) >> 1;     // the round that frees the slot
+                            ok = wait_warp(&empty[r % ROUNDS], (r / ROUNDS) & 1, limit, abort);
+                        }
+                        if (!ok) break;
+                        uint8_t* dst = ring + slot * L::SB;
+                        uint64_t* round = &full[((it + 1) >> 1) % ROUNDS];
+                        const bool zero = kv == 1 && seen < width;    // V rows that nothing sees are multiplied by 0
+                        uint64_t* bar = zero ? &edge : round;
+                        if (lane == 0) {
+                            tc::mbar_arrive_expect_tx(bar, L::SB);
+                            if (it == 0) tc::mbar_arrive(bar);        // round 0 has no values
+                            for (int s = 0; s < D / 64; ++s)
+                                tc::tma_load_3d(dst + s * 16384, kv ? &mv : &mk, s * 64, x.hk, x.k0 + j0, bar);
+                        }
+                        ++it;
+                        if (zero) {
+                            ok = wait_warp(&edge, edges & 1, limit, abort);
+                            ++edges;
+                            if (!ok) break;
+                            // 16-byte pieces of rows [seen, width); the swizzle permutes pieces within a row only
+                            for (int e = lane; e < (width - seen) * (D / 8); e += 32) {
+                                const int r = seen + e / (D / 8), c = e % (D / 8);
+                                *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                            }
+                            tc::fence_proxy_async();
+                            __syncwarp();
+                            if (lane == 0) tc::mbar_arrive(round);
+                        }
                     }
                 }
             }
-        }
-        if (!ok && lane == 0) {
-            // give up: the copies issued so far land before the CTA leaves
-            bool d = tc::drain_phase(&q_full, nu) && tc::drain_phase(&edge, edges);
-            for (uint32_t s = 0; s < (uint32_t)L::SLOTS; ++s) {
-                const uint32_t n = it / L::SLOTS + (s < it % L::SLOTS ? 1 : 0);
-                d = tc::drain_phase(&full[s], n) && d;
-            }
-            // this unit's Q may have been issued as well: its phase follows the nu counted
-            tc::mbar_wait_bounded(&q_full, nu & 1, 1u << 16);
-            atomicOr(&g_window_error, d ? tc::ERR_WAIT : tc::ERR_WAIT | tc::ERR_DRAIN);
-        }
-    } else if (warp == 9) {
-        // ---------------- MMAs (one thread issues; the warp stays together for unit_at) ----------------
-        uint32_t it = 0, nu = 0, np = 0;       // ring position, units, softmax steps of each tile
-        bool ok = true;
-        const uint32_t sqa = tc::smem_u32(sq), ra = tc::smem_u32(ring);
-        auto qk = [&](int t, uint32_t slot, int width) {
-            const uint32_t id = tc::idesc_bf16(128, width, false, false, p.neg != 0);
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
-                tc::mma_f16_ss(tm + t * 128, tc::sw128_desc(sqa + t * L::QB + off), tc::sw128_desc(ra + slot * L::SB + off),
-                               id, k > 0);
-            }
-        };
-        auto pv = [&](int t, uint32_t slot, int width, bool first) {
-            const uint32_t id = tc::idesc_bf16(128, D, false, true);
-            for (int k = 0; k < width / 16; ++k)
-                tc::mma_f16_ts(tm + 256 + t * D, tm + t * 128 + k * 8, tc::sw128_desc_mn(ra + slot * L::SB + k * 2048, 16384),
-                               id, !(first && k == 0));
-        };
-        for (long u = blockIdx.x; u < p.units && ok; u += gridDim.x, ++nu) {
-            const Unit x = unit_at(p, u);
-            int j0, width;
-            x.tile(0, &j0, &width);
-            ok = wait_warp(&q_full, nu & 1, limit, abort) &&
-                 wait_warp(&full[it % L::SLOTS], (it / L::SLOTS) & 1, limit, abort);
-            if (!ok) break;
-            tc::fence_after_sync();
-            if (lane == 0) {
-                for (int t = 0; t < 2; ++t) {
-                    qk(t, it % L::SLOTS, width);
-                    tc::mma_commit(&s_full[t]);
+            if (ok && it > 0 && lane == 0) tc::mbar_arrive(&full[(it >> 1) % ROUNDS]);   // the last round has no keys
+            if (!ok && lane == 0) {
+                // Give up.  The copies issued so far land before the CTA leaves: those of Q and of the
+                // zeroed tiles complete their phases; a round's phase may stay open for want of its
+                // other half, so its bytes are given the default bound of a wait, too.
+                bool d = tc::drain_phase(&q_full, nq) && tc::drain_phase(&edge, edges);
+                const uint32_t whole = (it + 1) >> 1;          // rounds 0 .. whole - 1 have both halves
+                for (uint32_t r = whole > ROUNDS ? whole - ROUNDS : 0; r < whole; ++r)
+                    d = tc::mbar_wait_bounded(&full[r % ROUNDS], (r / ROUNDS) & 1, tc::WAIT_POLLS) && d;
+                if (it > 0 && (it & 1) == 0) {                   // values without their keys: supply the arrival
+                    tc::mbar_arrive(&full[whole % ROUNDS]);
+                    d = tc::mbar_wait_bounded(&full[whole % ROUNDS], (whole / ROUNDS) & 1, tc::WAIT_POLLS) && d;
                 }
-                tc::mma_commit(&empty[it % L::SLOTS]);
-                if (x.ntiles == 1) tc::mma_commit(&q_empty);
+                atomicOr(&g_window_error, d ? tc::ERR_WAIT : tc::ERR_WAIT | tc::ERR_DRAIN);
             }
-            ++it;
-            for (int i = 0; i < x.ntiles && ok; ++i, ++np) {
-                const uint32_t vs = it % L::SLOTS, vp = (it / L::SLOTS) & 1;
-                const uint32_t ks = (it + 1) % L::SLOTS, kp = ((it + 1) / L::SLOTS) & 1;
-                const bool more = i + 1 < x.ntiles;
-                int nwidth = 0;
-                if (more) x.tile(i + 1, &j0, &nwidth);
-                ok = wait_warp(&full[vs], vp, limit, abort) && (!more || wait_warp(&full[ks], kp, limit, abort));
-                for (int t = 0; t < 2 && ok; ++t) {
-                    ok = wait_warp(&p_full[t], np & 1, limit, abort);
-                    if (!ok) break;
-                    tc::fence_after_sync();
-                    if (lane == 0) {
-                        pv(t, vs, width, i == 0);
+        } else if (warp == 13) {
+            // ---------------- MMAs: the warp computes together, one lane issues ----------------
+            uint32_t rd = 0, nu = 0, np = 0;       // rounds, units, softmax steps of each tile
+            bool ok = true;
+            const bool one = lane == 0;
+            const uint32_t sqa = uniform(tc::smem_u32(sq)), ra = uniform(tc::smem_u32(ring)), tmu = uniform(tm);
+            auto qk = [&](int t, uint32_t slot, int width) {
+                const uint32_t id = tc::idesc_bf16(128, width, false, false, p.neg != 0);
+                const uint64_t a = tc::sw128_desc(sqa + t * L::QB), b = tc::sw128_desc(ra + slot * L::SB);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;      // descriptors count 16 bytes
+                    tc::mma_f16_ss_if(one, tmu + t * 128, a + off, b + off, id, k > 0);
+                }
+            };
+            auto pv = [&](int t, uint32_t slot, int half, int width, bool first) {
+                const uint32_t id = tc::idesc_bf16(128, D, false, true);
+                const uint64_t b = tc::sw128_desc_mn(ra + slot * L::SB, 16384);
+#pragma unroll
+                for (int k = 4 * half; k < 4 * half + 4; ++k)
+                    if (k * 16 < width)
+                        tc::mma_f16_ts_if(one, tmu + 256 + t * D, tmu + t * 128 + k * 8, b + k * (2048 >> 4), id,
+                                          !(first && k == 0));
+            };
+            // widths of a unit's tiles, uniform over the warp
+            struct Tiles { int nwin, ntiles, wlast, slast; };
+            auto tiles_of = [&](long u) {
+                const Unit x = unit_at(p, u);
+                Tiles t;
+                int j0, w;
+                t.nwin = uniform(x.nwin);
+                t.ntiles = uniform(x.ntiles);
+                x.tile(x.nwin - 1, &j0, &w);
+                t.wlast = uniform(w);
+                x.tile(x.ntiles - 1, &j0, &w);
+                t.slast = uniform(w);
+                return t;
+            };
+            auto width_of = [&](const Tiles& t, int i) { return i == t.ntiles - 1 ? t.slast : i == t.nwin - 1 ? t.wlast : KT; };
+            Tiles x = {0, 0, 0, 0};
+            if ((long)blockIdx.x < p.units) {
+                x = tiles_of(blockIdx.x);
+                ok = wait_warp(&q_full, 0, limit, abort) && wait_warp(&full[0], 0, limit, abort);
+                tc::fence_after_sync();
+                if (ok) {
+                    for (int t = 0; t < 2; ++t) {
+                        qk(t, 0, width_of(x, 0));
+                        tc::mma_commit_if(one, &s_full[t]);
+                    }
+                    tc::mma_commit_if(one, &empty[0]);
+                    if (x.ntiles == 1) tc::mma_commit_if(one, &q_empty);
+                }
+                rd = 1;
+            }
+            for (long u = blockIdx.x; u < p.units && ok; u += gridDim.x, ++nu) {
+                const bool next_unit = u + gridDim.x < p.units;
+                Tiles y = x;
+                if (next_unit) y = tiles_of(u + gridDim.x);
+                for (int i = 0; i < x.ntiles && ok; ++i, ++np, ++rd) {
+                    const bool last = i + 1 == x.ntiles, more = !last || next_unit;
+                    const uint32_t vs = (2 * rd - 1) % L::SLOTS, ks = (2 * rd) % L::SLOTS;
+                    const int width = width_of(x, i), nwidth = last ? width_of(y, 0) : width_of(x, i + 1);
+                    ok = wait_warp(&full[rd % ROUNDS], (rd / ROUNDS) & 1, limit, abort);
+                    for (int t = 0; t < 2 && ok; ++t) {
+                        if (i == 0 && nu > 0) ok = wait_warp(&o_empty[t], (nu - 1) & 1, limit, abort);
+                        ok = ok && wait_warp(&p_full[t][0], np & 1, limit, abort);
+                        if (!ok) break;
+                        tc::fence_after_sync();
+                        pv(t, vs, 0, width, i == 0);
+                        ok = wait_warp(&p_full[t][1], np & 1, limit, abort);
+                        if (!ok) break;
+                        tc::fence_after_sync();
+                        pv(t, vs, 1, width, i == 0);
+                        if (last) {
+                            tc::mma_commit_if(one, &o_full[t]);
+                            if (more && t == 0) ok = wait_warp(&q_full, (nu + 1) & 1, limit, abort);
+                            if (!ok) break;
+                        }
                         if (more) {
                             qk(t, ks, nwidth);
-                            tc::mma_commit(&s_full[t]);
-                        } else {
-                            tc::mma_commit(&o_full[t]);
+                            tc::mma_commit_if(one, &s_full[t]);
                         }
                     }
+                    if (!ok) break;
+                    tc::mma_commit_if(one, &empty[rd % ROUNDS]);
+                    // the S issued in this round was a unit's last: its Q may be overwritten
+                    if (last ? more && y.ntiles == 1 : i + 2 == x.ntiles) tc::mma_commit_if(one, &q_empty);
                 }
+                x = y;
+            }
+            // everything issued has finished before TMEM and shared memory are given back
+            if (lane == 0) {
+                tc::mma_commit(&drained);
+                const bool d = tc::mbar_wait_bounded(&drained, 0, tc::WAIT_POLLS);
+                if (!ok || !d) atomicOr(&g_window_error, d ? tc::ERR_WAIT : tc::ERR_WAIT | tc::ERR_DRAIN);
+            }
+            __syncwarp();
+        }
+    } else if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        // ---------------- output rows: O / l, one row per thread ----------------
+        const int r = tid & 127;
+        uint32_t nu = 0;
+        bool ok = true;
+        for (long u = blockIdx.x; u < p.units && ok; u += gridDim.x, ++nu) {
+            const Unit x = unit_at(p, u);
+            for (int t = 0; t < 2; ++t) {
+                ok = wait_warp(&l_full[t], nu & 1, limit, abort) && wait_warp(&o_full[t], nu & 1, limit, abort);
                 if (!ok) break;
-                if (lane == 0) {
-                    tc::mma_commit(&empty[vs]);
-                    if (more) tc::mma_commit(&empty[ks]);
-                    if (i + 2 == x.ntiles) tc::mma_commit(&q_empty);
+                tc::fence_after_sync();
+                const uint32_t to = tm + 256 + t * D + ((uint32_t)(warp & 3) << 21);
+                const float inv = 1.0f / s_l[t][r];
+                const int q = x.q0 + t * p.qpt + r / p.gp;
+                const bool live = q < x.q1;
+                const size_t row = (size_t)q * p.a.Hq + x.h0 + r % p.gp;
+                uint16_t* out = reinterpret_cast<uint16_t*>(p.a.o) + row * D;
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k) {
+                    float o[32];
+                    tc::tmem_ld32(to + k * 32, o);
+                    tc::tmem_ld_wait();
+                    if (k == D / 32 - 1) {        // O and l have been read: the next unit may write them
+                        tc::fence_before_sync();
+                        tc::mbar_arrive(&o_empty[t]);
+                    }
+                    if (live) {
+#pragma unroll
+                        for (int c = 0; c < 32; c += 16) {            // 32 bytes, a whole sector, per store where o allows it
+                            float v[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const __nv_bfloat162 h = __floats2bfloat162_rn(o[c + 2 * e] * inv, o[c + 2 * e + 1] * inv);
+                                v[e] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&h));
+                            }
+                            if (p.wide) {
+                                st_stream_f8(reinterpret_cast<float*>(out + k * 32 + c), v);
+                            } else {
+                                st_stream_f4(reinterpret_cast<float*>(out + k * 32 + c), make_float4(v[0], v[1], v[2], v[3]));
+                                st_stream_f4(reinterpret_cast<float*>(out + k * 32 + c + 8), make_float4(v[4], v[5], v[6], v[7]));
+                            }
+                        }
+                    }
+                    __syncwarp();
                 }
-                it += more ? 2 : 1;
-                width = nwidth;
             }
         }
-        // everything issued has finished before TMEM and shared memory are given back
-        if (lane == 0) {
-            tc::mma_commit(&drained);
-            const bool d = tc::mbar_wait_bounded(&drained, 0, tc::WAIT_POLLS);
-            if (!ok || !d) atomicOr(&g_window_error, d ? tc::ERR_WAIT : tc::ERR_WAIT | tc::ERR_DRAIN);
-        }
-        __syncwarp();
-    } else if (warp < 8) {
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         // ---------------- softmax of tile t, one row per thread ----------------
         const int t = warp >> 2, r = tid & 127;
         const uint32_t ts = tm + t * 128 + ((uint32_t)(warp & 3) << 21);        // this warp's 32 lanes of S (and P)
@@ -308,9 +423,8 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
         bool ok = true;
         for (long u = blockIdx.x; u < p.units && ok; u += gridDim.x, ++nu) {
             const Unit x = unit_at(p, u);
-            const int qi = t * p.qpt + r / p.gp;                  // query of this row, counted from q0
-            const int pos = x.p0 + qi;
-            float ref = -INFINITY, l = 0.f;                       // reference (scaled) and sum
+            const int pos = x.p0 + t * p.qpt + r / p.gp;          // position of this row's query
+            float ref = -INFINITY, l0 = 0.f, l1 = 0.f;            // reference (scaled), sum in two parts
             // the tile's rows see everything between these positions without a mask
             const int pmin = x.p0 + t * p.qpt, pmax = min(x.hi, pmin + p.qpt - 1);
             for (int i = 0; i < x.ntiles; ++i, ++np) {
@@ -320,36 +434,42 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
                 if (!ok) break;
                 tc::fence_after_sync();
                 float s[KT];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (k * 32 < width) tc::tmem_ld32(ts + k * 32, s + k * 32);
-                tc::tmem_ld_wait();
                 const bool window = i < x.nwin;
                 const bool whole = window && j0 + width - 1 <= pmin && j0 > pmax - p.a.window;
-                if (!whole) {
-                    // columns [a, b] of the window and columns below z of the sinks
-                    const int b = window ? pos - j0 : -1, a = window ? max(0, pos - p.a.window + 1 - j0) : 0;
-                    const int z = window ? min(p.a.sinks - j0, b + 1) : x.nsink - j0;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if (k * 32 < width) {
-                            // bit c: column 32 k + c is seen
-                            const int hi = min(31, b - 32 * k), lo = max(0, a - 32 * k), zz = min(32, z - 32 * k);
-                            uint32_t seen = hi >= lo && lo < 32 ? (0xffffffffu >> (31 - hi)) & (0xffffffffu << lo) : 0u;
-                            if (zz > 0) seen |= 0xffffffffu >> (32 - zz);
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) s[32 * k + c] = (seen >> c) & 1u ? s[32 * k + c] : -INFINITY;
-                        }
-                    }
-                }
+                // columns [a, b] of the window and columns below z of the sinks are seen
+                const int b = window ? pos - j0 : -1, a = window ? max(0, pos - p.a.window + 1 - j0) : 0;
+                const int z = window ? min(p.a.sinks - j0, b + 1) : x.nsink - j0;
                 float m = -INFINITY;
+                tc::tmem_ld32(ts, s);
+                if (32 < width) tc::tmem_ld32(ts + 32, s + 32);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     if (k * 32 < width) {
-                        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        if (k == 0 || k == 2) {            // columns 64 .. 127 arrive while 0 .. 63 are searched
+                            tc::tmem_ld_wait();
+                            if (k == 0 && 64 < width) {
+                                tc::tmem_ld32(ts + 64, s + 64);
+                                if (96 < width) tc::tmem_ld32(ts + 96, s + 96);
+                            }
+                        }
+                        if (!whole) {
+                            // bit c: column 32 k + c is seen.  A warp's rows are few queries, so most
+                            // chunks of an edge tile are seen by all of them or by none.
+                            const int hi = min(31, b - 32 * k), lo = max(0, a - 32 * k), zz = min(32, z - 32 * k);
+                            uint32_t seen = hi >= lo && lo < 32 ? (0xffffffffu >> (31 - hi)) & (0xffffffffu << lo) : 0u;
+                            if (zz > 0) seen |= 0xffffffffu >> (32 - zz);
+                            if (!__all_sync(~0u, seen == 0xffffffffu)) {
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) m4[c & 3] = fmaxf(m4[c & 3], s[32 * k + c]);
-                        m = fmaxf(m, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
+                                for (int c = 0; c < 32; ++c) s[32 * k + c] = (seen >> c) & 1u ? s[32 * k + c] : -INFINITY;
+                            }
+                        }
+                        float m0 = s[32 * k], m1 = s[32 * k + 1];
+#pragma unroll
+                        for (int c = 2; c < 32; c += 4) {
+                            m0 = fmaxf(fmaxf(m0, s[32 * k + c]), s[32 * k + c + 1]);
+                            if (c + 3 < 32) m1 = fmaxf(fmaxf(m1, s[32 * k + c + 2]), s[32 * k + c + 3]);
+                        }
+                        m = fmaxf(fmaxf(m, m0), m1);
                     }
                 }
                 m *= p.c;
@@ -358,82 +478,59 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
                 if (__any_sync(~0u, grow)) {
                     const float nref = grow ? m : ref;
                     const float f = ref == -INFINITY ? 0.f : exp2f(ref - nref);
-                    l *= f;
+                    l0 *= f;
+                    l1 *= f;
                     ref = nref;
                     if (i > 0) {
 #pragma unroll
-                        for (int k = 0; k < D / 32; ++k) {
-                            float o[32];
-                            tc::tmem_ld32(to + k * 32, o);
+                        for (int k = 0; k < D / 16; ++k) {
+                            float o[16];
+                            tc::tmem_ld16(to + k * 16, o);
                             tc::tmem_ld_wait();
 #pragma unroll
-                            for (int c = 0; c < 32; ++c) o[c] *= f;
-                            tc::tmem_st32(to + k * 32, reinterpret_cast<const uint32_t*>(o));
+                            for (int c = 0; c < 16; ++c) o[c] *= f;
+                            tc::tmem_st16(to + k * 16, o);
                         }
                     }
                 }
                 const float base = ref == -INFINITY ? 0.f : -ref;   // nothing seen yet: every weight is exp2(-inf) = 0
-                float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     if (k * 32 < width) {
                         uint32_t w[16];
 #pragma unroll
                         for (int c = 0; c < 32; c += 2) {
-                            const float e0 = exp2f(fmaf(s[32 * k + c], p.c, base)), e1 = exp2f(fmaf(s[32 * k + c + 1], p.c, base));
-                            l4[c & 2] += e0;
-                            l4[(c & 2) + 1] += e1;
+                            float e0, e1;
+                            fma2(e0, e1, s[32 * k + c], s[32 * k + c + 1], p.c, base);
+                            e0 = exp2f(e0);
+                            e1 = exp2f(e1);
+                            add2(l0, l1, e0, e1);
                             // weights rounded to bf16 for the product; l keeps float32
                             const __nv_bfloat162 h = __floats2bfloat162_rn(e0, e1);
                             w[c >> 1] = *reinterpret_cast<const uint32_t*>(&h);
                         }
                         tc::tmem_st16u(ts + k * 16, w);
                     }
-                }
-                l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-                tc::tmem_st_wait();
-                tc::fence_before_sync();
-                tc::mbar_arrive(&p_full[t]);
-            }
-            if (!ok) break;
-            ok = wait_warp(&o_full[t], nu & 1, limit, abort);
-            if (!ok) break;
-            tc::fence_after_sync();
-            const float inv = 1.0f / l;
-            const int q = x.q0 + qi;
-            const bool live = q < x.q1;
-            const size_t row = (size_t)q * p.a.Hq + x.h0 + r % p.gp;
-            uint16_t* out = reinterpret_cast<uint16_t*>(p.a.o) + row * D;
-#pragma unroll
-            for (int k = 0; k < D / 32; ++k) {
-                float o[32];
-                tc::tmem_ld32(to + k * 32, o);
-                tc::tmem_ld_wait();
-                if (live) {
-#pragma unroll
-                    for (int c = 0; c < 32; c += 16) {            // 32 bytes, a whole sector, per store where o allows it
-                        float v[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const __nv_bfloat162 h = __floats2bfloat162_rn(o[c + 2 * e] * inv, o[c + 2 * e + 1] * inv);
-                            v[e] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&h));
-                        }
-                        if (p.wide) {
-                            st_stream_f8(reinterpret_cast<float*>(out + k * 32 + c), v);
-                        } else {
-                            st_stream_f4(reinterpret_cast<float*>(out + k * 32 + c), make_float4(v[0], v[1], v[2], v[3]));
-                            st_stream_f4(reinterpret_cast<float*>(out + k * 32 + c + 8), make_float4(v[4], v[5], v[6], v[7]));
-                        }
+                    if (k & 1) {
+                        tc::tmem_st_wait();
+                        tc::fence_before_sync();
+                        tc::mbar_arrive(&p_full[t][k >> 1]);
                     }
                 }
-                __syncwarp();
             }
-            if (live && p.a.lse) p.a.lse[row] = 0.6931471805599453f * ref + logf(l);
-            tc::fence_before_sync();       // O has been read before the next unit's first product (p_full orders it)
+            if (!ok) break;
+            if (nu > 0) ok = wait_warp(&o_empty[t], (nu - 1) & 1, limit, abort);   // the last unit's l has been read
+            if (!ok) break;
+            s_l[t][r] = l0 + l1;
+            tc::mbar_arrive(&l_full[t]);
+            const int q = x.q0 + t * p.qpt + r / p.gp;
+            if (p.a.lse && q < x.q1)
+                p.a.lse[(size_t)q * p.a.Hq + x.h0 + r % p.gp] = 0.6931471805599453f * ref + logf(l0 + l1);
+            __syncwarp();
         }
     }
     __syncthreads();
-    if (warp == 9) tc::tmem_dealloc(tm, 512);
+    if (warp == 13) tc::tmem_dealloc(tm, 512);
 }
 
 template <int D>
