@@ -13,8 +13,9 @@
 // weights then stay below 2^8, which costs bf16 and fp32 nothing): O is rarely touched.
 //
 // Roles of the 16 warps: 0-3 the softmax of tile A, 4-7 that of tile B (one thread per
-// row), 8-11 the output rows of both, 12 the TMA loads, 13 the MMAs (14 and 15 only fill
-// their warpgroup).  While one tile is in its softmax the tensor core works on the other;
+// row), 8-11 the output rows of both, 12 the TMA loads, 13 and 14 the MMAs of a tile each
+// (15 only fills its warpgroup).  While one tile is in its softmax the tensor core works on
+// the other, and one issuing warp's waits hide behind the other's MMAs;
 // the first half of a tile's P V runs while the second half of its P is being made.  CTAs
 // are persistent: the loads and the first S of the next unit run while this unit's rows
 // are written.
@@ -37,6 +38,9 @@ constexpr int KT = 128;                     // keys per tile
 // r-th softmax step and the keys K of the next one: one full and one empty barrier per
 // round, ROUNDS of them in turn (more rounds than the ring holds).
 constexpr int ROUNDS = 8;
+// Unit geometries ahead of their readers.  The loads of a unit wait for the last S of the
+// unit before, whose products waited for the output rows of the third before it: four do.
+constexpr int UNITS = 4;
 
 template <int D>
 struct PF {
@@ -128,8 +132,10 @@ KDA_DEV Unit unit_at(const PfParams& p, long u) {
     return x;
 }
 
-// A wait of a whole warp: every lane gets the same answer.
+// A wait of a whole warp: every lane gets the same answer.  The first poll stands apart:
+// most waits end with it (3 % on the whole kernel).
 KDA_DEV bool wait_warp(uint64_t* bar, uint32_t parity, uint32_t limit, volatile int* abort) {
+    if (limit && __all_sync(~0u, tc::mbar_try_wait(bar, parity))) return true;
     return __all_sync(~0u, tc::mbar_wait_role(bar, parity, limit, abort));
 }
 
@@ -157,7 +163,8 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
     using L = PF<D>;
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t full[ROUNDS], empty[ROUNDS], edge, q_full, q_empty, s_full[2], p_full[2][2], o_full[2],
-        l_full[2], o_empty[2], drained;
+        l_full[2], o_empty[2], u_full[UNITS], drained;
+    __shared__ Unit s_unit[UNITS];
     __shared__ float s_l[2][128];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
@@ -168,10 +175,11 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
     volatile int* abort = &s_abort;
 
     if (tid == 0) {
-        for (int i = 0; i < ROUNDS; ++i) { tc::mbar_init(&full[i], 2); tc::mbar_init(&empty[i], 1); }
+        for (int i = 0; i < ROUNDS; ++i) { tc::mbar_init(&full[i], 2); tc::mbar_init(&empty[i], 2); }
+        for (int i = 0; i < UNITS; ++i) tc::mbar_init(&u_full[i], 1);
         tc::mbar_init(&edge, 1);
         tc::mbar_init(&q_full, 1);
-        tc::mbar_init(&q_empty, 1);
+        tc::mbar_init(&q_empty, 2);
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&s_full[i], 1);
             tc::mbar_init(&p_full[i][0], 128);
@@ -180,7 +188,7 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
             tc::mbar_init(&l_full[i], 128);
             tc::mbar_init(&o_empty[i], 128);
         }
-        tc::mbar_init(&drained, 1);
+        tc::mbar_init(&drained, 2);
         tc::mbar_fence_init();
         s_abort = 0;
     }
@@ -211,6 +219,8 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
                         if (nu > 0) ok = wait_warp(&q_empty, (nu - 1) & 1, limit, abort);
                         if (!ok) break;
                         if (lane == 0) {
+                            s_unit[nu % UNITS] = x;
+                            tc::mbar_arrive(&u_full[nu % UNITS]);
                             tc::mbar_arrive_expect_tx(&q_full, 2 * L::QB);
                             for (int t = 0; t < 2; ++t)
                                 for (int s = 0; s < D / 64; ++s)
@@ -267,90 +277,95 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
                 }
                 atomicOr(&g_window_error, d ? tc::ERR_WAIT : tc::ERR_WAIT | tc::ERR_DRAIN);
             }
-        } else if (warp == 13) {
-            // ---------------- MMAs: the warp computes together, one lane issues ----------------
-            uint32_t rd = 0, nu = 0, np = 0;       // rounds, units, softmax steps of each tile
+        } else if (warp < 15) {
+            // ---------------- MMAs of tile t: the warp computes together, one lane issues ----------------
+            // The loops stay rolled: this code runs once per round between the softmax warps' long
+            // straight runs, and instructions that are fetched anew cost more than the loop.
+            const int t = warp - 13;
+            uint32_t rd = 0, nu = 0, np = 0;       // rounds, units, softmax steps
             bool ok = true;
             const bool one = lane == 0;
-            const uint32_t sqa = uniform(tc::smem_u32(sq)), ra = uniform(tc::smem_u32(ring)), tmu = uniform(tm);
-            auto qk = [&](int t, uint32_t slot, int width) {
+            const uint32_t ra = uniform(tc::smem_u32(ring)), tmu = uniform(tm);
+            const uint64_t qd = tc::sw128_desc(uniform(tc::smem_u32(sq)) + t * L::QB);
+            auto qk = [&](uint32_t slot, int width) {
                 const uint32_t id = tc::idesc_bf16(128, width, false, false, p.neg != 0);
-                const uint64_t a = tc::sw128_desc(sqa + t * L::QB), b = tc::sw128_desc(ra + slot * L::SB);
-#pragma unroll
+                const uint64_t kd = tc::sw128_desc(ra + slot * L::SB);
+#pragma unroll 1
                 for (int k = 0; k < D / 16; ++k) {
                     const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;      // descriptors count 16 bytes
-                    tc::mma_f16_ss_if(one, tmu + t * 128, a + off, b + off, id, k > 0);
+                    tc::mma_f16_ss_if(one, tmu + t * 128, qd + off, kd + off, id, k > 0);
                 }
             };
-            auto pv = [&](int t, uint32_t slot, int half, int width, bool first) {
+            auto pv = [&](uint32_t slot, int k0, int k1, bool first) {
                 const uint32_t id = tc::idesc_bf16(128, D, false, true);
-                const uint64_t b = tc::sw128_desc_mn(ra + slot * L::SB, 16384);
-#pragma unroll
-                for (int k = 4 * half; k < 4 * half + 4; ++k)
-                    if (k * 16 < width)
-                        tc::mma_f16_ts_if(one, tmu + 256 + t * D, tmu + t * 128 + k * 8, b + k * (2048 >> 4), id,
-                                          !(first && k == 0));
+                const uint64_t vd = tc::sw128_desc_mn(ra + slot * L::SB, 16384);
+#pragma unroll 1
+                for (int k = k0; k < k1; ++k)
+                    tc::mma_f16_ts_if(one, tmu + 256 + t * D, tmu + t * 128 + k * 8, vd + k * (2048 >> 4), id,
+                                      !(first && k == 0));
             };
             // widths of a unit's tiles, uniform over the warp
             struct Tiles { int nwin, ntiles, wlast, slast; };
-            auto tiles_of = [&](long u) {
-                const Unit x = unit_at(p, u);
-                Tiles t;
+            auto tiles_of = [&](uint32_t n) {
+                const Unit x = s_unit[n % UNITS];
+                Tiles r;
                 int j0, w;
-                t.nwin = uniform(x.nwin);
-                t.ntiles = uniform(x.ntiles);
+                r.nwin = uniform(x.nwin);
+                r.ntiles = uniform(x.ntiles);
                 x.tile(x.nwin - 1, &j0, &w);
-                t.wlast = uniform(w);
+                r.wlast = uniform(w);
                 x.tile(x.ntiles - 1, &j0, &w);
-                t.slast = uniform(w);
-                return t;
+                r.slast = uniform(w);
+                return r;
             };
-            auto width_of = [&](const Tiles& t, int i) { return i == t.ntiles - 1 ? t.slast : i == t.nwin - 1 ? t.wlast : KT; };
+            auto width_of = [&](const Tiles& r, int i) { return i == r.ntiles - 1 ? r.slast : i == r.nwin - 1 ? r.wlast : KT; };
             Tiles x = {0, 0, 0, 0};
+            uint32_t vs = L::SLOTS - 1, ks = 0;    // slots of this round's values and keys
             if ((long)blockIdx.x < p.units) {
-                x = tiles_of(blockIdx.x);
-                ok = wait_warp(&q_full, 0, limit, abort) && wait_warp(&full[0], 0, limit, abort);
+                ok = wait_warp(&u_full[0], 0, limit, abort) && wait_warp(&q_full, 0, limit, abort) &&
+                     wait_warp(&full[0], 0, limit, abort);
                 tc::fence_after_sync();
                 if (ok) {
-                    for (int t = 0; t < 2; ++t) {
-                        qk(t, 0, width_of(x, 0));
-                        tc::mma_commit_if(one, &s_full[t]);
-                    }
+                    x = tiles_of(0);
+                    qk(0, width_of(x, 0));
+                    tc::mma_commit_if(one, &s_full[t]);
                     tc::mma_commit_if(one, &empty[0]);
                     if (x.ntiles == 1) tc::mma_commit_if(one, &q_empty);
                 }
                 rd = 1;
             }
+#pragma unroll 1
             for (long u = blockIdx.x; u < p.units && ok; u += gridDim.x, ++nu) {
                 const bool next_unit = u + gridDim.x < p.units;
                 Tiles y = x;
-                if (next_unit) y = tiles_of(u + gridDim.x);
-                for (int i = 0; i < x.ntiles && ok; ++i, ++np, ++rd) {
+#pragma unroll 1
+                for (int i = 0; i < x.ntiles; ++i, ++np, ++rd) {
                     const bool last = i + 1 == x.ntiles, more = !last || next_unit;
-                    const uint32_t vs = (2 * rd - 1) % L::SLOTS, ks = (2 * rd) % L::SLOTS;
-                    const int width = width_of(x, i), nwidth = last ? width_of(y, 0) : width_of(x, i + 1);
+                    vs = vs + 2 >= L::SLOTS ? vs + 2 - L::SLOTS : vs + 2;
+                    ks = ks + 2 >= L::SLOTS ? ks + 2 - L::SLOTS : ks + 2;
+                    const int steps = width_of(x, i) / 16;
                     ok = wait_warp(&full[rd % ROUNDS], (rd / ROUNDS) & 1, limit, abort);
-                    for (int t = 0; t < 2 && ok; ++t) {
-                        if (i == 0 && nu > 0) ok = wait_warp(&o_empty[t], (nu - 1) & 1, limit, abort);
-                        ok = ok && wait_warp(&p_full[t][0], np & 1, limit, abort);
-                        if (!ok) break;
+                    if (ok && i == 0 && nu > 0) ok = wait_warp(&o_empty[t], (nu - 1) & 1, limit, abort);
+#pragma unroll 1
+                    for (int h = 0; h < 2 && ok; ++h) {
+                        ok = wait_warp(&p_full[t][h], np & 1, limit, abort);
                         tc::fence_after_sync();
-                        pv(t, vs, 0, width, i == 0);
-                        ok = wait_warp(&p_full[t][1], np & 1, limit, abort);
-                        if (!ok) break;
-                        tc::fence_after_sync();
-                        pv(t, vs, 1, width, i == 0);
-                        if (last) {
-                            tc::mma_commit_if(one, &o_full[t]);
-                            if (more && t == 0) ok = wait_warp(&q_full, (nu + 1) & 1, limit, abort);
-                            if (!ok) break;
-                        }
-                        if (more) {
-                            qk(t, ks, nwidth);
-                            tc::mma_commit_if(one, &s_full[t]);
-                        }
+                        if (ok) pv(vs, 4 * h, min(steps, 4 * h + 4), i == 0);
                     }
                     if (!ok) break;
+                    if (last) {
+                        tc::mma_commit_if(one, &o_full[t]);
+                        if (next_unit) {
+                            ok = wait_warp(&u_full[(nu + 1) % UNITS], ((nu + 1) / UNITS) & 1, limit, abort) &&
+                                 wait_warp(&q_full, (nu + 1) & 1, limit, abort);
+                            if (!ok) break;
+                            y = tiles_of(nu + 1);
+                        }
+                    }
+                    if (more) {
+                        qk(ks, last ? width_of(y, 0) : width_of(x, i + 1));
+                        tc::mma_commit_if(one, &s_full[t]);
+                    }
                     tc::mma_commit_if(one, &empty[rd % ROUNDS]);
                     // the S issued in this round was a unit's last: its Q may be overwritten
                     if (last ? more && y.ntiles == 1 : i + 2 == x.ntiles) tc::mma_commit_if(one, &q_empty);
@@ -358,7 +373,7 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
                 x = y;
             }
             // everything issued has finished before TMEM and shared memory are given back
-            if (lane == 0) {
+            if (one) {
                 tc::mma_commit(&drained);
                 const bool d = tc::mbar_wait_bounded(&drained, 0, tc::WAIT_POLLS);
                 if (!ok || !d) atomicOr(&g_window_error, d ? tc::ERR_WAIT : tc::ERR_WAIT | tc::ERR_DRAIN);
@@ -372,7 +387,9 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
         uint32_t nu = 0;
         bool ok = true;
         for (long u = blockIdx.x; u < p.units && ok; u += gridDim.x, ++nu) {
-            const Unit x = unit_at(p, u);
+            ok = wait_warp(&u_full[nu % UNITS], (nu / UNITS) & 1, limit, abort);
+            if (!ok) break;
+            const Unit x = s_unit[nu % UNITS];
             for (int t = 0; t < 2; ++t) {
                 ok = wait_warp(&l_full[t], nu & 1, limit, abort) && wait_warp(&o_full[t], nu & 1, limit, abort);
                 if (!ok) break;
@@ -422,7 +439,9 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
         uint32_t np = 0, nu = 0;
         bool ok = true;
         for (long u = blockIdx.x; u < p.units && ok; u += gridDim.x, ++nu) {
-            const Unit x = unit_at(p, u);
+            ok = wait_warp(&u_full[nu % UNITS], (nu / UNITS) & 1, limit, abort);
+            if (!ok) break;
+            const Unit x = s_unit[nu % UNITS];
             const int pos = x.p0 + t * p.qpt + r / p.gp;          // position of this row's query
             float ref = -INFINITY, l0 = 0.f, l1 = 0.f;            // reference (scaled), sum in two parts
             // the tile's rows see everything between these positions without a mask
