@@ -1,16 +1,788 @@
-// bf16 prefill of the scalar-gated delta rule: the per-token recurrence.
+// Chunked prefill of the gated delta rule with one decay per value head, bf16, on tcgen05.
+//
+// With g_i the log-decay summed over a chunk's tokens up to i, rk_i and rq_i the inverse
+// key and query norms (1 without qk_l2norm) and S the state before the chunk:
+//   A_ij  = beta_i rk_i rk_j e^{g_i - g_j} (k_i . k_j)        (j < i)
+//   T     = (I + A)^-1
+//   R_i   = beta_i (v_i - e^{g_i} rk_i (K S)_i)
+//   V'    = T R
+//   o_i   = scale rq_i (e^{g_i} (Q S)_i + sum_{j <= i} e^{g_i - g_j} rk_j (q_i . k_j) V'_j)
+//   S    <- e^{g_C} S + K^T V'',   V''_j = e^{g_C - g_j} rk_j V'_j
+// The decay is a scalar per token, so every factor sits outside the matrix products and K
+// and Q are MMA operands as they come from memory, bf16 without a rounding: only S, T, R
+// and V'' are float32, and each is fed as two bf16 parts (x = hi + lo, 2^-17 left), so
+// that states keep float32 accuracy.  Exponents are differences of exact sums (64-bit
+// fixed point): a decay of e^-600 over the chunk costs the short ones nothing.
+//
+// prep: one CTA per (chunk, key head) forms K K^T and Q K^T once for all value heads of
+// the key head, then per value head A, its inverse (16 x 16 blocks by substitution, merged
+// by [[X, 0], [B, Y]]^-1 = [[X^-1, 0], [-Y^-1 B X^-1, Y^-1]] on mma.sync with three tf32
+// products for each float32 one), and writes a record: T as two bf16 parts, the masked and
+// scaled Q K^T in bf16, the tokens' factors.
+// scan: one CTA per (sequence, value head, 32 value columns) walks the chunks.  Tokens (or
+// key channels) are TMEM lanes, the 32 columns of an operand's hi and lo parts one
+// 128-byte row of 64 MN-major elements: one N = 64 MMA forms both products.
+#include <math.h>
+
 #include "kda_common.cuh"
+#include "tcgen05.cuh"
+#include "tma_host.cuh"
 
 namespace kda {
 namespace gdn {
 
-cudaError_t launch_recurrent(const kda_gdn_prefill_args& a, cudaStream_t s);
+constexpr int C = 128;                        // chunk length
+constexpr int DH = 128;                       // key and value width
+constexpr int TILE = C * DH * 2;              // a K or Q tile: two slabs of 64 channels
 
-size_t chunked_workspace_size(const kda_gdn_prefill_args&) { return 256; }   // the error word
+// One record per (chunk, value head).  A 128 x 128 lower-triangular operand is stored as its
+// slab of columns 0 .. 63 and the lower half of its slab of columns 64 .. 127 (the upper
+// half is zero), rows of 128 bytes in the 128-byte swizzle.
+constexpr int TRI = 16384 + 8192;
+constexpr int REC_THI = 0, REC_TLO = TRI, REC_A = 2 * TRI, REC_F = 3 * TRI;
+constexpr int REC = 3 * TRI + C * 16 + 128;   // + four factors per token + e^{g_C}
+constexpr int WS_HEAD = 256;                  // the error word's line
+
+struct Params {
+    kda_gdn_prefill_args a;
+    long chunks;
+    uint32_t wait_limit;
+};
+
+// byte offset of 16-byte piece c (0 .. 7) of row r in a slab of 128-byte rows
+KDA_DEV uint32_t swz(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
+
+// Sequence and position of chunk `idx`, counted over the sequences; by whole warps.
+KDA_DEV void chunk_at(const kda_gdn_prefill_args& a, long idx, int* seq, int* chunk) {
+    const int lane = threadIdx.x & 31;
+    for (int base = 0; base < a.num_seqs; base += 32) {
+        const int m = base + lane;
+        const int len = m < a.num_seqs ? a.cu_seqlens[m + 1] - a.cu_seqlens[m] : 0;
+        int pre = (len + C - 1) / C;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(~0u, pre, o);
+            if (lane >= o) pre += x;
+        }
+        const unsigned hit = __ballot_sync(~0u, idx < pre);
+        if (hit) {
+            const int f = __ffs(hit) - 1;
+            const int before = __shfl_sync(~0u, pre, f > 0 ? f - 1 : 0);
+            *seq = base + f;
+            *chunk = (int)(idx - (f > 0 ? before : 0));
+            return;
+        }
+        idx -= __shfl_sync(~0u, pre, 31);
+    }
+    *seq = 0;
+    *chunk = 0;
+}
+
+// chunks of the sequences before n; by whole warps
+KDA_DEV long chunks_before(const kda_gdn_prefill_args& a, int n) {
+    long s = 0;
+    for (int m = threadIdx.x & 31; m < n; m += 32) s += (a.cu_seqlens[m + 1] - a.cu_seqlens[m] + C - 1) / C;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+    return s;
+}
+
+// x = hi + lo, both bf16: pairs packed with the lower index in the low half
+KDA_DEV void split2(float x0, float x1, uint32_t* hi, uint32_t* lo) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(&h);
+    const __nv_bfloat162 l =
+        __floats2bfloat162_rn(x0 - __uint_as_float(u << 16), x1 - __uint_as_float(u & 0xffff0000u));
+    *hi = u;
+    *lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+
+// ---------------------------------------------------------------------------
+// prep
+// ---------------------------------------------------------------------------
+constexpr int PT = 256;                       // threads
+constexpr int XS = 136;                       // row stride of the inverse's float matrix (8 banks apart)
+constexpr int YS = 72;
+constexpr int P_X = 0, P_Y = P_X + C * XS * 4, P_W = P_Y + 64 * YS * 4, P_END = P_W + 8 * C * 4;
+constexpr int P_SMEM = (P_END > 2 * TILE ? P_END : 2 * TILE) + 1024;
+
+// x = hi + lo with hi a tf32 value; what the tensor core drops of lo is below 2^-21 of x
+KDA_DEV void split_tf32(float x, float* hi, float* lo) {
+    *hi = __uint_as_float(__float_as_uint(x) & 0xffffe000u);
+    *lo = x - *hi;
+}
+
+// acc (16 x 16) += L[16 x 16 nk] R[16 nk x 16] from row-major float matrices in shared
+// memory: float32 operands as two tf32 parts each, the product of the low parts left out.
+// (Two bf16 parts would leave 2^-17, which the inverse of strongly correlated keys
+// amplifies to 2e-5 of the state.)  Within each step of 8, k is taken in the order 0, 2, 4,
+// 6, 1, 3, 5, 7, so that a lane's two values of A are neighbours.
+KDA_DEV void block_product(float (*acc)[4], const float* Lm, int ls, const float* Rm, int rs, int nk, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll 2
+    for (int k = 0; k < 2 * nk; ++k) {
+        float ah[4], al[4];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const float2 x = *reinterpret_cast<const float2*>(Lm + (g + q * 8) * ls + k * 8 + 2 * t);
+            split_tf32(x.x, &ah[q], &al[q]);
+            split_tf32(x.y, &ah[q + 2], &al[q + 2]);
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            float bh[2], bl[2];
+            const float* r = Rm + (k * 8 + 2 * t) * rs + n * 8 + g;
+            split_tf32(r[0], &bh[0], &bl[0]);
+            split_tf32(r[rs], &bh[1], &bl[1]);
+            tc::mma_m16n8k8_tf32(acc[n], ah, bh);
+            tc::mma_m16n8k8_tf32(acc[n], al, bh);
+            tc::mma_m16n8k8_tf32(acc[n], ah, bl);
+        }
+    }
+}
+KDA_DEV void block_store(const float (*acc)[4], float* M, int ms, float sign, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        *reinterpret_cast<float2*>(M + g * ms + n * 8 + 2 * t) = make_float2(sign * acc[n][0], sign * acc[n][1]);
+        *reinterpret_cast<float2*>(M + (g + 8) * ms + n * 8 + 2 * t) = make_float2(sign * acc[n][2], sign * acc[n][3]);
+    }
+}
+
+__global__ void __launch_bounds__(PT, 2)
+gdn_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk) {
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t loaded, done;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_ok;
+    __shared__ float s_rk[C], s_rq[C], s_beta[C];
+    __shared__ long long s_g[C], s_wsum[4];
+    const kda_gdn_prefill_args& a = p.a;
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int row = tid & 127, half = tid >> 7;             // TMEM lane and column half of this thread
+    const int hk = blockIdx.x % a.Hk;
+    const long idx = blockIdx.x / a.Hk;
+    int n, ch;
+    chunk_at(a, idx, &n, &ch);
+    const int t0 = a.cu_seqlens[n] + ch * C, len = min(C, a.cu_seqlens[n + 1] - t0);
+
+    if (tid == 0) {
+        tc::mbar_init(&loaded, 1);
+        tc::mbar_init(&done, 1);
+        tc::mbar_fence_init();
+        s_ok = 1;
+    }
+    if (warp == 0) {
+        tc::tmem_alloc(&s_tmem, 256);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tm = s_tmem;
+    if (tid == 0) {
+        tc::mbar_arrive_expect_tx(&loaded, 2 * TILE);
+        for (int s = 0; s < 2; ++s) {
+            tc::tma_load_3d(sm + s * 16384, &mk, s * 64, hk, t0, &loaded);
+            tc::tma_load_3d(sm + TILE + s * 16384, &mq, s * 64, hk, t0, &loaded);
+        }
+    }
+    bool ok = tc::mbar_wait_bounded(&loaded, 0, p.wait_limit);
+    if (!ok && tid == 0) {          // give up: the copies land before the CTA leaves
+        const bool d = tc::mbar_wait_bounded(&loaded, 0, tc::WAIT_POLLS);
+        atomicOr(reinterpret_cast<int*>(a.workspace), d ? tc::ERR_WAIT : tc::ERR_WAIT | tc::ERR_DRAIN);
+        s_ok = 0;
+    }
+    __syncthreads();
+    ok = s_ok;
+    if (ok) {
+        // rows behind the sequence belong to its neighbour: zero them
+        if (len < C) {
+            for (int e = tid; e < (C - len) * 32; e += PT) {
+                const int r = len + (e >> 5), q = e & 31;       // 16 pieces of K, 16 of Q
+                *reinterpret_cast<uint4*>(sm + (q >> 4) * TILE + ((q >> 3) & 1) * 16384 + r * 128 + (q & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            tc::fence_proxy_async();
+        }
+        __syncthreads();
+        if (tid == 0) {
+            const uint32_t kb = tc::smem_u32(sm), qb = kb + TILE, id = tc::idesc_bf16(128, 128);
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
+                tc::mma_f16_ss(tm, tc::sw128_desc(kb + off), tc::sw128_desc(kb + off), id, k > 0);
+                tc::mma_f16_ss(tm + 128, tc::sw128_desc(qb + off), tc::sw128_desc(kb + off), id, k > 0);
+            }
+            tc::mma_commit(&done);
+        }
+        {
+            // squares of this row: threads of half 0 the key's, of half 1 the query's
+            const uint8_t* base = sm + half * TILE;
+            float ss = 0.f;
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+                const uint4 u = *reinterpret_cast<const uint4*>(base + (c >> 3) * 16384 + swz(row, c & 7));
+                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float lo = __uint_as_float(w[i] << 16), hi = __uint_as_float(w[i] & 0xffff0000u);
+                    ss += lo * lo + hi * hi;
+                }
+            }
+            const float r = a.qk_l2norm ? rsqrtf(ss + 1e-6f) : 1.0f;
+            (half ? s_rq : s_rk)[row] = r;
+        }
+        ok = tc::mbar_wait_bounded(&done, 0, p.wait_limit);
+        if (!ok && tid == 0) {
+            const bool d = tc::mbar_wait_bounded(&done, 0, tc::WAIT_POLLS);
+            atomicOr(reinterpret_cast<int*>(a.workspace), d ? tc::ERR_WAIT : tc::ERR_WAIT | tc::ERR_DRAIN);
+            s_ok = 0;
+        }
+        tc::fence_after_sync();
+        __syncthreads();
+        ok = s_ok;
+    }
+    float* X = reinterpret_cast<float*>(sm + P_X);        // the tiles have been consumed
+    float* Y = reinterpret_cast<float*>(sm + P_Y);
+    float* W = reinterpret_cast<float*>(sm + P_W);        // W[b][j] = rk_j e^{g_(16 b - 1) - g_j}, j < 16 b
+    const int rep = a.Hv / a.Hk;
+    const bool live = row < len;
+    constexpr float FIX = 4294967296.f, UNFIX = 1.f / 4294967296.f;
+    for (int e = 0; ok && e < rep; ++e) {
+        const int h = hk * rep + e;
+        uint8_t* rec = reinterpret_cast<uint8_t*>(a.workspace) + WS_HEAD + (idx * a.Hv + h) * (size_t)REC;
+        // sums of the log-decays (base 2), exact in 2^-32 fixed point.  A step below -4096 is
+        // an exponential of 0 in any sum; a NaN travels with beta.
+        if (half == 0) {
+            long long g = 0;
+            float beta = 0.f;
+            if (live) {
+                const size_t at = (size_t)(t0 + row) * a.Hv + h;
+                const float x = log_decay_mode(a.z[at], __expf(a.A[h]), a.g_min, a.gate_mode) * 1.4426950408889634f;
+                beta = x == x ? a.beta[at] : x;
+                g = (long long)(fminf(fmaxf(x, -4096.f), 4096.f) * FIX);
+            }
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(~0u, g, o);
+                if (lane >= o) g += y;
+            }
+            if (lane == 31) s_wsum[warp] = g;
+            s_g[row] = g;
+            s_beta[row] = beta;
+        }
+        __syncthreads();
+        if (half == 0) {
+            long long g = s_g[row];
+            for (int w = 0; w < warp; ++w) g += s_wsum[w];
+            s_g[row] = g;
+        }
+        __syncthreads();
+        const long long gi = s_g[row], gC = s_g[C - 1];
+        for (int j = tid; j < 8 * C; j += PT) {
+            const int b = j / C, c = j % C;
+            W[j] = c < 16 * b ? s_rk[c] * exp2f((float)(s_g[16 * b - 1] - s_g[c]) * UNFIX) : 0.f;
+        }
+        if (half == 1) {
+            const float eg = exp2f((float)gi * UNFIX), beta = s_beta[row];
+            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (live)
+                f = make_float4(beta, beta * eg * s_rk[row], exp2f((float)(gC - gi) * UNFIX) * s_rk[row],
+                                eg * s_rq[row] * a.scale);
+            *reinterpret_cast<float4*>(rec + REC_F + row * 16) = f;
+            if (row == 0) *reinterpret_cast<float*>(rec + REC_F + C * 16) = exp2f((float)gC * UNFIX);
+        }
+        __syncthreads();
+        // A and the masked Q K^T, row by row: 64 columns per thread, 16 at a time
+        {
+            const int b = row >> 4;
+            const float u = b ? exp2f((float)(gi - s_g[16 * b - 1]) * UNFIX) : 0.f;     // e^{g_i - g_(16 b - 1)}
+            const float ka = live ? s_beta[row] * s_rk[row] : 0.f, qa = live ? s_rq[row] * a.scale : 0.f;
+            const uint32_t lane0 = tm + ((uint32_t)(warp & 3) << 21);
+#pragma unroll 1
+            for (int cb = half * 4; cb < half * 4 + 4; ++cb) {
+                float G[16], P[16];
+                tc::tmem_ld16(lane0 + cb * 16, G);
+                tc::tmem_ld16(lane0 + 128 + cb * 16, P);
+                tc::tmem_ld_wait();
+                float w[16];                                 // rk_j e^{g_i - g_j}, 0 for j > i
+                if (cb < b) {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) w[c] = u * W[b * C + cb * 16 + c];
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        const int j = cb * 16 + c;
+                        w[c] = cb == b && j <= row ? s_rk[j] * exp2f((float)(gi - s_g[j]) * UNFIX) : 0.f;
+                    }
+                }
+                // masked places by selection, not by a product with 0
+                uint32_t q[8];
+#pragma unroll
+                for (int c = 0; c < 16; c += 2) {
+                    const int j = cb * 16 + c;
+                    const float x0 = j <= row && live ? qa * w[c] * P[c] : 0.f;
+                    const float x1 = j + 1 <= row && live ? qa * w[c + 1] * P[c + 1] : 0.f;
+                    const __nv_bfloat162 hh = __floats2bfloat162_rn(x0, x1);
+                    q[c >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
+                }
+                if (cb < 4 || row >= 64) {
+                    uint8_t* dst = rec + REC_A + (cb < 4 ? 0 : 16384 - 64 * 128);
+                    const int piece = (cb & 3) * 2;
+                    *reinterpret_cast<uint4*>(dst + swz(row, piece)) = make_uint4(q[0], q[1], q[2], q[3]);
+                    *reinterpret_cast<uint4*>(dst + swz(row, piece + 1)) = make_uint4(q[4], q[5], q[6], q[7]);
+                }
+                if (cb <= b) {
+#pragma unroll
+                    for (int c = 0; c < 16; c += 4) {
+                        float x[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int j = cb * 16 + c + i;
+                            x[i] = j < row && live ? ka * w[c + i] * G[c + i] : 0.f;
+                        }
+                        *reinterpret_cast<float4*>(X + row * XS + cb * 16 + c) = make_float4(x[0], x[1], x[2], x[3]);
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        // inverses of the diagonal blocks: lane c < 16 of warp b solves for column c of block b
+        {
+            float* B = X + warp * 16 * XS + warp * 16;
+            float x[16];
+            if (lane < 16) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float s = i == lane ? 1.f : 0.f;
+#pragma unroll
+                    for (int j = 0; j < i; ++j) s -= B[i * XS + j] * x[j];
+                    x[i] = s;
+                }
+            }
+            __syncwarp();
+            if (lane < 16) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) B[i * XS + lane] = x[i];
+            }
+        }
+        __syncthreads();
+        // merges: 16 -> 32 (a warp each), 32 -> 64, 64 -> 128 (16 x 16 tiles over the warps)
+        if (warp < 4) {
+            const int o = warp * 32;
+            float acc[2][4] = {};
+            float* y = Y + warp * 16 * YS;
+            block_product(acc, X + (o + 16) * XS + o, XS, X + o * XS + o, XS, 1, lane);
+            block_store(acc, y, YS, 1.f, lane);
+            __syncwarp();
+            float acd[2][4] = {};
+            block_product(acd, X + (o + 16) * XS + o + 16, XS, y, YS, 1, lane);
+            block_store(acd, X + (o + 16) * XS + o, XS, -1.f, lane);
+        }
+        __syncthreads();
+#pragma unroll 1
+        for (int s = 32; s < C; s *= 2) {
+            const int nb = s / 16, tiles = (C / (2 * s)) * nb * nb;
+            for (int w = warp; w < tiles; w += 8) {              // Y = B X, X lower: k from the tile's column on
+                const int m = w / (nb * nb), r = w / nb % nb, c = w % nb, o = m * 2 * s;
+                float acc[2][4] = {};
+                block_product(acc, X + (o + s + 16 * r) * XS + o + 16 * c, XS, X + (o + 16 * c) * XS + o + 16 * c, XS, nb - c, lane);
+                block_store(acc, Y + (m * s + 16 * r) * YS + 16 * c, YS, 1.f, lane);
+            }
+            __syncthreads();
+            for (int w = warp; w < tiles; w += 8) {              // - Y^-1 (B X): k up to the tile's row
+                const int m = w / (nb * nb), r = w / nb % nb, c = w % nb, o = m * 2 * s;
+                float acc[2][4] = {};
+                block_product(acc, X + (o + s + 16 * r) * XS + o + s, XS, Y + m * s * YS + 16 * c, YS, r + 1, lane);
+                block_store(acc, X + (o + s + 16 * r) * XS + o + 16 * c, XS, -1.f, lane);
+            }
+            __syncthreads();
+        }
+        // T = hi + lo, 16 bytes of each per thread and step; blocks above the diagonal are zero
+        for (int i = tid; i < (C + 64) * 8; i += PT) {
+            const int c = i & 7, rr = i >> 3;
+            const int r = rr < C ? rr : rr - 64, col = (rr < C ? 0 : 64) + c * 8;
+            uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
+            if (col / 16 <= r / 16) {
+                const float4 x = *reinterpret_cast<const float4*>(X + r * XS + col), y = *reinterpret_cast<const float4*>(X + r * XS + col + 4);
+                split2(x.x, x.y, &hi[0], &lo[0]);
+                split2(x.z, x.w, &hi[1], &lo[1]);
+                split2(y.x, y.y, &hi[2], &lo[2]);
+                split2(y.z, y.w, &hi[3], &lo[3]);
+            }
+            const uint32_t at = (rr < C ? 0 : 16384 - 64 * 128) + swz(r, c);
+            *reinterpret_cast<uint4*>(rec + REC_THI + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(rec + REC_TLO + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        __syncthreads();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 0) tc::tmem_dealloc(tm, 256);
+}
+
+// ---------------------------------------------------------------------------
+// scan
+// ---------------------------------------------------------------------------
+constexpr int COLS = 32;                      // value columns per CTA
+constexpr int ST = 320;                       // 8 warps of rows, the loads, the MMAs
+constexpr int S_K = 0, S_Q = 2 * TILE, S_THI = 3 * TILE, S_TLO = S_THI + 32768, S_A = S_TLO + 32768,
+              S_S = S_A + 32768, S_R = S_S + 16384, S_END = S_R + 16384;
+constexpr int S_SMEM = S_END + 1024;
+// V' in bf16 (the masked product's operand) borrows the zero half-slab of T's low part,
+// which is read earlier in the chunk, and leaves it zero again
+constexpr int S_V = S_TLO + 16384;
+// TMEM columns
+constexpr int D_KS = 0, D_TR = 64, D_KV = 128, D_QS = 192, D_AV = 224;
+
+// descriptor of the 128 x 32 MN-major operand with 64-byte rows (64-byte swizzle)
+KDA_DEV uint64_t sw64_desc_mn(uint32_t addr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((addr >> 4) & 0x3FFFu);
+    d |= (uint64_t)1 << 16;                            // one 32-element block: unused
+    d |= (uint64_t)((512u >> 4) & 0x3FFFu) << 32;      // 8-row K groups
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)4 << 61;                            // 64-byte swizzle
+    return d;
+}
+
+KDA_DEV bool wait_warp(uint64_t* bar, uint32_t parity, uint32_t limit, volatile int* abort) {
+    if (limit && __all_sync(~0u, tc::mbar_try_wait(bar, parity))) return true;
+    return __all_sync(~0u, tc::mbar_wait_role(bar, parity, limit, abort));
+}
+
+// this thread's 16 columns of a row, hi and lo parts, into the 128-byte row [hi 32 | lo 32]
+KDA_DEV void store_split(uint8_t* base, int row, int w, const float* x) {
+    uint32_t hi[8], lo[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) split2(x[2 * i], x[2 * i + 1], &hi[i], &lo[i]);
+    *reinterpret_cast<uint4*>(base + swz(row, 2 * w)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(base + swz(row, 2 * w + 1)) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+    *reinterpret_cast<uint4*>(base + swz(row, 4 + 2 * w)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    *reinterpret_cast<uint4*>(base + swz(row, 5 + 2 * w)) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+}
+
+__global__ void __launch_bounds__(ST, 1)
+gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk) {
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t k_full[2], k_empty[2], q_full, q_empty, t_full, t_empty, a_full, a_empty, edge,
+        s_ready, r_ready, v_ready, ks_done, qs_done, tr_done, kv_done, av_done, drained;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+    const kda_gdn_prefill_args& a = p.a;
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int slice = blockIdx.x % (DH / COLS);
+    const int h = blockIdx.x / (DH / COLS) % a.Hv;
+    const int n = blockIdx.x / (DH / COLS) / a.Hv;
+    const int hk = h / (a.Hv / a.Hk);
+    const int t0 = a.cu_seqlens[n], T = a.cu_seqlens[n + 1] - t0;
+    const int nc = (T + C - 1) / C;
+    const uint32_t limit = p.wait_limit;
+    volatile int* abort = &s_abort;
+
+    if (tid == 0) {
+        uint64_t* ones[] = {&k_full[0], &k_full[1], &k_empty[0], &k_empty[1], &q_full, &q_empty, &t_full, &t_empty, &a_full,
+                            &a_empty, &edge, &ks_done, &qs_done, &tr_done, &kv_done, &av_done, &drained};
+        for (uint64_t* b : ones) tc::mbar_init(b, 1);
+        tc::mbar_init(&s_ready, 256);
+        tc::mbar_init(&r_ready, 256);
+        tc::mbar_init(&v_ready, 256);
+        tc::mbar_fence_init();
+        s_abort = 0;
+    }
+    // the halves above the diagonal of the three triangular operands
+    for (int i = tid; i < 3 * 512; i += ST)
+        *reinterpret_cast<uint4*>(sm + S_THI + (i >> 9) * 32768 + 16384 + (i & 511) * 16) = make_uint4(0, 0, 0, 0);
+    tc::fence_proxy_async();
+    if (warp == 9) {
+        tc::tmem_alloc(&s_tmem, 256);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tm = s_tmem;
+
+    if (warp == 8) {
+        // ---------------- loads ----------------
+        const long base = chunks_before(a, n);
+        bool ok = true;
+        uint32_t kq = 0, nt = 0, na = 0, ne = 0;        // chunks whose K and Q, T, A were issued; edge tiles
+        for (int c = 0; c < nc && ok; ++c) {
+            const uint8_t* rec = reinterpret_cast<const uint8_t*>(a.workspace) + WS_HEAD + ((base + c) * a.Hv + h) * (size_t)REC;
+            const int b = c & 1, left = T - c * C;
+            uint8_t* kt = sm + S_K + b * TILE;
+            if (c >= 2) ok = wait_warp(&k_empty[b], (c / 2 - 1) & 1, limit, abort);
+            if (!ok) break;
+            const bool zero = left < C;                  // rows of the next sequence: 0 x NaN
+            uint64_t* bar = zero ? &edge : &k_full[b];
+            if (lane == 0) {
+                tc::mbar_arrive_expect_tx(bar, TILE);
+                for (int s = 0; s < 2; ++s) tc::tma_load_3d(kt + s * 16384, &mk, s * 64, hk, t0 + c * C, bar);
+            }
+            if (c >= 1) ok = wait_warp(&q_empty, (c - 1) & 1, limit, abort);
+            if (ok && lane == 0) {
+                tc::mbar_arrive_expect_tx(&q_full, TILE);
+                for (int s = 0; s < 2; ++s) tc::tma_load_3d(sm + S_Q + s * 16384, &mq, s * 64, hk, t0 + c * C, &q_full);
+            }
+            if (zero) {
+                ++ne;
+                ok = wait_warp(&edge, 0, limit, abort) && ok;
+                for (int e = lane; e < (C - left) * 16; e += 32) {
+                    const int r = left + (e >> 4), q = e & 15;
+                    *reinterpret_cast<uint4*>(kt + (q >> 3) * 16384 + r * 128 + (q & 7) * 16) = make_uint4(0, 0, 0, 0);
+                }
+                tc::fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&k_full[b]);
+            }
+            ++kq;
+            if (!ok) break;
+            if (c >= 1) ok = wait_warp(&t_empty, (c - 1) & 1, limit, abort);
+            if (!ok) break;
+            if (lane == 0) {
+                tc::mbar_arrive_expect_tx(&t_full, 2 * TRI);
+                tc::bulk_load(sm + S_THI, rec + REC_THI, 16384, &t_full);
+                tc::bulk_load(sm + S_THI + 16384 + 8192, rec + REC_THI + 16384, 8192, &t_full);
+                tc::bulk_load(sm + S_TLO, rec + REC_TLO, 16384, &t_full);
+                tc::bulk_load(sm + S_TLO + 16384 + 8192, rec + REC_TLO + 16384, 8192, &t_full);
+            }
+            ++nt;
+            if (c >= 1) ok = wait_warp(&a_empty, (c - 1) & 1, limit, abort);
+            if (!ok) break;
+            if (lane == 0) {
+                tc::mbar_arrive_expect_tx(&a_full, TRI);
+                tc::bulk_load(sm + S_A, rec + REC_A, 16384, &a_full);
+                tc::bulk_load(sm + S_A + 16384 + 8192, rec + REC_A + 16384, 8192, &a_full);
+            }
+            ++na;
+        }
+        if (!ok && lane == 0) {     // give up: what was issued lands before the CTA leaves (at most one
+            bool d = true;          // phase per barrier is open; one that was never issued runs into its limit)
+            for (int b = 0; b < 2; ++b) d = tc::drain_phase(&k_full[b], (kq + 1 - b) / 2) && d;
+            d = tc::drain_phase(&q_full, kq) && tc::drain_phase(&t_full, nt) && tc::drain_phase(&a_full, na) &&
+                tc::drain_phase(&edge, ne) && d;
+            tc::mbar_wait_bounded(&k_full[kq & 1], (kq / 2) & 1, 1u << 16);
+            atomicOr(reinterpret_cast<int*>(a.workspace), d ? tc::ERR_WAIT : tc::ERR_WAIT | tc::ERR_DRAIN);
+        }
+    } else if (warp == 9) {
+        // ---------------- MMAs: the warp computes together, one lane issues ----------------
+        bool ok = true;
+        const bool one = lane == 0;
+        const uint32_t tmu = __shfl_sync(~0u, tm, 0), sb = __shfl_sync(~0u, tc::smem_u32(sm), 0);
+        const uint32_t id64 = tc::idesc_bf16(128, 64, false, true), id32 = tc::idesc_bf16(128, 32, false, true),
+                       idt = tc::idesc_bf16(128, 64, true, true);
+        const uint64_t dS = tc::sw128_desc_mn(sb + S_S, 16384), dR = tc::sw128_desc_mn(sb + S_R, 16384);
+        // D[., cols] = A (K-major tile of two slabs) times B (MN-major, 16 K rows per step)
+        auto rows = [&](uint32_t d, uint64_t ad, uint64_t bd, uint32_t step, uint32_t id, bool acc) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                tc::mma_f16_ss_if(one, d, ad + (((k >> 2) * 16384 + (k & 3) * 32) >> 4), bd + k * (step >> 4), id, acc || k > 0);
+        };
+#pragma unroll 1
+        for (int c = 0; c < nc; ++c) {
+            const uint32_t ph = c & 1, kb = sb + S_K + (c & 1) * TILE;
+            const uint64_t dK = tc::sw128_desc(kb);
+            ok = wait_warp(&k_full[c & 1], (c / 2) & 1, limit, abort) && wait_warp(&s_ready, ph, limit, abort);
+            if (!ok) break;
+            tc::fence_after_sync();
+            rows(tmu + D_KS, dK, dS, 2048, id64, false);
+            tc::mma_commit_if(one, &ks_done);
+            ok = wait_warp(&q_full, ph, limit, abort);
+            if (!ok) break;
+            rows(tmu + D_QS, tc::sw128_desc(sb + S_Q), dS, 2048, id32, false);     // S rounded to bf16: o only
+            tc::mma_commit_if(one, &qs_done);
+            tc::mma_commit_if(one, &q_empty);
+            ok = wait_warp(&t_full, ph, limit, abort) && wait_warp(&r_ready, ph, limit, abort);
+            if (!ok) break;
+            tc::fence_after_sync();
+            rows(tmu + D_TR, tc::sw128_desc(sb + S_THI), dR, 2048, id64, false);
+            rows(tmu + D_TR, tc::sw128_desc(sb + S_TLO), dR, 2048, id32, true);
+            tc::mma_commit_if(one, &tr_done);
+            tc::mma_commit_if(one, &t_empty);
+            ok = wait_warp(&v_ready, ph, limit, abort);
+            if (!ok) break;
+            tc::fence_after_sync();
+            const uint64_t dKt = tc::sw128_desc_mn(kb, 16384);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)                                            // K^T: tokens are the K rows
+                tc::mma_f16_ss_if(one, tmu + D_KV, dKt + k * (2048 >> 4), dR + k * (2048 >> 4), idt, k > 0);
+            tc::mma_commit_if(one, &kv_done);
+            tc::mma_commit_if(one, &k_empty[c & 1]);
+            ok = wait_warp(&a_full, ph, limit, abort);
+            if (!ok) break;
+            rows(tmu + D_AV, tc::sw128_desc(sb + S_A), sw64_desc_mn(sb + S_V), 1024, id32, false);
+            tc::mma_commit_if(one, &av_done);
+            tc::mma_commit_if(one, &a_empty);
+        }
+        if (one) {
+            tc::mma_commit(&drained);
+            const bool d = tc::mbar_wait_bounded(&drained, 0, tc::WAIT_POLLS);
+            if (!ok || !d) atomicOr(reinterpret_cast<int*>(a.workspace), d ? tc::ERR_WAIT : tc::ERR_WAIT | tc::ERR_DRAIN);
+        }
+        __syncwarp();
+    } else {
+        // ---------------- rows: thread (row, w) owns columns 16 w .. 16 w + 15 of its row ----------------
+        const int row = tid & 127, w = tid >> 7;
+        const int col = slice * COLS + 16 * w;
+        const long base = chunks_before(a, n);
+        const uint32_t tl = tm + ((uint32_t)(warp & 3) << 21);
+        const size_t sbase = ((size_t)n * a.Hv + h) * (size_t)DH * DH + (size_t)row * DH + col;   // row = key channel
+        float S[16];
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+            const float4 x = a.S0 ? *reinterpret_cast<const float4*>(a.S0 + sbase + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+            S[i] = x.x; S[i + 1] = x.y; S[i + 2] = x.z; S[i + 3] = x.w;
+        }
+        bool ok = true;
+        if (nc > 0) {
+            store_split(sm + S_S, row, w, S);
+            tc::fence_proxy_async();
+            tc::mbar_arrive(&s_ready);
+        }
+#pragma unroll 1
+        for (int c = 0; c < nc; ++c) {
+            const uint32_t ph = c & 1;
+            const int t = t0 + c * C + row;                   // row = token
+            const bool live = c * C + row < T;
+            const uint8_t* rec = reinterpret_cast<const uint8_t*>(a.workspace) + WS_HEAD + ((base + c) * a.Hv + h) * (size_t)REC;
+            const float4 f = *reinterpret_cast<const float4*>(rec + REC_F + row * 16);
+            const float gamma = *reinterpret_cast<const float*>(rec + REC_F + C * 16);
+            float v[16];
+            const size_t at = ((size_t)t * a.Hv + h) * DH + col;
+            if (live) {
+                load8_bf16(reinterpret_cast<const uint16_t*>(a.v) + at, v);
+                load8_bf16(reinterpret_cast<const uint16_t*>(a.v) + at + 8, v + 8);
+            }
+            // R = beta (v - e^g rk K S)
+            ok = wait_warp(&ks_done, ph, limit, abort);
+            if (!ok) break;
+            tc::fence_after_sync();
+            float x[16], y[16];
+            tc::tmem_ld16(tl + D_KS + 16 * w, x);
+            tc::tmem_ld16(tl + D_KS + 32 + 16 * w, y);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = live ? f.x * v[i] - f.y * (x[i] + y[i]) : 0.f;
+            store_split(sm + S_R, row, w, x);
+            tc::fence_proxy_async();
+            tc::fence_before_sync();
+            tc::mbar_arrive(&r_ready);
+            // V' = T R, and V'' = e^{g_C - g} rk V' over R (T R is done with it)
+            ok = wait_warp(&tr_done, ph, limit, abort);
+            if (!ok) break;
+            tc::fence_after_sync();
+            tc::tmem_ld16(tl + D_TR + 16 * w, x);
+            tc::tmem_ld16(tl + D_TR + 32 + 16 * w, y);
+            tc::tmem_ld_wait();
+            uint32_t vb[8];
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+                x[i] = live ? x[i] + y[i] : 0.f;
+                x[i + 1] = live ? x[i + 1] + y[i + 1] : 0.f;
+                const __nv_bfloat162 hh = __floats2bfloat162_rn(x[i], x[i + 1]);          // for o only
+                vb[i >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
+                x[i] *= f.z;
+                x[i + 1] *= f.z;
+            }
+            {
+                uint8_t* vr = sm + S_V + row * 64;                 // 64-byte rows, pieces swapped by (row / 2) mod 4
+                const int sw = (row >> 1) & 3;
+                *reinterpret_cast<uint4*>(vr + (((2 * w) ^ sw) << 4)) = make_uint4(vb[0], vb[1], vb[2], vb[3]);
+                *reinterpret_cast<uint4*>(vr + (((2 * w + 1) ^ sw) << 4)) = make_uint4(vb[4], vb[5], vb[6], vb[7]);
+            }
+            store_split(sm + S_R, row, w, x);
+            tc::fence_proxy_async();
+            tc::fence_before_sync();
+            tc::mbar_arrive(&v_ready);
+            float o[16];
+            if (a.o) {                                             // e^g scale rq Q S (the product is long done)
+                ok = wait_warp(&qs_done, ph, limit, abort);
+                if (!ok) break;
+                tc::fence_after_sync();
+                tc::tmem_ld16(tl + D_QS + 16 * w, o);
+                tc::tmem_ld_wait();
+            }
+            // S <- e^{g_C} S + K^T V''
+            ok = wait_warp(&kv_done, ph, limit, abort);
+            if (!ok) break;
+            tc::fence_after_sync();
+            tc::tmem_ld16(tl + D_KV + 16 * w, x);
+            tc::tmem_ld16(tl + D_KV + 32 + 16 * w, y);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) S[i] = gamma * S[i] + (x[i] + y[i]);
+            if (c + 1 < nc) {
+                store_split(sm + S_S, row, w, S);
+                tc::fence_proxy_async();
+                tc::fence_before_sync();
+                tc::mbar_arrive(&s_ready);
+            }
+            ok = wait_warp(&av_done, ph, limit, abort);
+            if (!ok) break;
+            tc::fence_after_sync();
+            {
+                uint8_t* vr = sm + S_V + row * 64 + 32 * w;        // the zero half-slab is one again
+                *reinterpret_cast<uint4*>(vr) = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4*>(vr + 16) = make_uint4(0, 0, 0, 0);
+            }
+            if (a.o) {
+                tc::tmem_ld16(tl + D_AV + 16 * w, x);
+                tc::tmem_ld_wait();
+                if (live) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[i] = f.w * o[i] + x[i];
+                    store8_bf16(reinterpret_cast<uint16_t*>(a.o) + at, o);
+                    store8_bf16(reinterpret_cast<uint16_t*>(a.o) + at + 8, o + 8);
+                }
+                __syncwarp();
+            }
+        }
+        if (a.S_T && ok) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<float4*>(a.S_T + sbase + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 9) tc::tmem_dealloc(tm, 256);
+}
+
+// ---------------------------------------------------------------------------
+
+static long count_chunks(const kda_gdn_prefill_args& a) {
+    long s = 0;
+    for (int n = 0; n < a.num_seqs; ++n) s += (a.cu_seqlens_host[n + 1] - a.cu_seqlens_host[n] + C - 1) / C;
+    return s;
+}
+
+size_t chunked_workspace_size(const kda_gdn_prefill_args& a) {
+    return WS_HEAD + (size_t)count_chunks(a) * a.Hv * REC;
+}
 
 cudaError_t launch_chunked(const kda_gdn_prefill_args& a, cudaStream_t s) {
-    const cudaError_t e = cudaMemsetAsync(a.workspace, 0, 4, s);
-    return e != cudaSuccess ? e : launch_recurrent(a, s);
+    Params p;
+    p.a = a;
+    p.chunks = count_chunks(a);
+    p.wait_limit = wait_limit();
+    cudaError_t e = cudaMemsetAsync(a.workspace, 0, 4, s);
+    CUtensorMap mq = {}, mk = {};
+    if (p.chunks > 0) {
+        if (e == cudaSuccess) e = make_map_heads(&mq, a.q, DH, a.Hk, a.T_total, (uint64_t)a.Hk * DH, 1, C);
+        if (e == cudaSuccess) e = make_map_heads(&mk, a.k, DH, a.Hk, a.T_total, (uint64_t)a.Hk * DH, 1, C);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(gdn_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, P_SMEM);
+        if (e != cudaSuccess) return e;
+        gdn_prep_kernel<<<(unsigned)(p.chunks * a.Hk), PT, P_SMEM, s>>>(p, mq, mk);
+        count_launches(1);
+        e = cudaGetLastError();
+    }
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(gdn_scan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S_SMEM);
+    if (e != cudaSuccess) return e;
+    gdn_scan_kernel<<<(unsigned)((long)a.num_seqs * a.Hv * (DH / COLS)), ST, S_SMEM, s>>>(p, mq, mk);
+    count_launches(1);
+    return cudaGetLastError();
 }
 
 }  // namespace gdn
