@@ -425,15 +425,17 @@ gdn_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
 // scan
 // ---------------------------------------------------------------------------
 constexpr int COLS = 32;                      // value columns per CTA
-constexpr int ST = 320;                       // 8 warps of rows, the loads, the MMAs
+constexpr int ST = 448;                       // warps 0-7 state rows, 8-11 output rows, 12 loads, 13 MMAs
 constexpr int S_K = 0, S_Q = 2 * TILE, S_THI = 3 * TILE, S_TLO = S_THI + 32768, S_A = S_TLO + 32768,
               S_S = S_A + 32768, S_R = S_S + 16384, S_END = S_R + 16384;
 constexpr int S_SMEM = S_END + 1024;
-// V' in bf16 (the masked product's operand) borrows the zero half-slab of T's low part,
-// which is read earlier in the chunk, and leaves it zero again
-constexpr int S_V = S_TLO + 16384;
-// TMEM columns
-constexpr int D_KS = 0, D_TR = 64, D_KV = 128, D_QS = 192, D_AV = 224;
+// The zero half-slabs of the triangular operands are lent out while no MMA reads them and
+// zeroed again by their readers (all are 128 rows of 64 bytes, 64-byte swizzle): T's high part
+// takes the chunk's values v until R is formed, its low part V' in bf16 (the masked product's
+// operand) from T R on, the masked Q K^T the output rows on their way out.
+constexpr int S_VIN = S_THI + 16384, S_V = S_TLO + 16384, S_O = S_A + 16384;
+// TMEM columns (Q S twice: the outputs of a chunk are read while the next one's are formed)
+constexpr int D_KS = 0, D_TR = 64, D_KV = 128, D_AV = 192, D_QS = 256, D_COLS = 512;
 
 // descriptor of the 128 x 32 MN-major operand with 64-byte rows (64-byte swizzle)
 KDA_DEV uint64_t sw64_desc_mn(uint32_t addr) {
@@ -446,9 +448,23 @@ KDA_DEV uint64_t sw64_desc_mn(uint32_t addr) {
     return d;
 }
 
-KDA_DEV bool wait_warp(uint64_t* bar, uint32_t parity, uint32_t limit, volatile int* abort) {
-    if (limit && __all_sync(~0u, tc::mbar_try_wait(bar, parity))) return true;
-    return __all_sync(~0u, tc::mbar_wait_role(bar, parity, limit, abort));
+// byte offset of 16-byte piece c (0 .. 3) of row r in rows of 64 bytes
+KDA_DEV uint32_t swz64(int r, int c) { return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4)); }
+
+// A wait that gives up by raising *abort and going on: everything behind it stays within
+// the CTA's own buffers and rows, and the roles leave at the top of their next chunk.  (A
+// vote in every wait would cost the serial chain some 50 cycles each.)
+KDA_DEV void wait_go(uint64_t* bar, uint32_t parity, uint32_t limit, volatile int* abort) {
+    if (limit && tc::mbar_try_wait(bar, parity)) return;
+    tc::mbar_wait_role(bar, parity, limit, abort);
+}
+
+// whether any of the 128 output threads says so
+KDA_DEV bool any_of_128(bool x) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r) : "r"((uint32_t)x) : "memory");
+    return r != 0;
 }
 
 // this thread's 16 columns of a row, hi and lo parts, into the 128-byte row [hi 32 | lo 32]
@@ -463,10 +479,11 @@ KDA_DEV void store_split(uint8_t* base, int row, int w, const float* x) {
 }
 
 __global__ void __launch_bounds__(ST, 1)
-gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk) {
+gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo) {
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t k_full[2], k_empty[2], q_full, q_empty, t_full, t_empty, a_full, a_empty, edge,
-        s_ready, r_ready, v_ready, ks_done, qs_done, tr_done, kv_done, av_done, drained;
+    __shared__ __align__(8) uint64_t k_full[2], k_empty[2], q_full, t_full, a_full, v_full, edge, s_ready, r_ready, v_ready,
+        ks_done, qs_done, tr_done, kv_done, av_done, drained;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     const kda_gdn_prefill_args& a = p.a;
@@ -482,12 +499,12 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
     volatile int* abort = &s_abort;
 
     if (tid == 0) {
-        uint64_t* ones[] = {&k_full[0], &k_full[1], &k_empty[0], &k_empty[1], &q_full, &q_empty, &t_full, &t_empty, &a_full,
-                            &a_empty, &edge, &ks_done, &qs_done, &tr_done, &kv_done, &av_done, &drained};
+        uint64_t* ones[] = {&k_full[0], &k_full[1], &k_empty[0], &k_empty[1], &q_full, &t_full, &a_full, &v_full, &edge, &ks_done,
+                            &qs_done, &tr_done, &kv_done, &av_done, &drained};
         for (uint64_t* b : ones) tc::mbar_init(b, 1);
         tc::mbar_init(&s_ready, 256);
-        tc::mbar_init(&r_ready, 256);
-        tc::mbar_init(&v_ready, 256);
+        tc::mbar_init(&r_ready, 256 + 128);
+        tc::mbar_init(&v_ready, 256 + 128);
         tc::mbar_fence_init();
         s_abort = 0;
     }
@@ -495,40 +512,44 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
     for (int i = tid; i < 3 * 512; i += ST)
         *reinterpret_cast<uint4*>(sm + S_THI + (i >> 9) * 32768 + 16384 + (i & 511) * 16) = make_uint4(0, 0, 0, 0);
     tc::fence_proxy_async();
-    if (warp == 9) {
-        tc::tmem_alloc(&s_tmem, 256);
+    if (warp == 13) {
+        tc::tmem_alloc(&s_tmem, D_COLS);
         tc::tmem_relinquish();
     }
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tm = s_tmem;
+    const long base = chunks_before(a, n);
+    const uint8_t* recs = reinterpret_cast<const uint8_t*>(a.workspace) + WS_HEAD + (base * a.Hv + h) * (size_t)REC;
+    const size_t rec_step = (size_t)a.Hv * REC;
 
-    if (warp == 8) {
+    if (warp == 12) {
         // ---------------- loads ----------------
-        const long base = chunks_before(a, n);
-        bool ok = true;
-        uint32_t kq = 0, nt = 0, na = 0, ne = 0;        // chunks whose K and Q, T, A were issued; edge tiles
-        for (int c = 0; c < nc && ok; ++c) {
-            const uint8_t* rec = reinterpret_cast<const uint8_t*>(a.workspace) + WS_HEAD + ((base + c) * a.Hv + h) * (size_t)REC;
+        int c = 0;
+        bool zeroed = false;
+        for (; c < nc; ++c) {
+            if (__any_sync(~0u, *abort)) break;
+            const uint8_t* rec = recs + c * rec_step;
             const int b = c & 1, left = T - c * C;
             uint8_t* kt = sm + S_K + b * TILE;
-            if (c >= 2) ok = wait_warp(&k_empty[b], (c / 2 - 1) & 1, limit, abort);
-            if (!ok) break;
+            if (c >= 2) wait_go(&k_empty[b], (c / 2 - 1) & 1, limit, abort);
             const bool zero = left < C;                  // rows of the next sequence: 0 x NaN
             uint64_t* bar = zero ? &edge : &k_full[b];
+            __syncwarp();
             if (lane == 0) {
                 tc::mbar_arrive_expect_tx(bar, TILE);
                 for (int s = 0; s < 2; ++s) tc::tma_load_3d(kt + s * 16384, &mk, s * 64, hk, t0 + c * C, bar);
             }
-            if (c >= 1) ok = wait_warp(&q_empty, (c - 1) & 1, limit, abort);
-            if (ok && lane == 0) {
+            if (c >= 1) wait_go(&qs_done, (c - 1) & 1, limit, abort);
+            __syncwarp();
+            if (lane == 0) {
                 tc::mbar_arrive_expect_tx(&q_full, TILE);
                 for (int s = 0; s < 2; ++s) tc::tma_load_3d(sm + S_Q + s * 16384, &mq, s * 64, hk, t0 + c * C, &q_full);
             }
             if (zero) {
-                ++ne;
-                ok = wait_warp(&edge, 0, limit, abort) && ok;
+                zeroed = true;
+                wait_go(&edge, 0, limit, abort);
                 for (int e = lane; e < (C - left) * 16; e += 32) {
                     const int r = left + (e >> 4), q = e & 15;
                     *reinterpret_cast<uint4*>(kt + (q >> 3) * 16384 + r * 128 + (q & 7) * 16) = make_uint4(0, 0, 0, 0);
@@ -537,39 +558,48 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&k_full[b]);
             }
-            ++kq;
-            if (!ok) break;
-            if (c >= 1) ok = wait_warp(&t_empty, (c - 1) & 1, limit, abort);
-            if (!ok) break;
+            if (c >= 1) wait_go(&tr_done, (c - 1) & 1, limit, abort);
+            __syncwarp();
             if (lane == 0) {
+                tc::mbar_arrive_expect_tx(&v_full, C * COLS * 2);
+                tc::tma_load_3d(sm + S_VIN, &mv, slice * COLS, h, t0 + c * C, &v_full);
                 tc::mbar_arrive_expect_tx(&t_full, 2 * TRI);
                 tc::bulk_load(sm + S_THI, rec + REC_THI, 16384, &t_full);
                 tc::bulk_load(sm + S_THI + 16384 + 8192, rec + REC_THI + 16384, 8192, &t_full);
                 tc::bulk_load(sm + S_TLO, rec + REC_TLO, 16384, &t_full);
                 tc::bulk_load(sm + S_TLO + 16384 + 8192, rec + REC_TLO + 16384, 8192, &t_full);
             }
-            ++nt;
-            if (c >= 1) ok = wait_warp(&a_empty, (c - 1) & 1, limit, abort);
-            if (!ok) break;
+            if (c >= 1) wait_go(&av_done, (c - 1) & 1, limit, abort);
+            __syncwarp();
             if (lane == 0) {
                 tc::mbar_arrive_expect_tx(&a_full, TRI);
                 tc::bulk_load(sm + S_A, rec + REC_A, 16384, &a_full);
                 tc::bulk_load(sm + S_A + 16384 + 8192, rec + REC_A + 16384, 8192, &a_full);
+                // two chunks ahead into L2: this slice's values, and its share of what all slices read
+                if (c + 2 < nc) {
+                    const uint8_t* far = rec + 2 * rec_step;
+                    const int t2 = t0 + (c + 2) * C;
+                    tc::tma_prefetch_3d(&mv, slice * COLS, h, t2);
+                    if (slice < 2) tc::tma_prefetch_3d(&mk, slice * 64, hk, t2);
+                    else tc::tma_prefetch_3d(&mq, (slice - 2) * 64, hk, t2);
+                    if (slice < 3) tc::bulk_prefetch(far + slice * TRI, TRI);
+                    else tc::bulk_prefetch(far + REC_F, C * 16 + 128);
+                }
             }
-            ++na;
         }
-        if (!ok && lane == 0) {     // give up: what was issued lands before the CTA leaves (at most one
-            bool d = true;          // phase per barrier is open; one that was never issued runs into its limit)
-            for (int b = 0; b < 2; ++b) d = tc::drain_phase(&k_full[b], (kq + 1 - b) / 2) && d;
-            d = tc::drain_phase(&q_full, kq) && tc::drain_phase(&t_full, nt) && tc::drain_phase(&a_full, na) &&
-                tc::drain_phase(&edge, ne) && d;
-            tc::mbar_wait_bounded(&k_full[kq & 1], (kq / 2) & 1, 1u << 16);
-            atomicOr(reinterpret_cast<int*>(a.workspace), d ? tc::ERR_WAIT : tc::ERR_WAIT | tc::ERR_DRAIN);
+        // the last phase of every load has landed before the CTA leaves
+        if (lane == 0) {
+            bool d = tc::drain_phase(&edge, zeroed ? 1 : 0);
+            for (int b = 0; b < 2; ++b) d = tc::drain_phase(&k_full[b], (c + 1 - b) / 2) && d;
+            d = tc::drain_phase(&q_full, c) && tc::drain_phase(&t_full, c) && tc::drain_phase(&a_full, c) &&
+                tc::drain_phase(&v_full, c) && d;
+            if (*abort || !d)
+                atomicOr(reinterpret_cast<int*>(a.workspace), d ? tc::ERR_WAIT : tc::ERR_WAIT | tc::ERR_DRAIN);
         }
-    } else if (warp == 9) {
+    } else if (warp == 13) {
         // ---------------- MMAs: the warp computes together, one lane issues ----------------
-        bool ok = true;
-        const bool one = lane == 0;
+        // Per chunk 48 MMAs of some 70 cycles whatever their N: K S, T R and K^T V'' on the chain
+        // from state to state, Q S and (masked Q K^T) V' in the gaps that the rows' arithmetic leaves.
         const uint32_t tmu = __shfl_sync(~0u, tm, 0), sb = __shfl_sync(~0u, tc::smem_u32(sm), 0);
         const uint32_t id64 = tc::idesc_bf16(128, 64, false, true), id32 = tc::idesc_bf16(128, 32, false, true),
                        idt = tc::idesc_bf16(128, 64, true, true);
@@ -578,56 +608,116 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
         auto rows = [&](uint32_t d, uint64_t ad, uint64_t bd, uint32_t step, uint32_t id, bool acc) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                tc::mma_f16_ss_if(one, d, ad + (((k >> 2) * 16384 + (k & 3) * 32) >> 4), bd + k * (step >> 4), id, acc || k > 0);
+                tc::mma_f16_ss_elect(d, ad + (((k >> 2) * 16384 + (k & 3) * 32) >> 4), bd + k * (step >> 4), id, acc || k > 0);
         };
 #pragma unroll 1
         for (int c = 0; c < nc; ++c) {
+            if (__any_sync(~0u, *abort)) break;
             const uint32_t ph = c & 1, kb = sb + S_K + (c & 1) * TILE;
-            const uint64_t dK = tc::sw128_desc(kb);
-            ok = wait_warp(&k_full[c & 1], (c / 2) & 1, limit, abort) && wait_warp(&s_ready, ph, limit, abort);
-            if (!ok) break;
+            const uint64_t dK = tc::sw128_desc(kb), dKt = tc::sw128_desc_mn(kb, 16384);
+            wait_go(&k_full[c & 1], (c / 2) & 1, limit, abort);
+            wait_go(&s_ready, ph, limit, abort);
+            __syncwarp();
             tc::fence_after_sync();
             rows(tmu + D_KS, dK, dS, 2048, id64, false);
-            tc::mma_commit_if(one, &ks_done);
-            ok = wait_warp(&q_full, ph, limit, abort);
-            if (!ok) break;
-            rows(tmu + D_QS, tc::sw128_desc(sb + S_Q), dS, 2048, id32, false);     // S rounded to bf16: o only
-            tc::mma_commit_if(one, &qs_done);
-            tc::mma_commit_if(one, &q_empty);
-            ok = wait_warp(&t_full, ph, limit, abort) && wait_warp(&r_ready, ph, limit, abort);
-            if (!ok) break;
+            tc::mma_commit_elect(&ks_done);
+            wait_go(&q_full, ph, limit, abort);
+            __syncwarp();
+            rows(tmu + D_QS + 64 * ph, tc::sw128_desc(sb + S_Q), dS, 2048, id64, false);
+            tc::mma_commit_elect(&qs_done);
+            wait_go(&t_full, ph, limit, abort);
+            wait_go(&r_ready, ph, limit, abort);
+            __syncwarp();
             tc::fence_after_sync();
             rows(tmu + D_TR, tc::sw128_desc(sb + S_THI), dR, 2048, id64, false);
             rows(tmu + D_TR, tc::sw128_desc(sb + S_TLO), dR, 2048, id32, true);
-            tc::mma_commit_if(one, &tr_done);
-            tc::mma_commit_if(one, &t_empty);
-            ok = wait_warp(&v_ready, ph, limit, abort);
-            if (!ok) break;
+            tc::mma_commit_elect(&tr_done);
+            wait_go(&a_full, ph, limit, abort);
+            wait_go(&v_ready, ph, limit, abort);
+            __syncwarp();
             tc::fence_after_sync();
-            const uint64_t dKt = tc::sw128_desc_mn(kb, 16384);
 #pragma unroll
             for (int k = 0; k < 8; ++k)                                            // K^T: tokens are the K rows
-                tc::mma_f16_ss_if(one, tmu + D_KV, dKt + k * (2048 >> 4), dR + k * (2048 >> 4), idt, k > 0);
-            tc::mma_commit_if(one, &kv_done);
-            tc::mma_commit_if(one, &k_empty[c & 1]);
-            ok = wait_warp(&a_full, ph, limit, abort);
-            if (!ok) break;
+                tc::mma_f16_ss_elect(tmu + D_KV, dKt + k * (2048 >> 4), dR + k * (2048 >> 4), idt, k > 0);
+            tc::mma_commit_elect(&kv_done);
+            tc::mma_commit_elect(&k_empty[c & 1]);
             rows(tmu + D_AV, tc::sw128_desc(sb + S_A), sw64_desc_mn(sb + S_V), 1024, id32, false);
-            tc::mma_commit_if(one, &av_done);
-            tc::mma_commit_if(one, &a_empty);
-        }
-        if (one) {
-            tc::mma_commit(&drained);
-            const bool d = tc::mbar_wait_bounded(&drained, 0, tc::WAIT_POLLS);
-            if (!ok || !d) atomicOr(reinterpret_cast<int*>(a.workspace), d ? tc::ERR_WAIT : tc::ERR_WAIT | tc::ERR_DRAIN);
+            tc::mma_commit_elect(&av_done);
         }
         __syncwarp();
+        tc::mma_commit_elect(&drained);
+        if (lane == 0) {
+            if (!tc::mbar_wait_bounded(&drained, 0, tc::WAIT_POLLS))
+                atomicOr(reinterpret_cast<int*>(a.workspace), tc::ERR_WAIT | tc::ERR_DRAIN);
+        }
+        __syncwarp();
+    } else if (warp >= 8) {
+        // ---------------- output rows: one token per thread, 32 columns ----------------
+        const int row = tid & 127;
+        const uint32_t tl = tm + ((uint32_t)(warp & 3) << 21);
+        if (nc > 0) {
+            tc::mbar_arrive(&r_ready);
+            tc::mbar_arrive(&v_ready);
+        }
+#pragma unroll 1
+        for (int c = 0; c < nc; ++c) {
+            if (any_of_128(*abort != 0)) break;      // all four warps or none: they share barriers below
+            const uint32_t ph = c & 1;
+            const float fw = __ldg(reinterpret_cast<const float*>(recs + c * rec_step + REC_F + row * 16 + 12));
+            float o[32], x[32];
+            wait_go(&qs_done, ph, limit, abort);
+            __syncwarp();
+            tc::fence_after_sync();
+            tc::tmem_ld32(tl + D_QS + 64 * ph, o);
+            tc::tmem_ld32(tl + D_QS + 64 * ph + 32, x);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = fw * (o[i] + x[i]);                // scale rq e^g (Q S)
+            wait_go(&av_done, ph, limit, abort);
+            __syncwarp();
+            tc::fence_after_sync();
+            tc::tmem_ld32(tl + D_AV, x);
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(sm + S_V + row * 64 + 16 * i) = zero;   // T's zeros again
+            tc::tmem_ld_wait();
+            tc::fence_proxy_async();
+            tc::fence_before_sync();
+            if (c + 1 < nc) tc::mbar_arrive(&r_ready);
+            const bool whole = (c + 1) * C <= T;
+            if (a.o) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] += x[i];
+                if (whole) {
+                    // through shared memory and one TMA store; the last chunk's rows one by one
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) store8_bf16(reinterpret_cast<uint16_t*>(sm + S_O + swz64(row, i)), o + 8 * i);
+                    tc::fence_proxy_async();
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                    if (tid == 256) {
+                        tc::tma_store_3d(&mo, slice * COLS, h, t0 + c * C, sm + S_O);
+                        tc::bulk_commit();
+                        tc::bulk_wait_read();
+                    }
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(sm + S_O + row * 64 + 16 * i) = zero;
+                    tc::fence_proxy_async();
+                } else if (c * C + row < T) {
+                    uint16_t* out = reinterpret_cast<uint16_t*>(a.o) + ((size_t)(t0 + c * C + row) * a.Hv + h) * DH + slice * COLS;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) store8_bf16(out + 8 * i, o + 8 * i);
+                }
+            }
+            if (c + 1 < nc) tc::mbar_arrive(&v_ready);
+            __syncwarp();
+        }
+        if (tid == 256) tc::bulk_wait_all();
     } else {
-        // ---------------- rows: thread (row, w) owns columns 16 w .. 16 w + 15 of its row ----------------
+        // ---------------- state rows: thread (row, w) owns columns 16 w .. 16 w + 15 of its row ----------------
         const int row = tid & 127, w = tid >> 7;
         const int col = slice * COLS + 16 * w;
-        const long base = chunks_before(a, n);
-        const uint32_t tl = tm + ((uint32_t)(warp & 3) << 21);
+        const uint32_t tl = tm + ((uint32_t)(warp & 3) << 21) + 16 * w;
         const size_t sbase = ((size_t)n * a.Hv + h) * (size_t)DH * DH + (size_t)row * DH + col;   // row = key channel
         float S[16];
 #pragma unroll
@@ -635,46 +725,55 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
             const float4 x = a.S0 ? *reinterpret_cast<const float4*>(a.S0 + sbase + i) : make_float4(0.f, 0.f, 0.f, 0.f);
             S[i] = x.x; S[i + 1] = x.y; S[i + 2] = x.z; S[i + 3] = x.w;
         }
-        bool ok = true;
+        // a chunk's factors are fetched behind the chunk before (the proxy fences wait for loads in flight)
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+        float gamma = 0.f;
+        auto fetch = [&](int c) {
+            const uint8_t* rec = recs + c * rec_step;
+            f = __ldg(reinterpret_cast<const float4*>(rec + REC_F + row * 16));
+            gamma = __ldg(reinterpret_cast<const float*>(rec + REC_F + C * 16));
+        };
         if (nc > 0) {
+            fetch(0);
             store_split(sm + S_S, row, w, S);
             tc::fence_proxy_async();
             tc::mbar_arrive(&s_ready);
         }
 #pragma unroll 1
         for (int c = 0; c < nc; ++c) {
+            if (__any_sync(~0u, *abort)) break;
             const uint32_t ph = c & 1;
-            const int t = t0 + c * C + row;                   // row = token
-            const bool live = c * C + row < T;
-            const uint8_t* rec = reinterpret_cast<const uint8_t*>(a.workspace) + WS_HEAD + ((base + c) * a.Hv + h) * (size_t)REC;
-            const float4 f = *reinterpret_cast<const float4*>(rec + REC_F + row * 16);
-            const float gamma = *reinterpret_cast<const float*>(rec + REC_F + C * 16);
-            float v[16];
-            const size_t at = ((size_t)t * a.Hv + h) * DH + col;
-            if (live) {
-                load8_bf16(reinterpret_cast<const uint16_t*>(a.v) + at, v);
-                load8_bf16(reinterpret_cast<const uint16_t*>(a.v) + at + 8, v + 8);
-            }
-            // R = beta (v - e^g rk K S)
-            ok = wait_warp(&ks_done, ph, limit, abort);
-            if (!ok) break;
+            const bool live = c * C + row < T;                // row = token
+            // R = beta (v - e^g rk K S); the values' place is zero again afterwards
+            wait_go(&v_full, ph, limit, abort);
+            __syncwarp();
+            uint4* vp = reinterpret_cast<uint4*>(sm + S_VIN + swz64(row, 2 * w));
+            uint4* vq = reinterpret_cast<uint4*>(sm + S_VIN + swz64(row, 2 * w + 1));
+            const uint4 va = *vp, vc = *vq;
+            *vp = *vq = make_uint4(0, 0, 0, 0);
+            wait_go(&ks_done, ph, limit, abort);
+            __syncwarp();
             tc::fence_after_sync();
             float x[16], y[16];
-            tc::tmem_ld16(tl + D_KS + 16 * w, x);
-            tc::tmem_ld16(tl + D_KS + 32 + 16 * w, y);
+            tc::tmem_ld16(tl + D_KS, x);
+            tc::tmem_ld16(tl + D_KS + 32, y);
             tc::tmem_ld_wait();
+            const uint32_t vr[8] = {va.x, va.y, va.z, va.w, vc.x, vc.y, vc.z, vc.w};
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = live ? f.x * v[i] - f.y * (x[i] + y[i]) : 0.f;
+            for (int i = 0; i < 16; ++i) {
+                const float v = __uint_as_float(i & 1 ? vr[i >> 1] & 0xffff0000u : vr[i >> 1] << 16);
+                x[i] = live ? f.x * v - f.y * (x[i] + y[i]) : 0.f;
+            }
             store_split(sm + S_R, row, w, x);
             tc::fence_proxy_async();
             tc::fence_before_sync();
             tc::mbar_arrive(&r_ready);
             // V' = T R, and V'' = e^{g_C - g} rk V' over R (T R is done with it)
-            ok = wait_warp(&tr_done, ph, limit, abort);
-            if (!ok) break;
+            wait_go(&tr_done, ph, limit, abort);
+            __syncwarp();
             tc::fence_after_sync();
-            tc::tmem_ld16(tl + D_TR + 16 * w, x);
-            tc::tmem_ld16(tl + D_TR + 32 + 16 * w, y);
+            tc::tmem_ld16(tl + D_TR, x);
+            tc::tmem_ld16(tl + D_TR + 32, y);
             tc::tmem_ld_wait();
             uint32_t vb[8];
 #pragma unroll
@@ -686,30 +785,18 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
                 x[i] *= f.z;
                 x[i + 1] *= f.z;
             }
-            {
-                uint8_t* vr = sm + S_V + row * 64;                 // 64-byte rows, pieces swapped by (row / 2) mod 4
-                const int sw = (row >> 1) & 3;
-                *reinterpret_cast<uint4*>(vr + (((2 * w) ^ sw) << 4)) = make_uint4(vb[0], vb[1], vb[2], vb[3]);
-                *reinterpret_cast<uint4*>(vr + (((2 * w + 1) ^ sw) << 4)) = make_uint4(vb[4], vb[5], vb[6], vb[7]);
-            }
+            *reinterpret_cast<uint4*>(sm + S_V + swz64(row, 2 * w)) = make_uint4(vb[0], vb[1], vb[2], vb[3]);
+            *reinterpret_cast<uint4*>(sm + S_V + swz64(row, 2 * w + 1)) = make_uint4(vb[4], vb[5], vb[6], vb[7]);
             store_split(sm + S_R, row, w, x);
             tc::fence_proxy_async();
             tc::fence_before_sync();
             tc::mbar_arrive(&v_ready);
-            float o[16];
-            if (a.o) {                                             // e^g scale rq Q S (the product is long done)
-                ok = wait_warp(&qs_done, ph, limit, abort);
-                if (!ok) break;
-                tc::fence_after_sync();
-                tc::tmem_ld16(tl + D_QS + 16 * w, o);
-                tc::tmem_ld_wait();
-            }
             // S <- e^{g_C} S + K^T V''
-            ok = wait_warp(&kv_done, ph, limit, abort);
-            if (!ok) break;
+            wait_go(&kv_done, ph, limit, abort);
+            __syncwarp();
             tc::fence_after_sync();
-            tc::tmem_ld16(tl + D_KV + 16 * w, x);
-            tc::tmem_ld16(tl + D_KV + 32 + 16 * w, y);
+            tc::tmem_ld16(tl + D_KV, x);
+            tc::tmem_ld16(tl + D_KV + 32, y);
             tc::tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 16; ++i) S[i] = gamma * S[i] + (x[i] + y[i]);
@@ -718,28 +805,10 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
                 tc::fence_proxy_async();
                 tc::fence_before_sync();
                 tc::mbar_arrive(&s_ready);
-            }
-            ok = wait_warp(&av_done, ph, limit, abort);
-            if (!ok) break;
-            tc::fence_after_sync();
-            {
-                uint8_t* vr = sm + S_V + row * 64 + 32 * w;        // the zero half-slab is one again
-                *reinterpret_cast<uint4*>(vr) = make_uint4(0, 0, 0, 0);
-                *reinterpret_cast<uint4*>(vr + 16) = make_uint4(0, 0, 0, 0);
-            }
-            if (a.o) {
-                tc::tmem_ld16(tl + D_AV + 16 * w, x);
-                tc::tmem_ld_wait();
-                if (live) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] = f.w * o[i] + x[i];
-                    store8_bf16(reinterpret_cast<uint16_t*>(a.o) + at, o);
-                    store8_bf16(reinterpret_cast<uint16_t*>(a.o) + at + 8, o + 8);
-                }
-                __syncwarp();
+                fetch(c + 1);
             }
         }
-        if (a.S_T && ok) {
+        if (a.S_T) {
 #pragma unroll
             for (int i = 0; i < 16; i += 4)
                 *reinterpret_cast<float4*>(a.S_T + sbase + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
@@ -747,7 +816,7 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
     }
     tc::fence_before_sync();
     __syncthreads();
-    if (warp == 9) tc::tmem_dealloc(tm, 256);
+    if (warp == 13) tc::tmem_dealloc(tm, D_COLS);
 }
 
 // ---------------------------------------------------------------------------
@@ -768,10 +837,12 @@ cudaError_t launch_chunked(const kda_gdn_prefill_args& a, cudaStream_t s) {
     p.chunks = count_chunks(a);
     p.wait_limit = wait_limit();
     cudaError_t e = cudaMemsetAsync(a.workspace, 0, 4, s);
-    CUtensorMap mq = {}, mk = {};
+    CUtensorMap mq = {}, mk = {}, mv = {}, mo = {};
     if (p.chunks > 0) {
         if (e == cudaSuccess) e = make_map_heads(&mq, a.q, DH, a.Hk, a.T_total, (uint64_t)a.Hk * DH, 1, C);
         if (e == cudaSuccess) e = make_map_heads(&mk, a.k, DH, a.Hk, a.T_total, (uint64_t)a.Hk * DH, 1, C);
+        if (e == cudaSuccess) e = make_map_heads(&mv, a.v, DH, a.Hv, a.T_total, (uint64_t)a.Hv * DH, 1, C, COLS);
+        if (e == cudaSuccess && a.o) e = make_map_heads(&mo, a.o, DH, a.Hv, a.T_total, (uint64_t)a.Hv * DH, 1, C, COLS);
         if (e == cudaSuccess) e = cudaFuncSetAttribute(gdn_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, P_SMEM);
         if (e != cudaSuccess) return e;
         gdn_prep_kernel<<<(unsigned)(p.chunks * a.Hk), PT, P_SMEM, s>>>(p, mq, mk);
@@ -780,7 +851,7 @@ cudaError_t launch_chunked(const kda_gdn_prefill_args& a, cudaStream_t s) {
     }
     if (e == cudaSuccess) e = cudaFuncSetAttribute(gdn_scan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S_SMEM);
     if (e != cudaSuccess) return e;
-    gdn_scan_kernel<<<(unsigned)((long)a.num_seqs * a.Hv * (DH / COLS)), ST, S_SMEM, s>>>(p, mq, mk);
+    gdn_scan_kernel<<<(unsigned)((long)a.num_seqs * a.Hv * (DH / COLS)), ST, S_SMEM, s>>>(p, mq, mk, mv, mo);
     count_launches(1);
     return cudaGetLastError();
 }

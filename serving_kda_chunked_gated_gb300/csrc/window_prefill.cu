@@ -284,8 +284,7 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
             const int t = warp - 13;
             uint32_t rd = 0, nu = 0, np = 0;       // rounds, units, softmax steps
             bool ok = true;
-            const bool one = lane == 0;
-            const uint32_t ra = uniform(tc::smem_u32(ring)), tmu = uniform(tm);
+                const uint32_t ra = uniform(tc::smem_u32(ring)), tmu = uniform(tm);
             const uint64_t qd = tc::sw128_desc(uniform(tc::smem_u32(sq)) + t * L::QB);
             auto qk = [&](uint32_t slot, int width) {
                 const uint32_t id = tc::idesc_bf16(128, width, false, false, p.neg != 0);
@@ -293,7 +292,7 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
 #pragma unroll 1
                 for (int k = 0; k < D / 16; ++k) {
                     const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;      // descriptors count 16 bytes
-                    tc::mma_f16_ss_if(one, tmu + t * 128, qd + off, kd + off, id, k > 0);
+                    tc::mma_f16_ss_elect(tmu + t * 128, qd + off, kd + off, id, k > 0);
                 }
             };
             auto pv = [&](uint32_t slot, int k0, int k1, bool first) {
@@ -301,7 +300,7 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
                 const uint64_t vd = tc::sw128_desc_mn(ra + slot * L::SB, 16384);
 #pragma unroll 1
                 for (int k = k0; k < k1; ++k)
-                    tc::mma_f16_ts_if(one, tmu + 256 + t * D, tmu + t * 128 + k * 8, vd + k * (2048 >> 4), id,
+                    tc::mma_f16_ts_elect(tmu + 256 + t * D, tmu + t * 128 + k * 8, vd + k * (2048 >> 4), id,
                                       !(first && k == 0));
             };
             // widths of a unit's tiles, uniform over the warp
@@ -328,9 +327,9 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
                 if (ok) {
                     x = tiles_of(0);
                     qk(0, width_of(x, 0));
-                    tc::mma_commit_if(one, &s_full[t]);
-                    tc::mma_commit_if(one, &empty[0]);
-                    if (x.ntiles == 1) tc::mma_commit_if(one, &q_empty);
+                    tc::mma_commit_elect(&s_full[t]);
+                    tc::mma_commit_elect(&empty[0]);
+                    if (x.ntiles == 1) tc::mma_commit_elect(&q_empty);
                 }
                 rd = 1;
             }
@@ -354,7 +353,7 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
                     }
                     if (!ok) break;
                     if (last) {
-                        tc::mma_commit_if(one, &o_full[t]);
+                        tc::mma_commit_elect(&o_full[t]);
                         if (next_unit) {
                             ok = wait_warp(&u_full[(nu + 1) % UNITS], ((nu + 1) / UNITS) & 1, limit, abort) &&
                                  wait_warp(&q_full, (nu + 1) & 1, limit, abort);
@@ -364,17 +363,18 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
                     }
                     if (more) {
                         qk(ks, last ? width_of(y, 0) : width_of(x, i + 1));
-                        tc::mma_commit_if(one, &s_full[t]);
+                        tc::mma_commit_elect(&s_full[t]);
                     }
-                    tc::mma_commit_if(one, &empty[rd % ROUNDS]);
+                    tc::mma_commit_elect(&empty[rd % ROUNDS]);
                     // the S issued in this round was a unit's last: its Q may be overwritten
-                    if (last ? more && y.ntiles == 1 : i + 2 == x.ntiles) tc::mma_commit_if(one, &q_empty);
+                    if (last ? more && y.ntiles == 1 : i + 2 == x.ntiles) tc::mma_commit_elect(&q_empty);
                 }
                 x = y;
             }
             // everything issued has finished before TMEM and shared memory are given back
-            if (one) {
-                tc::mma_commit(&drained);
+            __syncwarp();
+            tc::mma_commit_elect(&drained);
+            if (lane == 0) {
                 const bool d = tc::mbar_wait_bounded(&drained, 0, tc::WAIT_POLLS);
                 if (!ok || !d) atomicOr(&g_window_error, d ? tc::ERR_WAIT : tc::ERR_WAIT | tc::ERR_DRAIN);
             }
