@@ -526,30 +526,35 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
 
     if (warp == 12) {
         // ---------------- loads ----------------
-        int c = 0;
-        bool zeroed = false;
-        for (; c < nc; ++c) {
+        // Stops at a wait that gave up: arming a barrier whose last phase is open is not defined.
+        auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+            wait_go(bar, parity, limit, abort);
+            return !__any_sync(~0u, *abort);
+        };
+        uint32_t nk0 = 0, nk1 = 0, nq = 0, nt = 0, na = 0, ne = 0;    // phases begun per barrier
+        for (int c = 0; c < nc; ++c) {
             if (__any_sync(~0u, *abort)) break;
             const uint8_t* rec = recs + c * rec_step;
             const int b = c & 1, left = T - c * C;
             uint8_t* kt = sm + S_K + b * TILE;
-            if (c >= 2) wait_go(&k_empty[b], (c / 2 - 1) & 1, limit, abort);
+            if (c >= 2 && !wait_all(&k_empty[b], (c / 2 - 1) & 1)) break;
             const bool zero = left < C;                  // rows of the next sequence: 0 x NaN
             uint64_t* bar = zero ? &edge : &k_full[b];
-            __syncwarp();
             if (lane == 0) {
                 tc::mbar_arrive_expect_tx(bar, TILE);
                 for (int s = 0; s < 2; ++s) tc::tma_load_3d(kt + s * 16384, &mk, s * 64, hk, t0 + c * C, bar);
             }
-            if (c >= 1) wait_go(&qs_done, (c - 1) & 1, limit, abort);
-            __syncwarp();
+            if (zero) ++ne;
+            else if (b) ++nk1;
+            else ++nk0;
+            if (c >= 1 && !wait_all(&qs_done, (c - 1) & 1)) break;
             if (lane == 0) {
                 tc::mbar_arrive_expect_tx(&q_full, TILE);
                 for (int s = 0; s < 2; ++s) tc::tma_load_3d(sm + S_Q + s * 16384, &mq, s * 64, hk, t0 + c * C, &q_full);
             }
+            ++nq;
             if (zero) {
-                zeroed = true;
-                wait_go(&edge, 0, limit, abort);
+                if (!wait_all(&edge, 0)) break;
                 for (int e = lane; e < (C - left) * 16; e += 32) {
                     const int r = left + (e >> 4), q = e & 15;
                     *reinterpret_cast<uint4*>(kt + (q >> 3) * 16384 + r * 128 + (q & 7) * 16) = make_uint4(0, 0, 0, 0);
@@ -557,9 +562,10 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
                 tc::fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&k_full[b]);
+                if (b) ++nk1;
+                else ++nk0;
             }
-            if (c >= 1) wait_go(&tr_done, (c - 1) & 1, limit, abort);
-            __syncwarp();
+            if (c >= 1 && !wait_all(&tr_done, (c - 1) & 1)) break;
             if (lane == 0) {
                 tc::mbar_arrive_expect_tx(&v_full, C * COLS * 2);
                 tc::tma_load_3d(sm + S_VIN, &mv, slice * COLS, h, t0 + c * C, &v_full);
@@ -569,8 +575,8 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
                 tc::bulk_load(sm + S_TLO, rec + REC_TLO, 16384, &t_full);
                 tc::bulk_load(sm + S_TLO + 16384 + 8192, rec + REC_TLO + 16384, 8192, &t_full);
             }
-            if (c >= 1) wait_go(&av_done, (c - 1) & 1, limit, abort);
-            __syncwarp();
+            ++nt;
+            if (c >= 1 && !wait_all(&av_done, (c - 1) & 1)) break;
             if (lane == 0) {
                 tc::mbar_arrive_expect_tx(&a_full, TRI);
                 tc::bulk_load(sm + S_A, rec + REC_A, 16384, &a_full);
@@ -586,13 +592,13 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
                     else tc::bulk_prefetch(far + REC_F, C * 16 + 128);
                 }
             }
+            ++na;
         }
         // the last phase of every load has landed before the CTA leaves
         if (lane == 0) {
-            bool d = tc::drain_phase(&edge, zeroed ? 1 : 0);
-            for (int b = 0; b < 2; ++b) d = tc::drain_phase(&k_full[b], (c + 1 - b) / 2) && d;
-            d = tc::drain_phase(&q_full, c) && tc::drain_phase(&t_full, c) && tc::drain_phase(&a_full, c) &&
-                tc::drain_phase(&v_full, c) && d;
+            const bool d = tc::drain_phase(&edge, ne) && tc::drain_phase(&k_full[0], nk0) && tc::drain_phase(&k_full[1], nk1) &&
+                           tc::drain_phase(&q_full, nq) && tc::drain_phase(&t_full, nt) && tc::drain_phase(&v_full, nt) &&
+                           tc::drain_phase(&a_full, na);
             if (*abort || !d)
                 atomicOr(reinterpret_cast<int*>(a.workspace), d ? tc::ERR_WAIT : tc::ERR_WAIT | tc::ERR_DRAIN);
         }
@@ -665,7 +671,9 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
             const uint32_t ph = c & 1;
             const float fw = __ldg(reinterpret_cast<const float*>(recs + c * rec_step + REC_F + row * 16 + 12));
             float o[32], x[32];
-            wait_go(&qs_done, ph, limit, abort);
+            // A V' is the chunk's last product, and the next one waits for these rows: a barrier that
+            // could run two phases ahead of its reader (that of Q S) is not waited on here
+            wait_go(&av_done, ph, limit, abort);
             __syncwarp();
             tc::fence_after_sync();
             tc::tmem_ld32(tl + D_QS + 64 * ph, o);
@@ -673,9 +681,6 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
             tc::tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = fw * (o[i] + x[i]);                // scale rq e^g (Q S)
-            wait_go(&av_done, ph, limit, abort);
-            __syncwarp();
-            tc::fence_after_sync();
             tc::tmem_ld32(tl + D_AV, x);
             const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll

@@ -208,7 +208,7 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
         if (warp == 12) {
             // ---------------- loads: Q of a unit, then K and V tiles through the ring ----------------
             uint32_t it = 0, edges = 0, nu = 0, nq = 0;     // items, zeroed tiles, units, Q loads so far
-            bool ok = true;
+            bool ok = true, direct = true;         // direct: the last item counts on its round's barrier
             for (long u = blockIdx.x; u < p.units && ok; u += gridDim.x, ++nu) {
                 const Unit x = unit_at(p, u);
                 for (int i = 0; i < x.ntiles && ok; ++i) {
@@ -246,6 +246,7 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
                                 tc::tma_load_3d(dst + s * 16384, kv ? &mv : &mk, s * 64, x.hk, x.k0 + j0, bar);
                         }
                         ++it;
+                        direct = !zero;
                         if (zero) {
                             ok = wait_warp(&edge, edges & 1, limit, abort);
                             ++edges;
@@ -271,7 +272,7 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
                 const uint32_t whole = (it + 1) >> 1;          // rounds 0 .. whole - 1 have both halves
                 for (uint32_t r = whole > ROUNDS ? whole - ROUNDS : 0; r < whole; ++r)
                     d = tc::mbar_wait_bounded(&full[r % ROUNDS], (r / ROUNDS) & 1, tc::WAIT_POLLS) && d;
-                if (it > 0 && (it & 1) == 0) {                   // values without their keys: supply the arrival
+                if (it > 0 && (it & 1) == 0 && direct) {         // values without their keys: supply the arrival
                     tc::mbar_arrive(&full[whole % ROUNDS]);
                     d = tc::mbar_wait_bounded(&full[whole % ROUNDS], (whole / ROUNDS) & 1, tc::WAIT_POLLS) && d;
                 }
