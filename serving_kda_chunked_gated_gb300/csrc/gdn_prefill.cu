@@ -452,8 +452,8 @@ KDA_DEV uint64_t sw64_desc_mn(uint32_t addr) {
 KDA_DEV uint32_t swz64(int r, int c) { return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4)); }
 
 // A wait that gives up by raising *abort and going on: everything behind it stays within
-// the CTA's own buffers and rows, and the roles leave at the top of their next chunk.  (A
-// vote in every wait would cost the serial chain some 50 cycles each.)
+// the CTA's own buffers and rows, later waits return soon, and the roles look at *abort
+// every eighth chunk (a vote in every wait would cost the serial chain some 50 cycles each).
 KDA_DEV void wait_go(uint64_t* bar, uint32_t parity, uint32_t limit, volatile int* abort) {
     if (limit && tc::mbar_try_wait(bar, parity)) return;
     tc::mbar_wait_role(bar, parity, limit, abort);
@@ -618,7 +618,7 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
         };
 #pragma unroll 1
         for (int c = 0; c < nc; ++c) {
-            if (__any_sync(~0u, *abort)) break;
+            if ((c & 7) == 7 && __any_sync(~0u, *abort)) break;
             const uint32_t ph = c & 1, kb = sb + S_K + (c & 1) * TILE;
             const uint64_t dK = tc::sw128_desc(kb), dKt = tc::sw128_desc_mn(kb, 16384);
             wait_go(&k_full[c & 1], (c / 2) & 1, limit, abort);
@@ -667,7 +667,7 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
         }
 #pragma unroll 1
         for (int c = 0; c < nc; ++c) {
-            if (any_of_128(*abort != 0)) break;      // all four warps or none: they share barriers below
+            if ((c & 7) == 7 && any_of_128(*abort != 0)) break;    // all four warps or none: they share barriers
             const uint32_t ph = c & 1;
             const float fw = __ldg(reinterpret_cast<const float*>(recs + c * rec_step + REC_F + row * 16 + 12));
             float o[32], x[32];
@@ -746,7 +746,7 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
         }
 #pragma unroll 1
         for (int c = 0; c < nc; ++c) {
-            if (__any_sync(~0u, *abort)) break;
+            if ((c & 7) == 7 && __any_sync(~0u, *abort)) break;
             const uint32_t ph = c & 1;
             const bool live = c * C + row < T;                // row = token
             // R = beta (v - e^g rk K S); the values' place is zero again afterwards
