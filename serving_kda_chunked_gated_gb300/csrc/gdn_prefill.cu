@@ -616,39 +616,48 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
             for (int k = 0; k < 8; ++k)
                 tc::mma_f16_ss_elect(d, ad + (((k >> 2) * 16384 + (k & 3) * 32) >> 4), bd + k * (step >> 4), id, acc || k > 0);
         };
+        // Turn i: K^T V'' and (masked Q K^T) V' of chunk i - 1, then K S, Q S and T R of chunk i.  The
+        // way back to the loop's top (some 500 cycles of instruction fetch) so falls into the
+        // wait for V'', not between a state and the next K S.
 #pragma unroll 1
-        for (int c = 0; c < nc; ++c) {
-            if ((c & 7) == 7 && __any_sync(~0u, *abort)) break;
-            const uint32_t ph = c & 1, kb = sb + S_K + (c & 1) * TILE;
-            const uint64_t dK = tc::sw128_desc(kb), dKt = tc::sw128_desc_mn(kb, 16384);
-            wait_go(&k_full[c & 1], (c / 2) & 1, limit, abort);
-            wait_go(&s_ready, ph, limit, abort);
-            __syncwarp();
-            tc::fence_after_sync();
-            rows(tmu + D_KS, dK, dS, 2048, id64, false);
-            tc::mma_commit_elect(&ks_done);
-            wait_go(&q_full, ph, limit, abort);
-            __syncwarp();
-            rows(tmu + D_QS + 64 * ph, tc::sw128_desc(sb + S_Q), dS, 2048, id64, false);
-            tc::mma_commit_elect(&qs_done);
-            wait_go(&t_full, ph, limit, abort);
-            wait_go(&r_ready, ph, limit, abort);
-            __syncwarp();
-            tc::fence_after_sync();
-            rows(tmu + D_TR, tc::sw128_desc(sb + S_THI), dR, 2048, id64, false);
-            rows(tmu + D_TR, tc::sw128_desc(sb + S_TLO), dR, 2048, id32, true);
-            tc::mma_commit_elect(&tr_done);
-            wait_go(&a_full, ph, limit, abort);
-            wait_go(&v_ready, ph, limit, abort);
-            __syncwarp();
-            tc::fence_after_sync();
+        for (int i = 0; i <= nc; ++i) {
+            if ((i & 7) == 7 && __any_sync(~0u, *abort)) break;
+            if (i > 0) {
+                const uint32_t ph = (i - 1) & 1;
+                const uint64_t dKt = tc::sw128_desc_mn(sb + S_K + ph * TILE, 16384);
+                wait_go(&a_full, ph, limit, abort);
+                wait_go(&v_ready, ph, limit, abort);
+                __syncwarp();
+                tc::fence_after_sync();
 #pragma unroll
-            for (int k = 0; k < 8; ++k)                                            // K^T: tokens are the K rows
-                tc::mma_f16_ss_elect(tmu + D_KV, dKt + k * (2048 >> 4), dR + k * (2048 >> 4), idt, k > 0);
-            tc::mma_commit_elect(&kv_done);
-            tc::mma_commit_elect(&k_empty[c & 1]);
-            rows(tmu + D_AV, tc::sw128_desc(sb + S_A), sw64_desc_mn(sb + S_V), 1024, id32, false);
-            tc::mma_commit_elect(&av_done);
+                for (int k = 0; k < 8; ++k)                                        // K^T: tokens are the K rows
+                    tc::mma_f16_ss_elect(tmu + D_KV, dKt + k * (2048 >> 4), dR + k * (2048 >> 4), idt, k > 0);
+                tc::mma_commit_elect(&kv_done);
+                tc::mma_commit_elect(&k_empty[ph]);
+                rows(tmu + D_AV, tc::sw128_desc(sb + S_A), sw64_desc_mn(sb + S_V), 1024, id32, false);
+                tc::mma_commit_elect(&av_done);
+            }
+            if (i < nc) {
+                const uint32_t ph = i & 1;
+                const uint64_t dK = tc::sw128_desc(sb + S_K + ph * TILE);
+                wait_go(&k_full[ph], (i / 2) & 1, limit, abort);
+                wait_go(&s_ready, ph, limit, abort);
+                __syncwarp();
+                tc::fence_after_sync();
+                rows(tmu + D_KS, dK, dS, 2048, id64, false);
+                tc::mma_commit_elect(&ks_done);
+                wait_go(&q_full, ph, limit, abort);
+                __syncwarp();
+                rows(tmu + D_QS + 64 * ph, tc::sw128_desc(sb + S_Q), dS, 2048, id64, false);
+                tc::mma_commit_elect(&qs_done);
+                wait_go(&t_full, ph, limit, abort);
+                wait_go(&r_ready, ph, limit, abort);
+                __syncwarp();
+                tc::fence_after_sync();
+                rows(tmu + D_TR, tc::sw128_desc(sb + S_THI), dR, 2048, id64, false);
+                rows(tmu + D_TR, tc::sw128_desc(sb + S_TLO), dR, 2048, id32, true);
+                tc::mma_commit_elect(&tr_done);
+            }
         }
         __syncwarp();
         tc::mma_commit_elect(&drained);
@@ -738,18 +747,11 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
             f = __ldg(reinterpret_cast<const float4*>(rec + REC_F + row * 16));
             gamma = __ldg(reinterpret_cast<const float*>(rec + REC_F + C * 16));
         };
-        if (nc > 0) {
-            fetch(0);
-            store_split(sm + S_S, row, w, S);
-            tc::fence_proxy_async();
-            tc::mbar_arrive(&s_ready);
-        }
-#pragma unroll 1
-        for (int c = 0; c < nc; ++c) {
-            if ((c & 7) == 7 && __any_sync(~0u, *abort)) break;
+        // R = beta (v - e^g rk K S) of chunk c; the values' place is zero again afterwards
+        float x[16], y[16];
+        auto form_r = [&](int c) {
             const uint32_t ph = c & 1;
             const bool live = c * C + row < T;                // row = token
-            // R = beta (v - e^g rk K S); the values' place is zero again afterwards
             wait_go(&v_full, ph, limit, abort);
             __syncwarp();
             uint4* vp = reinterpret_cast<uint4*>(sm + S_VIN + swz64(row, 2 * w));
@@ -759,7 +761,6 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
             wait_go(&ks_done, ph, limit, abort);
             __syncwarp();
             tc::fence_after_sync();
-            float x[16], y[16];
             tc::tmem_ld16(tl + D_KS, x);
             tc::tmem_ld16(tl + D_KS + 32, y);
             tc::tmem_ld_wait();
@@ -773,44 +774,58 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
             tc::fence_proxy_async();
             tc::fence_before_sync();
             tc::mbar_arrive(&r_ready);
-            // V' = T R, and V'' = e^{g_C - g} rk V' over R (T R is done with it)
-            wait_go(&tr_done, ph, limit, abort);
-            __syncwarp();
-            tc::fence_after_sync();
-            tc::tmem_ld16(tl + D_TR, x);
-            tc::tmem_ld16(tl + D_TR + 32, y);
-            tc::tmem_ld_wait();
-            uint32_t vb[8];
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-                x[i] = live ? x[i] + y[i] : 0.f;
-                x[i + 1] = live ? x[i + 1] + y[i + 1] : 0.f;
-                const __nv_bfloat162 hh = __floats2bfloat162_rn(x[i], x[i + 1]);          // for o only
-                vb[i >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
-                x[i] *= f.z;
-                x[i + 1] *= f.z;
-            }
-            *reinterpret_cast<uint4*>(sm + S_V + swz64(row, 2 * w)) = make_uint4(vb[0], vb[1], vb[2], vb[3]);
-            *reinterpret_cast<uint4*>(sm + S_V + swz64(row, 2 * w + 1)) = make_uint4(vb[4], vb[5], vb[6], vb[7]);
-            store_split(sm + S_R, row, w, x);
+        };
+        auto give_s = [&] {
+            store_split(sm + S_S, row, w, S);
             tc::fence_proxy_async();
             tc::fence_before_sync();
-            tc::mbar_arrive(&v_ready);
-            // S <- e^{g_C} S + K^T V''
-            wait_go(&kv_done, ph, limit, abort);
-            __syncwarp();
-            tc::fence_after_sync();
-            tc::tmem_ld16(tl + D_KV, x);
-            tc::tmem_ld16(tl + D_KV + 32, y);
-            tc::tmem_ld_wait();
+            tc::mbar_arrive(&s_ready);
+        };
+        // The loop turns over while T R runs: from R of one chunk to R of the next.
+#pragma unroll 1
+        for (int i = 0; i <= nc; ++i) {
+            if ((i & 7) == 7 && __any_sync(~0u, *abort)) break;
+            if (i > 0) {
+                const int c = i - 1;
+                const uint32_t ph = c & 1;
+                const bool live = c * C + row < T;
+                // V' = T R, and V'' = e^{g_C - g} rk V' over R (T R is done with it)
+                wait_go(&tr_done, ph, limit, abort);
+                __syncwarp();
+                tc::fence_after_sync();
+                tc::tmem_ld16(tl + D_TR, x);
+                tc::tmem_ld16(tl + D_TR + 32, y);
+                tc::tmem_ld_wait();
+                uint32_t vb[8];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) S[i] = gamma * S[i] + (x[i] + y[i]);
-            if (c + 1 < nc) {
-                store_split(sm + S_S, row, w, S);
+                for (int e = 0; e < 16; e += 2) {
+                    x[e] = live ? x[e] + y[e] : 0.f;
+                    x[e + 1] = live ? x[e + 1] + y[e + 1] : 0.f;
+                    const __nv_bfloat162 hh = __floats2bfloat162_rn(x[e], x[e + 1]);      // for o only
+                    vb[e >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
+                    x[e] *= f.z;
+                    x[e + 1] *= f.z;
+                }
+                *reinterpret_cast<uint4*>(sm + S_V + swz64(row, 2 * w)) = make_uint4(vb[0], vb[1], vb[2], vb[3]);
+                *reinterpret_cast<uint4*>(sm + S_V + swz64(row, 2 * w + 1)) = make_uint4(vb[4], vb[5], vb[6], vb[7]);
+                store_split(sm + S_R, row, w, x);
                 tc::fence_proxy_async();
                 tc::fence_before_sync();
-                tc::mbar_arrive(&s_ready);
-                fetch(c + 1);
+                tc::mbar_arrive(&v_ready);
+                // S <- e^{g_C} S + K^T V''
+                wait_go(&kv_done, ph, limit, abort);
+                __syncwarp();
+                tc::fence_after_sync();
+                tc::tmem_ld16(tl + D_KV, x);
+                tc::tmem_ld16(tl + D_KV + 32, y);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) S[e] = gamma * S[e] + (x[e] + y[e]);
+            }
+            if (i < nc) {
+                give_s();
+                fetch(i);
+                form_r(i);
             }
         }
         if (a.S_T) {
