@@ -16,9 +16,8 @@
 //
 // prep: one CTA per (chunk, key head) forms K K^T and Q K^T once for all value heads of
 // the key head, then per value head A, its inverse (16 x 16 blocks by substitution, merged
-// by [[X, 0], [B, Y]]^-1 = [[X^-1, 0], [-Y^-1 B X^-1, Y^-1]] on mma.sync with three tf32
-// products for each float32 one), and writes a record: T as two bf16 parts, the masked and
-// scaled Q K^T in bf16, the tokens' factors.
+// by [[X, 0], [B, Z]]^-1 = [[X^-1, 0], [-Z^-1 B X^-1, Z^-1]]), and writes a record: T as two
+// bf16 parts, the masked and scaled Q K^T in bf16, the tokens' factors.
 // scan: one CTA per (sequence, value head, 32 value columns) walks the chunks.  Tokens (or
 // key channels) are TMEM lanes, the 32 columns of an operand's hi and lo parts one
 // 128-byte row of 64 MN-major elements: one N = 64 MMA forms both products.
@@ -100,11 +99,12 @@ KDA_DEV void split2(float x0, float x1, uint32_t* hi, uint32_t* lo) {
 // ---------------------------------------------------------------------------
 // prep
 // ---------------------------------------------------------------------------
-constexpr int PT = 256;                       // threads
-constexpr int XS = 136;                       // row stride of the inverse's float matrix (8 banks apart)
-constexpr int YS = 72;
-constexpr int P_X = 0, P_Y = P_X + C * XS * 4, P_W = P_Y + 64 * YS * 4, P_END = P_W + 8 * C * 4;
-constexpr int P_SMEM = (P_END > 2 * TILE ? P_END : 2 * TILE) + 1024;
+constexpr int PT = 512;                       // threads
+constexpr int XS = 140;                       // row stride of the inverse's float matrix
+constexpr int YS = 68;                        // and of the merges' intermediate one
+constexpr int P_X = 0, P_Y = P_X + C * XS * 4, P_W = P_Y + TRI, P_END = P_W + 8 * C * 4;
+constexpr int P_SMEM = P_END + 1024;
+static_assert(64 * YS * 4 <= TRI && 2 * TILE <= P_Y, "the intermediate matrix shares the record part's place, the tiles the inverse's");
 
 // x = hi + lo with hi a tf32 value; what the tensor core drops of lo is below 2^-21 of x
 KDA_DEV void split_tf32(float x, float* hi, float* lo) {
@@ -112,40 +112,45 @@ KDA_DEV void split_tf32(float x, float* hi, float* lo) {
     *lo = x - *hi;
 }
 
-// acc (16 x 16) += L[16 x 16 nk] R[16 nk x 16] from row-major float matrices in shared
-// memory: float32 operands as two tf32 parts each, the product of the low parts left out.
-// (Two bf16 parts would leave 2^-17, which the inverse of strongly correlated keys
-// amplifies to 2e-5 of the state.)  Within each step of 8, k is taken in the order 0, 2, 4,
-// 6, 1, 3, 5, 7, so that a lane's two values of A are neighbours.
-KDA_DEV void block_product(float (*acc)[4], const float* Lm, int ls, const float* Rm, int rs, int nk, int lane) {
+// out (16 x 16, row-major with stride os) = sign L[16 x 8 nk] R[8 nk x 16], row-major float
+// matrices in shared memory, by one warp: float32 operands as two tf32 parts each, the product
+// of the low parts left out.  (Two bf16 parts would leave 2^-17, which the inverse of strongly
+// correlated keys amplifies to 2e-5 of the state; as float32 FMAs the tiles are bound by
+// shared-memory reads, 3700 cycles for the 64 x 64 product against 1100 here.)  Within each
+// step of 8, k is taken in the order 0, 2, 4, 6, 1, 3, 5, 7, so that a lane's two values of L
+// are neighbours.  Six independent accumulators: the steps wait for nothing but their loads.
+KDA_DEV void tile_product(float* out, int os, float sign, const float* Lm, int ls, const float* Rm, int rs, int nk, int lane) {
     const int g = lane >> 2, t = lane & 3;
+    float acc[2][3][4] = {};
+    const float* l0 = Lm + g * ls + 2 * t;
+    const float* r0 = Rm + 2 * t * rs + g;
 #pragma unroll 2
-    for (int k = 0; k < 2 * nk; ++k) {
+    for (int k = 0; k < nk; ++k) {
         float ah[4], al[4];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            const float2 x = *reinterpret_cast<const float2*>(Lm + (g + q * 8) * ls + k * 8 + 2 * t);
+            const float2 x = *reinterpret_cast<const float2*>(l0 + q * 8 * ls + k * 8);
             split_tf32(x.x, &ah[q], &al[q]);
             split_tf32(x.y, &ah[q + 2], &al[q + 2]);
         }
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
             float bh[2], bl[2];
-            const float* r = Rm + (k * 8 + 2 * t) * rs + n * 8 + g;
+            const float* r = r0 + k * 8 * rs + n * 8;
             split_tf32(r[0], &bh[0], &bl[0]);
             split_tf32(r[rs], &bh[1], &bl[1]);
-            tc::mma_m16n8k8_tf32(acc[n], ah, bh);
-            tc::mma_m16n8k8_tf32(acc[n], al, bh);
-            tc::mma_m16n8k8_tf32(acc[n], ah, bl);
+            tc::mma_m16n8k8_tf32(acc[n][0], ah, bh);
+            tc::mma_m16n8k8_tf32(acc[n][1], al, bh);
+            tc::mma_m16n8k8_tf32(acc[n][2], ah, bl);
         }
     }
-}
-KDA_DEV void block_store(const float (*acc)[4], float* M, int ms, float sign, int lane) {
-    const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-        *reinterpret_cast<float2*>(M + g * ms + n * 8 + 2 * t) = make_float2(sign * acc[n][0], sign * acc[n][1]);
-        *reinterpret_cast<float2*>(M + (g + 8) * ms + n * 8 + 2 * t) = make_float2(sign * acc[n][2], sign * acc[n][3]);
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = sign * (acc[n][0][i] + (acc[n][1][i] + acc[n][2][i]));
+        *reinterpret_cast<float2*>(out + g * os + n * 8 + 2 * t) = make_float2(v[0], v[1]);
+        *reinterpret_cast<float2*>(out + (g + 8) * os + n * 8 + 2 * t) = make_float2(v[2], v[3]);
     }
 }
 
@@ -155,25 +160,41 @@ gdn_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
     __shared__ __align__(8) uint64_t loaded, done;
     __shared__ uint32_t s_tmem;
     __shared__ int s_ok;
-    __shared__ float s_rk[C], s_rq[C], s_beta[C];
+    __shared__ float s_rk[C], s_rq[C], s_beta[C], s_part[4][C];
     __shared__ long long s_g[C], s_wsum[4];
     const kda_gdn_prefill_args& a = p.a;
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int row = tid & 127, half = tid >> 7;             // TMEM lane and column half of this thread
-    const int hk = blockIdx.x % a.Hk;
+    const int row = tid & 127, quarter = tid >> 7;          // TMEM lane of this thread, its share of the columns
+    const int hk = blockIdx.x % a.Hk, rep = a.Hv / a.Hk;
     const long idx = blockIdx.x / a.Hk;
     int n, ch;
     chunk_at(a, idx, &n, &ch);
     const int t0 = a.cu_seqlens[n] + ch * C, len = min(C, a.cu_seqlens[n + 1] - t0);
+    const bool live = row < len;
 
     if (tid == 0) {
         tc::mbar_init(&loaded, 1);
         tc::mbar_init(&done, 1);
         tc::mbar_fence_init();
         s_ok = 1;
+        tc::mbar_arrive_expect_tx(&loaded, 2 * TILE);
+        for (int s = 0; s < 2; ++s) {
+            tc::tma_load_3d(sm + s * 16384, &mk, s * 64, hk, t0, &loaded);
+            tc::tma_load_3d(sm + TILE + s * 16384, &mq, s * 64, hk, t0, &loaded);
+        }
     }
-    if (warp == 0) {
+    // a head's decay logit and write strength are fetched a head ahead
+    float zn = 0.f, bn = 0.f;
+    auto fetch = [&](int e) {
+        if (quarter == 0 && live) {
+            const size_t at = (size_t)(t0 + row) * a.Hv + hk * rep + e;
+            zn = __ldg(a.z + at);
+            bn = __ldg(a.beta + at);
+        }
+    };
+    fetch(0);
+    if (warp == 1) {
         tc::tmem_alloc(&s_tmem, 256);
         tc::tmem_relinquish();
     }
@@ -181,21 +202,18 @@ gdn_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tm = s_tmem;
-    if (tid == 0) {
-        tc::mbar_arrive_expect_tx(&loaded, 2 * TILE);
-        for (int s = 0; s < 2; ++s) {
-            tc::tma_load_3d(sm + s * 16384, &mk, s * 64, hk, t0, &loaded);
-            tc::tma_load_3d(sm + TILE + s * 16384, &mq, s * 64, hk, t0, &loaded);
+    // One thread waits and the others stop at the barrier: sixteen polling warps would take
+    // issue slots from the SM's other CTA.
+    auto wait_for = [&](uint64_t* bar) {
+        if (tid == 0 && !tc::mbar_wait_bounded(bar, 0, p.wait_limit)) {
+            const bool d = tc::mbar_wait_bounded(bar, 0, tc::WAIT_POLLS);    // give up, but not before what was issued
+            atomicOr(reinterpret_cast<int*>(a.workspace), d ? tc::ERR_WAIT : tc::ERR_WAIT | tc::ERR_DRAIN);
+            s_ok = 0;
         }
-    }
-    bool ok = tc::mbar_wait_bounded(&loaded, 0, p.wait_limit);
-    if (!ok && tid == 0) {          // give up: the copies land before the CTA leaves
-        const bool d = tc::mbar_wait_bounded(&loaded, 0, tc::WAIT_POLLS);
-        atomicOr(reinterpret_cast<int*>(a.workspace), d ? tc::ERR_WAIT : tc::ERR_WAIT | tc::ERR_DRAIN);
-        s_ok = 0;
-    }
-    __syncthreads();
-    ok = s_ok;
+        __syncthreads();
+        return s_ok != 0;
+    };
+    bool ok = wait_for(&loaded);
     if (ok) {
         // rows behind the sequence belong to its neighbour: zero them
         if (len < C) {
@@ -204,24 +222,26 @@ gdn_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
                 *reinterpret_cast<uint4*>(sm + (q >> 4) * TILE + ((q >> 3) & 1) * 16384 + r * 128 + (q & 7) * 16) = make_uint4(0, 0, 0, 0);
             }
             tc::fence_proxy_async();
+            __syncthreads();
         }
-        __syncthreads();
-        if (tid == 0) {
-            const uint32_t kb = tc::smem_u32(sm), qb = kb + TILE, id = tc::idesc_bf16(128, 128);
+        if (warp == 0) {
+            const uint32_t kb = tc::smem_u32(sm), id = tc::idesc_bf16(128, 128);
+            const uint64_t dk = tc::sw128_desc(kb), dq = tc::sw128_desc(kb + TILE);
+#pragma unroll
             for (int k = 0; k < 8; ++k) {
-                const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
-                tc::mma_f16_ss(tm, tc::sw128_desc(kb + off), tc::sw128_desc(kb + off), id, k > 0);
-                tc::mma_f16_ss(tm + 128, tc::sw128_desc(qb + off), tc::sw128_desc(kb + off), id, k > 0);
+                const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+                tc::mma_f16_ss_elect(tm, dk + off, dk + off, id, k > 0);
+                tc::mma_f16_ss_elect(tm + 128, dq + off, dk + off, id, k > 0);
             }
-            tc::mma_commit(&done);
+            tc::mma_commit_elect(&done);
         }
         {
-            // squares of this row: threads of half 0 the key's, of half 1 the query's
-            const uint8_t* base = sm + half * TILE;
+            // squares of this row: two threads the key's, two the query's, 64 channels each
+            const uint8_t* base = sm + quarter * 16384;
             float ss = 0.f;
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                const uint4 u = *reinterpret_cast<const uint4*>(base + (c >> 3) * 16384 + swz(row, c & 7));
+            for (int c = 0; c < 8; ++c) {
+                const uint4 u = *reinterpret_cast<const uint4*>(base + swz(row, c));
                 const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -229,53 +249,43 @@ gdn_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
                     ss += lo * lo + hi * hi;
                 }
             }
-            const float r = a.qk_l2norm ? rsqrtf(ss + 1e-6f) : 1.0f;
-            (half ? s_rq : s_rk)[row] = r;
+            s_part[quarter][row] = ss;
         }
-        ok = tc::mbar_wait_bounded(&done, 0, p.wait_limit);
-        if (!ok && tid == 0) {
-            const bool d = tc::mbar_wait_bounded(&done, 0, tc::WAIT_POLLS);
-            atomicOr(reinterpret_cast<int*>(a.workspace), d ? tc::ERR_WAIT : tc::ERR_WAIT | tc::ERR_DRAIN);
-            s_ok = 0;
-        }
+        ok = wait_for(&done);
         tc::fence_after_sync();
-        __syncthreads();
-        ok = s_ok;
+        if (quarter < 2) {
+            const float ss = s_part[2 * quarter][row] + s_part[2 * quarter + 1][row];
+            (quarter ? s_rq : s_rk)[row] = a.qk_l2norm ? rsqrtf(ss + 1e-6f) : 1.0f;
+        }
     }
     float* X = reinterpret_cast<float*>(sm + P_X);        // the tiles have been consumed
-    float* Y = reinterpret_cast<float*>(sm + P_Y);
+    uint8_t* img = sm + P_Y;                              // the masked Q K^T on its way out, then Y
     float* W = reinterpret_cast<float*>(sm + P_W);        // W[b][j] = rk_j e^{g_(16 b - 1) - g_j}, j < 16 b
-    const int rep = a.Hv / a.Hk;
-    const bool live = row < len;
     constexpr float FIX = 4294967296.f, UNFIX = 1.f / 4294967296.f;
     for (int e = 0; ok && e < rep; ++e) {
         const int h = hk * rep + e;
         uint8_t* rec = reinterpret_cast<uint8_t*>(a.workspace) + WS_HEAD + (idx * a.Hv + h) * (size_t)REC;
         // sums of the log-decays (base 2), exact in 2^-32 fixed point.  A step below -4096 is
         // an exponential of 0 in any sum; a NaN travels with beta.
-        if (half == 0) {
+        if (quarter == 0) {
             long long g = 0;
             float beta = 0.f;
             if (live) {
-                const size_t at = (size_t)(t0 + row) * a.Hv + h;
-                const float x = log_decay_mode(a.z[at], __expf(a.A[h]), a.g_min, a.gate_mode) * 1.4426950408889634f;
-                beta = x == x ? a.beta[at] : x;
+                const float x = log_decay_mode(zn, __expf(__ldg(a.A + h)), a.g_min, a.gate_mode) * 1.4426950408889634f;
+                beta = x == x ? bn : x;
                 g = (long long)(fminf(fmaxf(x, -4096.f), 4096.f) * FIX);
             }
+            if (e + 1 < rep) fetch(e + 1);
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const long long y = __shfl_up_sync(~0u, g, o);
                 if (lane >= o) g += y;
             }
             if (lane == 31) s_wsum[warp] = g;
-            s_g[row] = g;
-            s_beta[row] = beta;
-        }
-        __syncthreads();
-        if (half == 0) {
-            long long g = s_g[row];
+            asm volatile("bar.sync 1, 128;" ::: "memory");
             for (int w = 0; w < warp; ++w) g += s_wsum[w];
             s_g[row] = g;
+            s_beta[row] = beta;
         }
         __syncthreads();
         const long long gi = s_g[row], gC = s_g[C - 1];
@@ -283,7 +293,7 @@ gdn_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
             const int b = j / C, c = j % C;
             W[j] = c < 16 * b ? s_rk[c] * exp2f((float)(s_g[16 * b - 1] - s_g[c]) * UNFIX) : 0.f;
         }
-        if (half == 1) {
+        if (quarter == 1) {
             const float eg = exp2f((float)gi * UNFIX), beta = s_beta[row];
             float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
             if (live)
@@ -292,72 +302,85 @@ gdn_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
             *reinterpret_cast<float4*>(rec + REC_F + row * 16) = f;
             if (row == 0) *reinterpret_cast<float*>(rec + REC_F + C * 16) = exp2f((float)gC * UNFIX);
         }
+        if (tid == 0) tc::bulk_wait_read();       // the last head's image has left
         __syncthreads();
-        // A and the masked Q K^T, row by row: 64 columns per thread, 16 at a time
+        // A into X and the masked Q K^T into its image: 16 x 16 blocks on and below the diagonal,
+        // column block quarter or quarter + 4 of the row
         {
             const int b = row >> 4;
             const float u = b ? exp2f((float)(gi - s_g[16 * b - 1]) * UNFIX) : 0.f;     // e^{g_i - g_(16 b - 1)}
             const float ka = live ? s_beta[row] * s_rk[row] : 0.f, qa = live ? s_rq[row] * a.scale : 0.f;
+            const float kau = ka * u, qau = qa * u;
             const uint32_t lane0 = tm + ((uint32_t)(warp & 3) << 21);
 #pragma unroll 1
-            for (int cb = half * 4; cb < half * 4 + 4; ++cb) {
+            for (int cb = quarter; cb < 8; cb += 4) {
+                if (cb >= 4 && (warp & 3) < 2) break;        // rows 0 .. 63 have no columns behind 63
+                uint8_t* dst = img + (cb < 4 ? 0 : 16384 - 64 * 128);
+                const int piece = (cb & 3) * 2;
                 float G[16], P[16];
                 tc::tmem_ld16(lane0 + cb * 16, G);
                 tc::tmem_ld16(lane0 + 128 + cb * 16, P);
                 tc::tmem_ld_wait();
-                float w[16];                                 // rk_j e^{g_i - g_j}, 0 for j > i
+                uint32_t q[8] = {0, 0, 0, 0, 0, 0, 0, 0};
                 if (cb < b) {
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) w[c] = u * W[b * C + cb * 16 + c];
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        const int j = cb * 16 + c;
-                        w[c] = cb == b && j <= row ? s_rk[j] * exp2f((float)(gi - s_g[j]) * UNFIX) : 0.f;
-                    }
-                }
-                // masked places by selection, not by a product with 0
-                uint32_t q[8];
-#pragma unroll
-                for (int c = 0; c < 16; c += 2) {
-                    const int j = cb * 16 + c;
-                    const float x0 = j <= row && live ? qa * w[c] * P[c] : 0.f;
-                    const float x1 = j + 1 <= row && live ? qa * w[c + 1] * P[c + 1] : 0.f;
-                    const __nv_bfloat162 hh = __floats2bfloat162_rn(x0, x1);
-                    q[c >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
-                }
-                if (cb < 4 || row >= 64) {
-                    uint8_t* dst = rec + REC_A + (cb < 4 ? 0 : 16384 - 64 * 128);
-                    const int piece = (cb & 3) * 2;
-                    *reinterpret_cast<uint4*>(dst + swz(row, piece)) = make_uint4(q[0], q[1], q[2], q[3]);
-                    *reinterpret_cast<uint4*>(dst + swz(row, piece + 1)) = make_uint4(q[4], q[5], q[6], q[7]);
-                }
-                if (cb <= b) {
+                    // below the diagonal nothing is masked, and rows behind the sequence have ka = qa = 0
+                    // over zeroed (finite) products
 #pragma unroll
                     for (int c = 0; c < 16; c += 4) {
-                        float x[4];
+                        const float4 w = *reinterpret_cast<const float4*>(W + b * C + cb * 16 + c);
+                        *reinterpret_cast<float4*>(X + row * XS + cb * 16 + c) =
+                            make_float4(kau * (w.x * G[c]), kau * (w.y * G[c + 1]), kau * (w.z * G[c + 2]), kau * (w.w * G[c + 3]));
+                        const __nv_bfloat162 h0 = __floats2bfloat162_rn(qau * (w.x * P[c]), qau * (w.y * P[c + 1]));
+                        const __nv_bfloat162 h1 = __floats2bfloat162_rn(qau * (w.z * P[c + 2]), qau * (w.w * P[c + 3]));
+                        q[c >> 1] = *reinterpret_cast<const uint32_t*>(&h0);
+                        q[(c >> 1) + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+                    }
+                } else if (cb == b) {
+                    // masked places by selection, not by a product with 0
+#pragma unroll
+                    for (int c = 0; c < 16; c += 4) {
+                        float x[4], y[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int j = cb * 16 + c + i;
-                            x[i] = j < row && live ? ka * w[c + i] * G[c + i] : 0.f;
+                            const float w = s_rk[j] * exp2f((float)(gi - s_g[j]) * UNFIX);      // rk_j e^{g_i - g_j}
+                            x[i] = j < row && live ? ka * w * G[c + i] : 0.f;
+                            y[i] = j <= row && live ? qa * w * P[c + i] : 0.f;
                         }
                         *reinterpret_cast<float4*>(X + row * XS + cb * 16 + c) = make_float4(x[0], x[1], x[2], x[3]);
+                        const __nv_bfloat162 h0 = __floats2bfloat162_rn(y[0], y[1]), h1 = __floats2bfloat162_rn(y[2], y[3]);
+                        q[c >> 1] = *reinterpret_cast<const uint32_t*>(&h0);
+                        q[(c >> 1) + 1] = *reinterpret_cast<const uint32_t*>(&h1);
                     }
                 }
+                *reinterpret_cast<uint4*>(dst + swz(row, piece)) = make_uint4(q[0], q[1], q[2], q[3]);
+                *reinterpret_cast<uint4*>(dst + swz(row, piece + 1)) = make_uint4(q[4], q[5], q[6], q[7]);
+                __syncwarp();
             }
+            tc::fence_proxy_async();
         }
         __syncthreads();
+        if (tid == 0) {
+            tc::bulk_store(rec + REC_A, img, TRI);
+            tc::bulk_commit();
+        }
         // inverses of the diagonal blocks: lane c < 16 of warp b solves for column c of block b
-        {
-            float* B = X + warp * 16 * XS + warp * 16;
+        if (warp >= 8) {
+            float* B = X + (warp - 8) * 16 * XS + (warp - 8) * 16;
             float x[16];
             if (lane < 16) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    float s = i == lane ? 1.f : 0.f;
+                    float s = i == lane ? 1.f : 0.f, s2 = 0.f;
 #pragma unroll
-                    for (int j = 0; j < i; ++j) s -= B[i * XS + j] * x[j];
-                    x[i] = s;
+                    for (int j = 0; j < i; j += 4) {           // B's row in fours: its upper part is zero
+                        const float4 r = *reinterpret_cast<const float4*>(B + i * XS + j);
+                        s -= r.x * x[j];
+                        if (j + 1 < i) s2 -= r.y * x[j + 1];
+                        if (j + 2 < i) s -= r.z * x[j + 2];
+                        if (j + 3 < i) s2 -= r.w * x[j + 3];
+                    }
+                    x[i] = s + s2;
                 }
             }
             __syncwarp();
@@ -366,36 +389,23 @@ gdn_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
                 for (int i = 0; i < 16; ++i) B[i * XS + lane] = x[i];
             }
         }
+        if (tid == 0) tc::bulk_wait_read();       // the image becomes Y
         __syncthreads();
-        // merges: 16 -> 32 (a warp each), 32 -> 64, 64 -> 128 (16 x 16 tiles over the warps)
-        if (warp < 4) {
-            const int o = warp * 32;
-            float acc[2][4] = {};
-            float* y = Y + warp * 16 * YS;
-            block_product(acc, X + (o + 16) * XS + o, XS, X + o * XS + o, XS, 1, lane);
-            block_store(acc, y, YS, 1.f, lane);
-            __syncwarp();
-            float acd[2][4] = {};
-            block_product(acd, X + (o + 16) * XS + o + 16, XS, y, YS, 1, lane);
-            block_store(acd, X + (o + 16) * XS + o, XS, -1.f, lane);
-        }
-        __syncthreads();
+        // Merges to blocks of 32, 64, 128 in 16 x 16 tiles, a warp each: Y = B X, then - Z Y with Z the
+        // lower block's inverse.  X and Z are lower triangular: k from the tile's column on, and up
+        // to the tile's row; the tiles are dealt so that every scheduler gets long and short ones.
+        float* Y = reinterpret_cast<float*>(img);
 #pragma unroll 1
-        for (int s = 32; s < C; s *= 2) {
-            const int nb = s / 16, tiles = (C / (2 * s)) * nb * nb;
-            for (int w = warp; w < tiles; w += 8) {              // Y = B X, X lower: k from the tile's column on
-                const int m = w / (nb * nb), r = w / nb % nb, c = w % nb, o = m * 2 * s;
-                float acc[2][4] = {};
-                block_product(acc, X + (o + s + 16 * r) * XS + o + 16 * c, XS, X + (o + 16 * c) * XS + o + 16 * c, XS, nb - c, lane);
-                block_store(acc, Y + (m * s + 16 * r) * YS + 16 * c, YS, 1.f, lane);
-            }
+        for (int s = 16; s < C; s *= 2) {
+            const int nb = s / 16, per = nb * nb, m = warp / per, i = (warp % per) / nb, j = (i + warp) % nb, o = m * 2 * s;
+            const bool on = m < C / (2 * s);
+            if (on)         // tile (i, j)
+                tile_product(Y + (m * s + 16 * i) * YS + 16 * j, YS, 1.f, X + (o + s + 16 * i) * XS + o + 16 * j, XS,
+                             X + (o + 16 * j) * XS + o + 16 * j, XS, 2 * (nb - j), lane);
             __syncthreads();
-            for (int w = warp; w < tiles; w += 8) {              // - Y^-1 (B X): k up to the tile's row
-                const int m = w / (nb * nb), r = w / nb % nb, c = w % nb, o = m * 2 * s;
-                float acc[2][4] = {};
-                block_product(acc, X + (o + s + 16 * r) * XS + o + s, XS, Y + m * s * YS + 16 * c, YS, r + 1, lane);
-                block_store(acc, X + (o + s + 16 * r) * XS + o + 16 * c, XS, -1.f, lane);
-            }
+            if (on)         // tile (j, i): the result takes B's place
+                tile_product(X + (o + s + 16 * j) * XS + o + 16 * i, XS, -1.f, X + (o + s + 16 * j) * XS + o + s, XS,
+                             Y + m * s * YS + 16 * i, YS, 2 * (j + 1), lane);
             __syncthreads();
         }
         // T = hi + lo, 16 bytes of each per thread and step; blocks above the diagonal are zero
@@ -416,9 +426,10 @@ gdn_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
         }
         __syncthreads();
     }
+    if (tid == 0) tc::bulk_wait_all();
     tc::fence_before_sync();
     __syncthreads();
-    if (warp == 0) tc::tmem_dealloc(tm, 256);
+    if (warp == 1) tc::tmem_dealloc(tm, 256);
 }
 
 // ---------------------------------------------------------------------------
