@@ -597,39 +597,45 @@ def gate_norm(o, g_in, norm_w=None, eps=1e-6, out=None, stream=None):
 
 def _dense(name, t, shape, dtype, dev):
     """``t``'s address, once it is what the entry point reads: ``shape`` (None: any
-    extent), ``dtype``, contiguous, on ``dev``.  None stays None."""
+    extent), ``dtype``, contiguous, on ``dev``.  None stays None.  (The calls below
+    are made once per token and layer: the checks take the shortest way.)"""
     if t is None:
         return None
-    if t.dtype != dtype or t.device != dev or not t.is_contiguous() or len(t.shape) != len(shape) or \
-            any(e is not None and e != x for e, x in zip(shape, t.shape)):
-        raise KDAError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, "
-                       f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.is_contiguous() and t.device == dev:
+        have = t.shape
+        if have == shape or (len(have) == len(shape) and all(e is None or e == x for e, x in zip(shape, have))):
+            return t.data_ptr()
+    raise KDAError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, "
+                   f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
 
 
 def _heads(name, t, shape, dtype, dev):
     """Address and token stride of a [tokens, heads, d] tensor with dense heads:
     contiguous, or a slice of a packed projection."""
-    if t.dtype != dtype or t.device != dev or tuple(t.shape) != tuple(shape):
+    if t.dtype is not dtype or t.device != dev or t.shape != shape:
         raise KDAError(f"{name}: expected {dtype} of shape {tuple(shape)} on {dev}, "
                        f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     n, h, d = shape
+    if t.is_contiguous():
+        return t.data_ptr(), h * d
     st = t.stride()
     if (d > 1 and st[2] != 1) or (h > 1 and st[1] != d):
         raise KDAError(f"{name}: the heads of a token must be dense, got strides {st}")
     return t.data_ptr(), (st[0] if n > 1 else h * d)
 
 
-def _launch(fn, args, dev, what):
-    """The call on the current stream of the tensors' device."""
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if dev.index != torch.cuda.current_device():
+def _launch(name, args, dev):
+    """The entry point ``name`` on the current stream of the tensors' device."""
+    fn = getattr(_lib or load_library(), name)
+    index = dev.index
+    stream = torch._C._cuda_getCurrentRawStream(index)      # current_stream(dev) without the object
+    if index == torch._C._cuda_getDevice():
+        status = fn(ctypes.byref(args), stream)
+    else:
         with torch.cuda.device(dev):
             status = fn(ctypes.byref(args), stream)
-    else:
-        status = fn(ctypes.byref(args), stream)
     if status != 0:
-        _check(status, what)
+        _check(status, name)
 
 
 def _on_stream(f):
@@ -647,7 +653,7 @@ def _on_stream(f):
 
 
 def _cuda_device(t, name):
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise KDAError(f"{name} must be a CUDA tensor, got {t.device}")
     return t.device
 
@@ -715,7 +721,7 @@ def gdn_prefill(q, k, v, z, beta, A, cu_seqlens=None, cu_seqlens_host=None, S0=N
         None, 0, _gate_code(gate))
     lib = load_library()
     if recurrent:
-        _launch(lib.kda_gdn_prefill_recurrent, a, dev, "kda_gdn_prefill_recurrent")
+        _launch("kda_gdn_prefill_recurrent", a, dev)
         return o, S_T
     need = lib.kda_gdn_prefill_workspace_size(ctypes.byref(a))
     if need:
@@ -728,7 +734,7 @@ def gdn_prefill(q, k, v, z, beta, A, cu_seqlens=None, cu_seqlens_host=None, S0=N
         elif workspace.device != dev or not workspace.is_contiguous():
             raise KDAError(f"the workspace must be a contiguous tensor on {dev}")
         a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _launch(lib.kda_gdn_prefill, a, dev, "kda_gdn_prefill")
+    _launch("kda_gdn_prefill", a, dev)
     return o, S_T
 
 
@@ -743,17 +749,17 @@ def gdn_decode_step(q, k, v, z, beta, A, state, slots=None, g_min=-5.0, scale=1.
     """
     dev = _cuda_device(q, "q")
     N, Hk, dk = q.shape
-    Hv, dv = v.shape[1], v.shape[2]
+    _, Hv, dv = v.shape
     bf, f32 = torch.bfloat16, torch.float32
-    o = torch.empty((N, Hv, dv), dtype=bf, device=dev) if out is None else out
+    o = torch.empty_like(v) if out is None else out
     a = GdnDecodeArgs(
         N, Hk, Hv, dk, dv, state.shape[0],
         _dense("q", q, (N, Hk, dk), bf, dev), _dense("k", k, (N, Hk, dk), bf, dev),
         _dense("v", v, (N, Hv, dv), bf, dev), _dense("z", z, (N, Hv), f32, dev),
         _dense("beta", beta, (N, Hv), f32, dev), _dense("A", A, (Hv,), f32, dev),
-        g_min, scale, 1 if qk_l2norm else 0, _dense("state", state, (None, Hv, dk, dv), f32, dev),
+        g_min, scale, 1 if qk_l2norm else 0, _dense("state", state, (state.shape[0], Hv, dk, dv), f32, dev),
         _dense("slots", slots, (N,), torch.int32, dev), _dense("out", o, (N, Hv, dv), bf, dev), _gate_code(gate))
-    _launch(load_library().kda_gdn_decode_step, a, dev, "kda_gdn_decode_step")
+    _launch("kda_gdn_decode_step", a, dev)
     return o
 
 
@@ -778,10 +784,10 @@ def qk_norm_rope(q, k, cos, sin, positions, q_weight=None, k_weight=None, eps=1e
     a = QkNormRopeArgs(
         T, Hq, Hkv, d, 2 * half, cos.shape[0], _dtype_code(q), qp, kp, qs, ks,
         _dense("q_weight", q_weight, (d,), f32, dev), _dense("k_weight", k_weight, (d,), f32, dev), eps,
-        _dense("cos", cos, (None, half), f32, dev), _dense("sin", sin, (cos.shape[0], half), f32, dev),
+        _dense("cos", cos, (cos.shape[0], half), f32, dev), _dense("sin", sin, (cos.shape[0], half), f32, dev),
         _dense("positions", positions, (T,), torch.int32, dev), 1 if interleaved else 0,
         _dense("q_out", qo, (T, Hq, d), dt, dev), _dense("k_out", ko, (T, Hkv, d), dt, dev))
-    _launch(load_library().kda_qk_norm_rope, a, dev, "kda_qk_norm_rope")
+    _launch("kda_qk_norm_rope", a, dev)
     return qo, ko
 
 
@@ -835,7 +841,7 @@ def window_prefill(q, k, v, window, sinks=0, cu_seqlens=None, cu_seqlens_host=No
         cuk_host.data_ptr(), qp, kp, vp, qs, ks, vs, d ** -0.5 if scale is None else scale,
         _dense("out", o, (T, Hq, d), bf, dev), lse.data_ptr() if want_lse else None, kc, vc,
         _dense("slots", slots, (N,), torch.int32, dev), num_slots, rows)
-    _launch(load_library().kda_window_prefill, a, dev, "kda_window_prefill")
+    _launch("kda_window_prefill", a, dev)
     return (o, lse) if want_lse else o
 
 
@@ -858,5 +864,5 @@ def window_decode(q, k, v, k_cache, v_cache, positions, window, sinks=0, slots=N
         N, Hq, Hkv, d, window, sinks, KDA_BF16, qp, kp, vp, qs, ks, vs, d ** -0.5 if scale is None else scale, kc, vc,
         _dense("positions", positions, (N,), torch.int32, dev), _dense("slots", slots, (N,), torch.int32, dev),
         num_slots, rows, _dense("out", o, (N, Hq, d), bf, dev))
-    _launch(load_library().kda_window_decode, a, dev, "kda_window_decode")
+    _launch("kda_window_decode", a, dev)
     return o
