@@ -149,6 +149,11 @@ KDA_DEV void fma2(float& d0, float& d1, float x0, float x1, float c, float b) {
         "fma.rn.ftz.f32x2 d, x, c, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
         : "=f"(d0), "=f"(d1) : "f"(x0), "f"(x1), "f"(c), "f"(b));
 }
+// The registers of an asynchronous TMEM load are the compiler's to use only behind the wait.
+KDA_DEV void after_wait(float* s, int n) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) asm volatile("" : "+f"(s[i]));
+}
 KDA_DEV void add2(float& l0, float& l1, float e0, float e1) {
     asm("{\n\t.reg .b64 l, e;\n\t"
         "mov.b64 l, {%0, %1};\n\tmov.b64 e, {%2, %3};\n\t"
@@ -163,7 +168,7 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
     using L = PF<D>;
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t full[ROUNDS], empty[ROUNDS], edge, q_full, q_empty, s_full[2], p_full[2][2], o_full[2],
-        l_full[2], o_empty[2], u_full[UNITS], drained;
+        l_full[2], o_empty[2], u_full[UNITS], turn[2], drained;
     __shared__ Unit s_unit[UNITS];
     __shared__ float s_l[2][128];
     __shared__ uint32_t s_tmem;
@@ -182,6 +187,7 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
         tc::mbar_init(&q_empty, 2);
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&s_full[i], 1);
+            tc::mbar_init(&turn[i], 1);
             tc::mbar_init(&p_full[i][0], 128);
             tc::mbar_init(&p_full[i][1], 128);
             tc::mbar_init(&o_full[i], 1);
@@ -280,8 +286,11 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
             }
         } else if (warp < 15) {
             // ---------------- MMAs of tile t: the warp computes together, one lane issues ----------------
-            // The loops stay rolled: this code runs once per round between the softmax warps' long
-            // straight runs, and instructions that are fetched anew cost more than the loop.
+            // The tiles take turns: A's products of a round, B's, A's of the next round, handed on by the
+            // barriers `turn`.  One tile's S is so ready while the other's products run, and the two
+            // softmaxes stay half a round apart; with the products interleaved both S arrive together
+            // and the softmaxes share the issue slots while the tensor core waits (4600 cycles a round).
+            // Two warps, because the waits and the commits of one hide behind the other's products.
             const int t = warp - 13;
             uint32_t rd = 0, nu = 0, np = 0;       // rounds, units, softmax steps
             bool ok = true;
@@ -290,19 +299,33 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
             auto qk = [&](uint32_t slot, int width) {
                 const uint32_t id = tc::idesc_bf16(128, width, false, false, p.neg != 0);
                 const uint64_t kd = tc::sw128_desc(ra + slot * L::SB);
-#pragma unroll 1
+#pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;      // descriptors count 16 bytes
                     tc::mma_f16_ss_elect(tmu + t * 128, qd + off, kd + off, id, k > 0);
                 }
             };
-            auto pv = [&](uint32_t slot, int k0, int k1, bool first) {
+            auto pv = [&](uint32_t slot, int half, int steps, bool first) {
                 const uint32_t id = tc::idesc_bf16(128, D, false, true);
                 const uint64_t vd = tc::sw128_desc_mn(ra + slot * L::SB, 16384);
+                const int k0 = 4 * half;
+                if (steps >= k0 + 4) {              // without a test between the products
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        tc::mma_f16_ts_elect(tmu + 256 + t * D, tmu + t * 128 + (k0 + k) * 8, vd + (k0 + k) * (2048 >> 4), id,
+                                             !(first && k0 + k == 0));
+                } else {
 #pragma unroll 1
-                for (int k = k0; k < k1; ++k)
-                    tc::mma_f16_ts_elect(tmu + 256 + t * D, tmu + t * 128 + k * 8, vd + k * (2048 >> 4), id,
-                                      !(first && k == 0));
+                    for (int k = k0; k < steps; ++k)
+                        tc::mma_f16_ts_elect(tmu + 256 + t * D, tmu + t * 128 + k * 8, vd + k * (2048 >> 4), id,
+                                             !(first && k == 0));
+                }
+            };
+            // Round r of A waits for B's round r - 1, that of B for A's round r.
+            auto my_turn = [&](uint32_t r) { return t ? wait_warp(&turn[1], r & 1, limit, abort) : r == 0 || wait_warp(&turn[0], (r - 1) & 1, limit, abort); };
+            auto hand_on = [&] {
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&turn[1 - t]);
             };
             // widths of a unit's tiles, uniform over the warp
             struct Tiles { int nwin, ntiles, wlast, slast; };
@@ -323,12 +346,13 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
             uint32_t vs = L::SLOTS - 1, ks = 0;    // slots of this round's values and keys
             if ((long)blockIdx.x < p.units) {
                 ok = wait_warp(&u_full[0], 0, limit, abort) && wait_warp(&q_full, 0, limit, abort) &&
-                     wait_warp(&full[0], 0, limit, abort);
+                     wait_warp(&full[0], 0, limit, abort) && my_turn(0);
                 tc::fence_after_sync();
                 if (ok) {
                     x = tiles_of(0);
                     qk(0, width_of(x, 0));
                     tc::mma_commit_elect(&s_full[t]);
+                    hand_on();
                     tc::mma_commit_elect(&empty[0]);
                     if (x.ntiles == 1) tc::mma_commit_elect(&q_empty);
                 }
@@ -346,12 +370,12 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
                     const int steps = width_of(x, i) / 16;
                     ok = wait_warp(&full[rd % ROUNDS], (rd / ROUNDS) & 1, limit, abort);
                     if (ok && i == 0 && nu > 0) ok = wait_warp(&o_empty[t], (nu - 1) & 1, limit, abort);
-#pragma unroll 1
-                    for (int h = 0; h < 2 && ok; ++h) {
-                        ok = wait_warp(&p_full[t][h], np & 1, limit, abort);
-                        tc::fence_after_sync();
-                        if (ok) pv(vs, 4 * h, min(steps, 4 * h + 4), i == 0);
-                    }
+                    ok = ok && my_turn(rd) && wait_warp(&p_full[t][0], np & 1, limit, abort);
+                    tc::fence_after_sync();
+                    if (ok) pv(vs, 0, steps, i == 0);
+                    ok = ok && wait_warp(&p_full[t][1], np & 1, limit, abort);
+                    tc::fence_after_sync();
+                    if (ok) pv(vs, 1, steps, i == 0);
                     if (!ok) break;
                     if (last) {
                         tc::mma_commit_elect(&o_full[t]);
@@ -366,6 +390,7 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
                         qk(ks, last ? width_of(y, 0) : width_of(x, i + 1));
                         tc::mma_commit_elect(&s_full[t]);
                     }
+                    hand_on();
                     tc::mma_commit_elect(&empty[rd % ROUNDS]);
                     // the S issued in this round was a unit's last: its Q may be overwritten
                     if (last ? more && y.ntiles == 1 : i + 2 == x.ntiles) tc::mma_commit_elect(&q_empty);
@@ -459,83 +484,108 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
                 // columns [a, b] of the window and columns below z of the sinks are seen
                 const int b = window ? pos - j0 : -1, a = window ? max(0, pos - p.a.window + 1 - j0) : 0;
                 const int z = window ? min(p.a.sinks - j0, b + 1) : x.nsink - j0;
-                float m = -INFINITY;
+                // masks 32 columns.  A warp's rows are few queries, so most chunks of an edge tile are
+                // seen by all of them.
+                auto mask = [&](int k) {
+                    if (!whole) {
+                        const int hi = min(31, b - 32 * k), lo = max(0, a - 32 * k), zz = min(32, z - 32 * k);
+                        uint32_t seen = hi >= lo && lo < 32 ? (0xffffffffu >> (31 - hi)) & (0xffffffffu << lo) : 0u;
+                        if (zz > 0) seen |= 0xffffffffu >> (32 - zz);
+                        if (!__all_sync(~0u, seen == 0xffffffffu)) {
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) s[32 * k + c] = (seen >> c) & 1u ? s[32 * k + c] : -INFINITY;
+                        }
+                    }
+                };
+                auto largest = [&](int k, float m) {
+                    float m0 = m, m1 = s[32 * k];
+#pragma unroll
+                    for (int c = 1; c < 31; c += 4) {
+                        m0 = fmaxf(fmaxf(m0, s[32 * k + c]), s[32 * k + c + 1]);
+                        m1 = fmaxf(fmaxf(m1, s[32 * k + c + 2]), c + 3 < 32 ? s[32 * k + c + 3] : m1);
+                    }
+                    return fmaxf(fmaxf(m0, m1), s[32 * k + 31]);
+                };
+                // exp2(c s - ref) of 32 columns, their sum, and P in bf16 over S (S is in registers)
+                auto weigh = [&](int k, float base, float& l0, float& l1) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int c = 0; c < 32; c += 2) {
+                        float e0, e1;
+                        fma2(e0, e1, s[32 * k + c], s[32 * k + c + 1], p.c, base);
+                        e0 = exp2f(e0);
+                        e1 = exp2f(e1);
+                        add2(l0, l1, e0, e1);
+                        // weights rounded to bf16 for the product; l keeps float32
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(e0, e1);
+                        w[c >> 1] = *reinterpret_cast<const uint32_t*>(&h);
+                    }
+                    tc::tmem_st16u(ts + k * 16, w);
+                };
+                // The row's reference is the largest score known before this tile (on the first tile: its
+                // own first half's), so the exponentials need not wait for the tile's maximum, nor for its
+                // last columns: TMEM reads crawl while the other tile's products run (64 columns in some
+                // 700 cycles).  Where the maximum outgrows the reference by 2^8 the tile is done again.
                 tc::tmem_ld32(ts, s);
                 if (32 < width) tc::tmem_ld32(ts + 32, s + 32);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (k * 32 < width) {
-                        if (k == 0 || k == 2) {            // columns 64 .. 127 arrive while 0 .. 63 are searched
-                            tc::tmem_ld_wait();
-                            if (k == 0 && 64 < width) {
-                                tc::tmem_ld32(ts + 64, s + 64);
-                                if (96 < width) tc::tmem_ld32(ts + 96, s + 96);
-                            }
-                        }
-                        if (!whole) {
-                            // bit c: column 32 k + c is seen.  A warp's rows are few queries, so most
-                            // chunks of an edge tile are seen by all of them or by none.
-                            const int hi = min(31, b - 32 * k), lo = max(0, a - 32 * k), zz = min(32, z - 32 * k);
-                            uint32_t seen = hi >= lo && lo < 32 ? (0xffffffffu >> (31 - hi)) & (0xffffffffu << lo) : 0u;
-                            if (zz > 0) seen |= 0xffffffffu >> (32 - zz);
-                            if (!__all_sync(~0u, seen == 0xffffffffu)) {
-#pragma unroll
-                                for (int c = 0; c < 32; ++c) s[32 * k + c] = (seen >> c) & 1u ? s[32 * k + c] : -INFINITY;
-                            }
-                        }
-                        float m0 = s[32 * k], m1 = s[32 * k + 1];
-#pragma unroll
-                        for (int c = 2; c < 32; c += 4) {
-                            m0 = fmaxf(fmaxf(m0, s[32 * k + c]), s[32 * k + c + 1]);
-                            if (c + 3 < 32) m1 = fmaxf(fmaxf(m1, s[32 * k + c + 2]), s[32 * k + c + 3]);
-                        }
-                        m = fmaxf(fmaxf(m, m0), m1);
-                    }
+                tc::tmem_ld_wait();
+                after_wait(s, 64);
+                if (64 < width) tc::tmem_ld32(ts + 64, s + 64);
+                if (96 < width) tc::tmem_ld32(ts + 96, s + 96);
+                mask(0);
+                if (32 < width) mask(1);
+                if (i == 0) {
+                    float m = largest(0, -INFINITY);
+                    if (32 < width) m = largest(1, m);
+                    ref = m * p.c;
                 }
-                m *= p.c;
-                // Rescale where the maximum outgrew the reference by 2^8 (always from no reference).
-                const bool grow = m > ref + 8.f;
-                if (__any_sync(~0u, grow)) {
-                    const float nref = grow ? m : ref;
-                    const float f = ref == -INFINITY ? 0.f : exp2f(ref - nref);
-                    l0 *= f;
-                    l1 *= f;
-                    ref = nref;
-                    if (i > 0) {
+                for (bool again = false;; again = true) {
+                    const float base = ref == -INFINITY ? 0.f : -ref;   // nothing seen yet: every weight is exp2(-inf) = 0
+                    float n0 = 0.f, n1 = 0.f;
+                    weigh(0, base, n0, n1);
+                    if (32 < width) weigh(1, base, n0, n1);
+                    if (!again) {
+                        tc::tmem_ld_wait();
+                        after_wait(s + 64, 64);
+                        if (64 < width) mask(2);
+                        if (96 < width) mask(3);
+                        float m = largest(0, -INFINITY);
+                        if (32 < width) m = largest(1, m);
+                        if (64 < width) m = largest(2, m);
+                        if (96 < width) m = largest(3, m);
+                        m *= p.c;
+                        const bool grow = m > ref + 8.f;                // (always from no reference)
+                        if (__any_sync(~0u, grow)) {
+                            const float nref = grow ? m : ref;
+                            const float f = ref == -INFINITY ? 0.f : exp2f(ref - nref);
+                            l0 *= f;
+                            l1 *= f;
+                            ref = nref;
+                            if (i > 0) {
+#pragma unroll 1
+                                for (int k = 0; k < D / 16; ++k) {
+                                    float o[16];
+                                    tc::tmem_ld16(to + k * 16, o);
+                                    tc::tmem_ld_wait();
 #pragma unroll
-                        for (int k = 0; k < D / 16; ++k) {
-                            float o[16];
-                            tc::tmem_ld16(to + k * 16, o);
-                            tc::tmem_ld_wait();
-#pragma unroll
-                            for (int c = 0; c < 16; ++c) o[c] *= f;
-                            tc::tmem_st16(to + k * 16, o);
+                                    for (int c = 0; c < 16; ++c) o[c] *= f;
+                                    tc::tmem_st16(to + k * 16, o);
+                                }
+                            }
+                            continue;
                         }
                     }
-                }
-                const float base = ref == -INFINITY ? 0.f : -ref;   // nothing seen yet: every weight is exp2(-inf) = 0
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (k * 32 < width) {
-                        uint32_t w[16];
-#pragma unroll
-                        for (int c = 0; c < 32; c += 2) {
-                            float e0, e1;
-                            fma2(e0, e1, s[32 * k + c], s[32 * k + c + 1], p.c, base);
-                            e0 = exp2f(e0);
-                            e1 = exp2f(e1);
-                            add2(l0, l1, e0, e1);
-                            // weights rounded to bf16 for the product; l keeps float32
-                            const __nv_bfloat162 h = __floats2bfloat162_rn(e0, e1);
-                            w[c >> 1] = *reinterpret_cast<const uint32_t*>(&h);
-                        }
-                        tc::tmem_st16u(ts + k * 16, w);
-                    }
-                    if (k & 1) {
-                        tc::tmem_st_wait();
-                        tc::fence_before_sync();
-                        tc::mbar_arrive(&p_full[t][k >> 1]);
-                    }
+                    tc::tmem_st_wait();
+                    tc::fence_before_sync();
+                    tc::mbar_arrive(&p_full[t][0]);
+                    if (64 < width) weigh(2, base, n0, n1);
+                    if (96 < width) weigh(3, base, n0, n1);
+                    l0 += n0;
+                    l1 += n1;
+                    tc::tmem_st_wait();
+                    tc::fence_before_sync();
+                    tc::mbar_arrive(&p_full[t][1]);
+                    break;
                 }
             }
             if (!ok) break;
