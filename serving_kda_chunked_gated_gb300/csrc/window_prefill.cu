@@ -526,12 +526,10 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
                 // own first half's), so the exponentials need not wait for the tile's maximum, nor for its
                 // last columns: TMEM reads crawl while the other tile's products run (64 columns in some
                 // 700 cycles).  Where the maximum outgrows the reference by 2^8 the tile is done again.
-                tc::tmem_ld32(ts, s);
-                if (32 < width) tc::tmem_ld32(ts + 32, s + 32);
+                tc::tmem_ld64(ts, s);              // one load of 64 columns: two of 32 cost 8 % of the kernel
                 tc::tmem_ld_wait();
                 after_wait(s, 64);
-                if (64 < width) tc::tmem_ld32(ts + 64, s + 64);
-                if (96 < width) tc::tmem_ld32(ts + 96, s + 96);
+                if (64 < width) tc::tmem_ld64(ts + 64, s + 64);
                 mask(0);
                 if (32 < width) mask(1);
                 if (i == 0) {
