@@ -23,6 +23,8 @@
 // 128-byte row of 64 MN-major elements: one N = 64 MMA forms both products.
 #include <math.h>
 
+#include <algorithm>
+
 #include "kda_common.cuh"
 #include "tcgen05.cuh"
 #include "tma_host.cuh"
@@ -42,10 +44,16 @@ constexpr int REC_THI = 0, REC_TLO = TRI, REC_A = 2 * TRI, REC_F = 3 * TRI;
 constexpr int REC = 3 * TRI + C * 16 + 128;   // + four factors per token + e^{g_C}
 constexpr int WS_HEAD = 256;                  // the error word's line
 
+// Scans of the longest sequences start first: with one of 4097 tokens among eight shorter ones it
+// otherwise starts when these are done.  The order is the host's, by value, for up to this many.
+constexpr int MAX_ORDER = 1024;
+
 struct Params {
     kda_gdn_prefill_args a;
     long chunks;
     uint32_t wait_limit;
+    int ordered;
+    uint16_t order[MAX_ORDER];
 };
 
 // byte offset of 16-byte piece c (0 .. 7) of row r in a slab of 128-byte rows
@@ -502,7 +510,7 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int slice = blockIdx.x % (DH / COLS);
     const int h = blockIdx.x / (DH / COLS) % a.Hv;
-    const int n = blockIdx.x / (DH / COLS) / a.Hv;
+    const int place = blockIdx.x / (DH / COLS) / a.Hv, n = p.ordered ? p.order[place] : place;
     const int hk = h / (a.Hv / a.Hk);
     const int t0 = a.cu_seqlens[n], T = a.cu_seqlens[n + 1] - t0;
     const int nc = (T + C - 1) / C;
@@ -513,9 +521,9 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
         uint64_t* ones[] = {&k_full[0], &k_full[1], &k_empty[0], &k_empty[1], &q_full, &t_full, &a_full, &v_full, &edge, &ks_done,
                             &qs_done, &tr_done, &kv_done, &av_done, &drained};
         for (uint64_t* b : ones) tc::mbar_init(b, 1);
-        tc::mbar_init(&s_ready, 256);
-        tc::mbar_init(&r_ready, 256 + 128);
-        tc::mbar_init(&v_ready, 256 + 128);
+        tc::mbar_init(&s_ready, 8);         // warps
+        tc::mbar_init(&r_ready, 8 + 4);
+        tc::mbar_init(&v_ready, 8 + 4);
         tc::mbar_fence_init();
         s_abort = 0;
     }
@@ -682,8 +690,8 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
         const int row = tid & 127;
         const uint32_t tl = tm + ((uint32_t)(warp & 3) << 21);
         if (nc > 0) {
-            tc::mbar_arrive(&r_ready);
-            tc::mbar_arrive(&v_ready);
+            tc::mbar_arrive_warp(&r_ready);
+            tc::mbar_arrive_warp(&v_ready);
         }
 #pragma unroll 1
         for (int c = 0; c < nc; ++c) {
@@ -708,7 +716,7 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
             tc::tmem_ld_wait();
             tc::fence_proxy_async();
             tc::fence_before_sync();
-            if (c + 1 < nc) tc::mbar_arrive(&r_ready);
+            if (c + 1 < nc) tc::mbar_arrive_warp(&r_ready);
             const bool whole = (c + 1) * C <= T;
             if (a.o) {
 #pragma unroll
@@ -734,7 +742,7 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
                     for (int i = 0; i < 4; ++i) store8_bf16(out + 8 * i, o + 8 * i);
                 }
             }
-            if (c + 1 < nc) tc::mbar_arrive(&v_ready);
+            if (c + 1 < nc) tc::mbar_arrive_warp(&v_ready);
             __syncwarp();
         }
         if (tid == 256) tc::bulk_wait_all();
@@ -750,14 +758,16 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
             const float4 x = a.S0 ? *reinterpret_cast<const float4*>(a.S0 + sbase + i) : make_float4(0.f, 0.f, 0.f, 0.f);
             S[i] = x.x; S[i + 1] = x.y; S[i + 2] = x.z; S[i + 3] = x.w;
         }
-        // a chunk's factors are fetched behind the chunk before (the proxy fences wait for loads in flight)
-        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-        float gamma = 0.f;
+        // A chunk's factors are fetched while T R of the chunk before runs: the next proxy fence, which
+        // waits for loads in flight, is then as far as their latency.
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f), fn = f;
+        float gamma = 0.f, gn = 0.f;
         auto fetch = [&](int c) {
             const uint8_t* rec = recs + c * rec_step;
-            f = __ldg(reinterpret_cast<const float4*>(rec + REC_F + row * 16));
-            gamma = __ldg(reinterpret_cast<const float*>(rec + REC_F + C * 16));
+            fn = __ldg(reinterpret_cast<const float4*>(rec + REC_F + row * 16));
+            gn = __ldg(reinterpret_cast<const float*>(rec + REC_F + C * 16));
         };
+        if (nc > 0) fetch(0);
         // R = beta (v - e^g rk K S) of chunk c; the values' place is zero again afterwards
         float x[16], y[16];
         auto form_r = [&](int c) {
@@ -784,13 +794,13 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
             store_split(sm + S_R, row, w, x);
             tc::fence_proxy_async();
             tc::fence_before_sync();
-            tc::mbar_arrive(&r_ready);
+            tc::mbar_arrive_warp(&r_ready);
         };
         auto give_s = [&] {
             store_split(sm + S_S, row, w, S);
             tc::fence_proxy_async();
             tc::fence_before_sync();
-            tc::mbar_arrive(&s_ready);
+            tc::mbar_arrive_warp(&s_ready);
         };
         // The loop turns over while T R runs: from R of one chunk to R of the next.
 #pragma unroll 1
@@ -822,7 +832,7 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
                 store_split(sm + S_R, row, w, x);
                 tc::fence_proxy_async();
                 tc::fence_before_sync();
-                tc::mbar_arrive(&v_ready);
+                tc::mbar_arrive_warp(&v_ready);
                 // S <- e^{g_C} S + K^T V''
                 wait_go(&kv_done, ph, limit, abort);
                 __syncwarp();
@@ -835,8 +845,10 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
             }
             if (i < nc) {
                 give_s();
-                fetch(i);
+                f = fn;
+                gamma = gn;
                 form_r(i);
+                if (i + 1 < nc) fetch(i + 1);
             }
         }
         if (a.S_T) {
@@ -858,6 +870,8 @@ static long count_chunks(const kda_gdn_prefill_args& a) {
     return s;
 }
 
+cudaError_t launch_recurrent(const kda_gdn_prefill_args& a, cudaStream_t s);
+
 size_t chunked_workspace_size(const kda_gdn_prefill_args& a) {
     return WS_HEAD + (size_t)count_chunks(a) * a.Hv * REC;
 }
@@ -867,7 +881,22 @@ cudaError_t launch_chunked(const kda_gdn_prefill_args& a, cudaStream_t s) {
     p.a = a;
     p.chunks = count_chunks(a);
     p.wait_limit = wait_limit();
+    p.ordered = a.num_seqs > 1 && a.num_seqs <= MAX_ORDER;
+    if (p.ordered) {
+        const int32_t* cu = a.cu_seqlens_host;
+        for (int n = 0; n < a.num_seqs; ++n) p.order[n] = (uint16_t)n;
+        std::stable_sort(p.order, p.order + a.num_seqs,
+                         [cu](uint16_t x, uint16_t y) { return cu[x + 1] - cu[x] > cu[y + 1] - cu[y]; });
+    }
     cudaError_t e = cudaMemsetAsync(a.workspace, 0, 4, s);
+    // Only a few tokens per sequence: a chunk takes its two kernels 36 us however full it is, the
+    // recurrence 1 us per token (32 heads); 64 sequences of 16 heads 264 us, and 11 us per token.
+    int longest = 0;
+    for (int n = 0; n < a.num_seqs; ++n) {
+        const int len = a.cu_seqlens_host[n + 1] - a.cu_seqlens_host[n];
+        longest = len > longest ? len : longest;
+    }
+    if (e == cudaSuccess && longest <= 24) return launch_recurrent(a, s);
     CUtensorMap mq = {}, mk = {}, mv = {}, mo = {};
     if (p.chunks > 0) {
         if (e == cudaSuccess) e = make_map_heads(&mq, a.q, DH, a.Hk, a.T_total, (uint64_t)a.Hk * DH, 1, C);

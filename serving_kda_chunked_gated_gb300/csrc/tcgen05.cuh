@@ -303,6 +303,13 @@ TC_DEV void mbar_arrive(uint64_t* mbar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(smem_u32(mbar)) : "memory");
 }
 
+// One arrival for a warp whose lanes have all got here (their earlier writes included): 32
+// arrivals on one word are served one after another.
+TC_DEV void mbar_arrive_warp(uint64_t* mbar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(mbar);
+}
+
 // expect `bytes` more transaction bytes on the mbarrier and arrive once
 TC_DEV void mbar_arrive_expect_tx(uint64_t* mbar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"

@@ -188,11 +188,11 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&s_full[i], 1);
             tc::mbar_init(&turn[i], 1);
-            tc::mbar_init(&p_full[i][0], 128);
-            tc::mbar_init(&p_full[i][1], 128);
+            tc::mbar_init(&p_full[i][0], 4);       // warps
+            tc::mbar_init(&p_full[i][1], 4);
             tc::mbar_init(&o_full[i], 1);
-            tc::mbar_init(&l_full[i], 128);
-            tc::mbar_init(&o_empty[i], 128);
+            tc::mbar_init(&l_full[i], 4);
+            tc::mbar_init(&o_empty[i], 4);
         }
         tc::mbar_init(&drained, 2);
         tc::mbar_fence_init();
@@ -433,7 +433,7 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
                     tc::tmem_ld_wait();
                     if (k == D / 32 - 1) {        // O and l have been read: the next unit may write them
                         tc::fence_before_sync();
-                        tc::mbar_arrive(&o_empty[t]);
+                        tc::mbar_arrive_warp(&o_empty[t]);
                     }
                     if (live) {
 #pragma unroll
@@ -575,14 +575,14 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
                     }
                     tc::tmem_st_wait();
                     tc::fence_before_sync();
-                    tc::mbar_arrive(&p_full[t][0]);
+                    tc::mbar_arrive_warp(&p_full[t][0]);
                     if (64 < width) weigh(2, base, n0, n1);
                     if (96 < width) weigh(3, base, n0, n1);
                     l0 += n0;
                     l1 += n1;
                     tc::tmem_st_wait();
                     tc::fence_before_sync();
-                    tc::mbar_arrive(&p_full[t][1]);
+                    tc::mbar_arrive_warp(&p_full[t][1]);
                     break;
                 }
             }
@@ -590,7 +590,7 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
             if (nu > 0) ok = wait_warp(&o_empty[t], (nu - 1) & 1, limit, abort);   // the last unit's l has been read
             if (!ok) break;
             s_l[t][r] = l0 + l1;
-            tc::mbar_arrive(&l_full[t]);
+            tc::mbar_arrive_warp(&l_full[t]);
             const int q = x.q0 + t * p.qpt + r / p.gp;
             if (p.a.lse && q < x.q1)
                 p.a.lse[(size_t)q * p.a.Hq + x.h0 + r % p.gp] = 0.6931471805599453f * ref + logf(l0 + l1);

@@ -18,7 +18,8 @@ def wait_limit_zero(kda_lib):
     kda.device_error(None)
 
 
-@pytest.mark.parametrize("lens", [[1], [200], [128, 0, 700]])
+# (no sequence longer than 24 tokens: the recurrence, which waits for nothing)
+@pytest.mark.parametrize("lens", [[1, 25], [200], [128, 0, 700]])
 def test_gdn_prefill(kda_lib, cuda_dev, wait_limit_zero, lens):
     import serving_kda_chunked_gated_gb300.kda as kda
     d, cu = gdn_inputs(lens, 1, 2, seed=31)
