@@ -1,0 +1,126 @@
+"""The hybrid stack's mixers as a model runs them: a linear-attention layer (ShortConv +
+Swish, gated delta rule, output gate) and a local softmax layer (per-head norm with
+rotation, windowed attention), on packed prompts, then token by token from the states and
+caches that the prompts left.  The decoded outputs are those of the same layers over the
+whole sequences in 64 bits.
+
+Tolerance: the prompts and the tokens go through the layers in bf16 at the same places
+(convolution, attention and gate outputs), each a rounding of at most 2^-8, on top of the
+layers' own: 1e-2 relative to a head's outputs, six such roundings in quadrature."""
+import pytest
+import torch
+
+from hybrid_testutil import gdn_reference, rel, rope_reference, visible
+
+pytestmark = pytest.mark.gpu
+
+HK, HV, HQ, HKV, D, W, SINKS, CONV = 2, 4, 4, 2, 128, 50, 3, 4
+TOL = 1e-2
+
+
+def _bf(g, *s, scale=1.0):
+    return (scale * torch.randn(*s, generator=g)).to(torch.bfloat16)
+
+
+def _weights(g):
+    C = (2 * HK + HV) * D
+    return dict(conv=torch.randn(C, CONV, generator=g) / CONV, A=torch.log(1 + 7 * torch.rand(HV, generator=g)),
+                qw=1 + 0.1 * torch.randn(D, generator=g), kw=1 + 0.1 * torch.randn(D, generator=g))
+
+
+def _tables(P=4096):
+    f = 1e4 ** (-torch.arange(D // 2, dtype=torch.float64) * 2 / D)
+    a = torch.arange(P, dtype=torch.float64)[:, None] * f
+    return a.cos().float(), a.sin().float()
+
+
+def _linear_reference(x, z, beta, g_in, w):
+    """One sequence: convolution and Swish (rounded to bf16 as the kernel stores them), the rule, the gate."""
+    T = x.shape[0]
+    pad = torch.cat([torch.zeros(CONV - 1, x.shape[1]), x.float()])
+    pre = sum(w["conv"].double()[:, i] * pad[i:i + T].double() for i in range(CONV))
+    y = (pre * torch.sigmoid(pre)).to(torch.bfloat16)
+    q, k, v = (t.unflatten(1, (-1, D)) for t in y.split([HK * D, HK * D, HV * D], 1))
+    o, S = gdn_reference(q, k, v, z, beta, w["A"], [0, T])
+    return o, S, torch.sigmoid(g_in.double()) * o / (o.pow(2).mean(-1, keepdim=True) + 1e-6).sqrt()
+
+
+def _window_reference(x, w, cos, sin):
+    T = x.shape[0]
+    q, k, v = (t.unflatten(1, (-1, D)) for t in x.split([HQ * D, HKV * D, HKV * D], 1))
+    pos = torch.arange(T)
+    q = rope_reference(q, w["qw"], cos, sin, pos, False)[0].to(torch.bfloat16).double()
+    k = rope_reference(k, w["kw"], cos, sin, pos, False)[0].to(torch.bfloat16).double()
+    o = torch.zeros(T, HQ, D, dtype=torch.float64)
+    for t in range(T):
+        j = torch.tensor(visible(t, W, SINKS))
+        for h in range(HQ):
+            s = k[j, h // (HQ // HKV)] @ q[t, h] * D ** -0.5
+            o[t, h] = torch.softmax(s, 0) @ v[j, h // (HQ // HKV)].double()
+    return o
+
+
+def test_prompts_then_tokens(kda_lib, cuda_dev):
+    import serving_kda_chunked_gated_gb300.kda as kda
+    g = torch.Generator().manual_seed(17)
+    w = _weights(g)
+    lens, steps = [140, 1, 67], 5
+    full = [n + steps for n in lens]
+    C = (2 * HK + HV) * D
+    xl = [_bf(g, n, C) for n in full]
+    xw = [_bf(g, n, (HQ + 2 * HKV) * D) for n in full]
+    z = [1.5 * torch.randn(n, HV, generator=g) - 3 for n in full]
+    beta = [torch.sigmoid(torch.randn(n, HV, generator=g)) for n in full]
+    gin = [_bf(g, n, HV, D) for n in full]
+    cos, sin = _tables()
+    dev = lambda t: t.to(cuda_dev)                                                   # noqa: E731
+    cat = lambda ts: dev(torch.cat([t[:n] for t, n in zip(ts, lens)]))               # noqa: E731
+    at = lambda ts, s: dev(torch.stack([t[n + s] for t, n in zip(ts, lens)]))        # noqa: E731
+    cu = torch.tensor([0] + list(torch.tensor(lens).cumsum(0)), dtype=torch.int32)
+    cud, wd = dev(cu), {k: dev(t) for k, t in w.items()}
+    slots = torch.tensor([2, 0, 3], dtype=torch.int32)
+    sd, cosd, sind = dev(slots), dev(cos), dev(sin)
+    N, pool = len(lens), 5
+    conv_pool = torch.zeros(pool, CONV - 1, C, device=cuda_dev)
+    state_pool = torch.zeros(pool, HV, D, D, device=cuda_dev)
+    kc, vc = (torch.zeros(pool, SINKS + W, HKV, D, dtype=torch.bfloat16, device=cuda_dev) for _ in "kv")
+
+    # the prompts
+    y, conv = kda.short_conv(cat(xl), wd["conv"], cu_seqlens=cud)
+    q, k, v = (t.unflatten(1, (-1, D)).contiguous() for t in y.split([HK * D, HK * D, HV * D], 1))
+    o, S = kda.gdn_prefill(q, k, v, cat(z), cat(beta), wd["A"], cu_seqlens=cud, cu_seqlens_host=cu)
+    yl = kda.gate_norm(o, cat(gin))
+    conv_pool[sd.long()], state_pool[sd.long()] = conv, S
+    pos = dev(torch.cat([torch.arange(n, dtype=torch.int32) for n in lens]))
+    split = lambda x: [t.unflatten(1, (-1, D)) for t in x.split([HQ * D, HKV * D, HKV * D], 1)]       # noqa: E731
+    qw, kw, vw = split(cat(xw))
+    qr, kr = kda.qk_norm_rope(qw, kw, cosd, sind, pos, q_weight=wd["qw"], k_weight=wd["kw"])
+    ow = kda.window_prefill(qr, kr, vw, W, SINKS, cu_seqlens=cud, cu_seqlens_host=cu, k_cache=kc, v_cache=vc, slots=sd)
+    got_l, got_w = [yl[cu[n]:cu[n + 1]] for n in range(N)], [ow[cu[n]:cu[n + 1]] for n in range(N)]
+
+    # the tokens
+    for s in range(steps):
+        y = kda.short_conv_step(at(xl, s), wd["conv"], conv_pool, slots=sd)
+        q, k, v = (t.unflatten(1, (-1, D)).contiguous() for t in y.split([HK * D, HK * D, HV * D], 1))
+        o = kda.gdn_decode_step(q, k, v, at(z, s), at(beta, s), wd["A"], state_pool, slots=sd)
+        yl = kda.gate_norm(o, at(gin, s))
+        pos = dev(torch.tensor([n + s for n in lens], dtype=torch.int32))
+        qw, kw, vw = split(at(xw, s))
+        qr, kr = kda.qk_norm_rope(qw, kw, cosd, sind, pos, q_weight=wd["qw"], k_weight=wd["kw"])
+        ow = kda.window_decode(qr, kr, vw, kc, vc, pos, W, SINKS, slots=sd)
+        for n in range(N):
+            got_l[n] = torch.cat([got_l[n], yl[n:n + 1]])
+            got_w[n] = torch.cat([got_w[n], ow[n:n + 1]])
+
+    for n in range(N):
+        _, S, yl = _linear_reference(xl[n], z[n], beta[n], gin[n], w)
+        rw = _window_reference(xw[n], w, cos, sin)
+        for h in range(HV):
+            assert rel(got_l[n][:, h], yl[:, h]) < TOL, (n, h, rel(got_l[n][:, h], yl[:, h]))
+            assert rel(got_l[n][lens[n]:, h], yl[lens[n]:, h]) < TOL
+            # the convolution's bf16 outputs may differ by a step where its float32 sum and the 64-bit
+            # one fall on two sides of a rounding boundary: 2^-8 of single values
+            assert rel(state_pool[slots[n], h], S[0, h]) < 1e-3
+        for h in range(HQ):
+            assert rel(got_w[n][:, h], rw[:, h]) < TOL and rel(got_w[n][lens[n]:, h], rw[lens[n]:, h]) < TOL
+    assert (state_pool[[1, 4]] == 0).all() and (kc[[1, 4]] == 0).all()
