@@ -125,8 +125,10 @@ cudaError_t launch_decode(const kda_gdn_decode_args& a, cudaStream_t stream) {
     const long heads = (long)a.N * a.Hv;
     if (heads == 0) return cudaSuccess;
     // Few heads leave SMs idle and each state waits on one SM's loads: four column
-    // slices of 32 channels then (a row of a slice is still one 128-byte line).
-    if (heads < 2 * 152)
+    // slices of 32 channels then (a row of a slice is still one 128-byte line), while at
+    // most two share an SM.  8 heads 2.6 us sliced, 3.5 whole; 64 heads 3.2, 3.6; 128
+    // heads 4.3, 3.7; 512 heads 10.4, 9.8.
+    if (heads * 4 <= 2 * 152)
         gdn_decode_kernel<32><<<(unsigned)(heads * 4), NT, 0, stream>>>(a);
     else
         gdn_decode_kernel<128><<<(unsigned)heads, NT, 0, stream>>>(a);

@@ -85,7 +85,8 @@ qk_norm_rope_kernel(kda_qk_norm_rope_args a, int groups) {
     const int H = a.Hq + a.Hkv;
     const long g = ((long)blockIdx.x * NT + threadIdx.x) / LANES;     // lane group = (token, HPG heads)
     const int l = threadIdx.x % LANES;
-    const int t = (int)(g / groups), h0 = (int)(g % groups) * HPG;
+    const long t = g / groups;
+    const int h0 = (int)(g % groups) * HPG;
     const bool have = t < a.T;            // every lane stays for the shuffles
     const int pos = have ? __ldg(a.positions + t) : -1;
     const int half = a.rot >> 1;
@@ -163,10 +164,12 @@ static cudaError_t go(const kda_qk_norm_rope_args& a, cudaStream_t s) {
 }
 template <bool BF16, bool PAIRS, int LANES>
 static cudaError_t by_heads(const kda_qk_norm_rope_args& a, cudaStream_t s) {
-    // Several heads per lane group share the token's cosines and sines; where that
-    // would leave threads idle (fewer than two full waves of them), one head each.
+    // Several heads per lane group share the token's cosines and sines; where that would
+    // leave SMs short of threads (less than one full wave of them with a head each), one
+    // head each.  40 heads of 128, bf16: 64 tokens 2.0 us by ones, 3.1 by fives; 512
+    // tokens 3.8 both; 1024 tokens 5.9, 5.1; 16384 tokens 82.6, 60.2.
     const int H = a.Hq + a.Hkv;
-    if ((long)a.T * H * LANES < 4L * 2 * 152 * 2048) return go<BF16, PAIRS, LANES, 1>(a, s);
+    if ((long)a.T * H * LANES < 152L * 2048) return go<BF16, PAIRS, LANES, 1>(a, s);
     // 4, 5 or 6, whichever leaves the fewest of a token's lane groups' places empty (8 need
     // more registers than they save time)
     const int idle4 = (4 - H % 4) % 4, idle5 = (5 - H % 5) % 5, idle6 = (6 - H % 6) % 6;

@@ -13,6 +13,8 @@
 
 #include <math.h>
 
+#include <atomic>
+
 namespace kda {
 namespace win {
 
@@ -83,7 +85,7 @@ window_decode_kernel(kda_window_decode_args a, int mtiles) {
     const int R = a.cache_rows - a.sinks;
     // visible rows: the first `ns` sinks, then the ring from position `first` on
     const int first = max(a.sinks, pos - a.window + 1);
-    const int ns = min(a.sinks, pos + 1);
+    const int ns = pos < a.sinks ? pos + 1 : a.sinks;
     const int total = ns + max(0, pos - first + 1);
     const int ring0 = pos >= a.sinks ? (first - a.sinks) % R : 0;
     const size_t rstride = (size_t)a.Hkv * D;
@@ -274,28 +276,62 @@ window_decode_kernel(kda_window_decode_args a, int mtiles) {
     cluster_sync();                                       // no CTA leaves while its shared memory is read
 }
 
+// CTAs of a cluster at most (the portable size) and devices whose counts are kept
+constexpr int DEC_SPLIT = 8, DEC_DEVICES = 64;
+
+template <int D>
+static void decode_shape(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, long units, int split, cudaStream_t s) {
+    *cfg = {};
+    cfg->gridDim = dim3((unsigned)(units * split));
+    cfg->blockDim = dim3(DEC_WARPS * 32);
+    cfg->dynamicSmemBytes = dec_smem<D>();
+    cfg->stream = s;
+    attr->id = cudaLaunchAttributeClusterDimension;
+    attr->val.clusterDim.x = split;
+    attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+    cfg->attrs = attr;
+    cfg->numAttrs = 1;
+}
+
+// How many clusters of `split` CTAs the current device holds at once: a property of the
+// device (clusters stay inside a group of SMs, and groups differ in size), asked once.
+template <int D>
+static cudaError_t resident_clusters(int split, int* count) {
+    static std::atomic<int> held[DEC_DEVICES][DEC_SPLIT + 1];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool keep = dev < DEC_DEVICES;
+    if (keep && (*count = held[dev][split].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr;
+    decode_shape<D>(&cfg, &attr, 1, split, nullptr);
+    e = cudaOccupancyMaxActiveClusters(count, window_decode_kernel<D>, &cfg);
+    if (e == cudaSuccess && keep) held[dev][split].store(*count, std::memory_order_relaxed);
+    return e;
+}
+
 template <int D>
 static cudaError_t decode_d(const kda_window_decode_args& a, cudaStream_t s) {
     const int mtiles = (a.Hq / a.Hkv + 15) / 16;
     const long units = (long)a.N * a.Hkv * mtiles;
-    // CTAs per (sequence, key head): enough to give every SM one, at most the portable
-    // cluster of 8, and never more than there are 16-key tiles for their warps.
-    const long most = ((long)a.sinks + a.window + DEC_KEYS * DEC_WARPS - 1) / (DEC_KEYS * DEC_WARPS);
-    int split = 1;
-    while (split < 8 && units * split < 152 && split < most) split *= 2;
     cudaError_t e = cudaFuncSetAttribute(window_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, dec_smem<D>());
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(units * split));
-    cfg.blockDim = dim3(DEC_WARPS * 32);
-    cfg.dynamicSmemBytes = dec_smem<D>();
-    cfg.stream = s;
+    // CTAs per (sequence, key head): as many as leave all clusters resident at once, at most one
+    // per 16-key tile of each warp.  Window of 4096, d = 128, us: 14 units 30.2 alone, 12.3 by
+    // fours, 9.6 by eights; 36 units 30.6, 12.9, but 27.0 by eights, whose clusters then come
+    // in turns; 100 units 35.6, 45.4 by twos.
+    const long most = ((long)a.sinks + a.window + DEC_KEYS * DEC_WARPS - 1) / (DEC_KEYS * DEC_WARPS);
+    int split = 1;
+    for (int c = DEC_SPLIT; c > 1 && split == 1; --c) {
+        if (c > most || units * c > 152) continue;
+        int fit = 0;
+        if ((e = resident_clusters<D>(c, &fit)) != cudaSuccess) return e;
+        if (units <= fit) split = c;
+    }
+    cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = split;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    decode_shape<D>(&cfg, &attr, units, split, s);
     e = cudaLaunchKernelEx(&cfg, window_decode_kernel<D>, a, mtiles);
     if (e != cudaSuccess) return e;
     count_launches(1);

@@ -181,3 +181,27 @@ def test_decode_long_window_split_over_ctas(kda_lib, cuda_dev):
         s = torch.einsum("hd,kd->hk", q[0].double(), K[rows, 0].double()) * d ** -0.5
         w = torch.softmax(s, -1)
         check_window(o, (w @ V[rows, 0].double())[None], (w @ V[rows, 0].double().abs())[None], f"position {pos}")
+
+
+@pytest.mark.parametrize("N", [11, 15, 20, 24, 33, 40, 60, 77])
+def test_decode_any_cluster_size(kda_lib, cuda_dev, N):
+    """Batch sizes that give each sequence from eight CTAs down to one, at positions up to the last int32."""
+    import serving_kda_chunked_gated_gb300.kda as kda
+    W, sinks, Hq, Hkv, d = 1100, 2, 3, 1, 64
+    g = torch.Generator().manual_seed(N)
+    kc, vc = (torch.randn(N, W + sinks, Hkv, d, generator=g).to(torch.bfloat16) for _ in "kv")
+    q, k, v = (torch.randn(N, h, d, generator=g).to(torch.bfloat16) for h in (Hq, Hkv, Hkv))
+    pos = torch.randint(0, 4000, (N,), generator=g, dtype=torch.int32)
+    pos[0], pos[1], pos[2] = 2 ** 31 - 1, 0, 1
+    kd, vd = kc.to(cuda_dev), vc.to(cuda_dev)
+    o = kda.window_decode(q.to(cuda_dev), k.to(cuda_dev), v.to(cuda_dev), kd, vd, pos.to(cuda_dev), W, sinks)
+    ro, size = torch.empty(N, Hq, d, dtype=torch.float64), torch.empty(N, Hq, d, dtype=torch.float64)
+    for n in range(N):
+        row = lambda p: p if p < sinks else sinks + (p - sinks) % W                          # noqa: E731
+        p = int(pos[n])
+        kc[n, row(p)], vc[n, row(p)] = k[n], v[n]
+        rows = torch.tensor([row(j) for j in visible(p, W, sinks)])
+        w = torch.softmax(torch.einsum("hd,kd->hk", q[n].double(), kc[n, rows, 0].double()) * d ** -0.5, -1)
+        ro[n], size[n] = w @ vc[n, rows, 0].double(), w @ vc[n, rows, 0].double().abs()
+    check_window(o, ro, size, f"{N} sequences")
+    assert torch.equal(kd.cpu(), kc) and torch.equal(vd.cpu(), vc)
