@@ -435,7 +435,8 @@ kda_status kda_kcp_apply(const float* M, float* X, const float* add, int H, int 
  * float32: the per-token recurrence on CUDA cores, no workspace.
  * kda_gdn_prefill_recurrent: the per-token recurrence for either type.
  * Rows of o outside every sequence do not exist (cu_seqlens ends at T_total);
- * non-finite values of one sequence never reach another.
+ * non-finite values of one sequence never reach another (within one, they may reach
+ * earlier tokens of their 128-token chunk in kda_gdn_prefill).
  */
 typedef struct {
     int num_seqs;
@@ -508,7 +509,8 @@ kda_status kda_gdn_decode_step(const kda_gdn_decode_args* args, void* stream);
  * A token whose position lies outside [0, num_pos) is skipped: its output rows
  * are left as they were.
  * Supported: d a multiple of 8 up to 256; rot a multiple of 16, 16 <= rot <= d;
- * Hq, Hkv >= 0, not both 0; strides multiples of 16 bytes and >= heads * d.
+ * Hq, Hkv >= 0, not both 0, 2^20 together at most; strides multiples of 16 bytes and
+ * >= heads * d.
  */
 typedef struct {
     int T, Hq, Hkv, d, rot, num_pos;
@@ -542,15 +544,17 @@ kda_status kda_qk_norm_rope(const kda_qk_norm_rope_args* args, void* stream);
  * [cu_seqlens_k[n], cu_seqlens_k[n+1]); its queries are the last of its keys
  * (a prompt resumed after earlier tokens has more keys than queries), so it has
  * at least as many keys as queries, else KDA_ERR_SEQLENS.  Keys and values that
- * no query sees are never used, whatever they hold.
+ * no query sees are never used, whatever they hold.  A non-finite value that some
+ * query of a sequence sees may also reach outputs of queries near it that do not (a
+ * weight of 0 times it); other sequences it never reaches.
  *
  * Caches (optional, k_cache and v_cache together): [num_slots, cache_rows, Hkv, d]
  * bf16, cache_rows >= sinks + window.  Position p of a sequence lives in row
  *   p                                        for p < sinks,
  *   sinks + (p - sinks) mod (cache_rows - sinks)  otherwise;
  * sequence n writes the rows that kda_window_decode will read: its first
- * min(sinks, len) and its last `window` positions, into slot slots[n] (or n).  Other
- * rows keep what they held.  A slot outside [0, num_slots) is skipped.
+ * min(sinks, len) and its last `window` positions, into slot slots[n] (or n; distinct).
+ * Other rows keep what they held.  A slot outside [0, num_slots) is skipped.
  * The caches must not overlap any other argument.
  */
 typedef struct {

@@ -126,7 +126,8 @@ kda_status kda_qk_norm_rope(const kda_qk_norm_rope_args* a, void* stream) {
     if (any_misaligned({a->q, a->k, (const void*)a->q_weight, (const void*)a->k_weight, (const void*)a->cos,
                         (const void*)a->sin, (const void*)a->positions, (const void*)a->q_out, (const void*)a->k_out}))
         return KDA_ERR_ALIGN;
-    if ((double)a->T * (a->Hq + a->Hkv) / 8 > (double)MAX_BLOCKS) return KDA_ERR_SHAPE;
+    // the kernel counts heads, and (token, four or more heads), in 32 bits
+    if ((long)a->Hq + a->Hkv > 1L << 20 || (long)a->T * ((a->Hq + 3) / 4 + (a->Hkv + 3) / 4) > MAX_BLOCKS) return KDA_ERR_SHAPE;
     return done(kda::qknr::launch(*a, reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -21,6 +21,13 @@
 // scan: one CTA per (sequence, value head, 32 value columns) walks the chunks.  Tokens (or
 // key channels) are TMEM lanes, the 32 columns of an operand's hi and lo parts one
 // 128-byte row of 64 MN-major elements: one N = 64 MMA forms both products.
+//
+// Neither is near HBM: prep is bound by the issue and latency of the inverse (some 19000 cycles
+// of an SM per chunk and value head), the scan by its chain K S -> R -> T R -> V'' -> K^T V'' -> S,
+// some 4550 cycles a chunk of which 1450 are MMAs, 1600 the rows' arithmetic and 1300 the
+// hand-overs between them; 32 columns rather than 64 or 128 because 32 heads then fill 128 SMs.
+// Measured: 131072 tokens, 16 key and 32 value heads, S0: 4.29 ms (30.5 M tokens/s); 8192
+// tokens, 32 / 32 heads: 0.30 ms, one half prep and one half scan.
 #include <math.h>
 
 #include <algorithm>
@@ -124,7 +131,7 @@ KDA_DEV void split_tf32(float x, float* hi, float* lo) {
 // matrices in shared memory, by one warp: float32 operands as two tf32 parts each, the product
 // of the low parts left out.  (Two bf16 parts would leave 2^-17, which the inverse of strongly
 // correlated keys amplifies to 2e-5 of the state; as float32 FMAs the tiles are bound by
-// shared-memory reads, 3700 cycles for the 64 x 64 product against 1100 here.)  Within each
+// shared-memory reads, 3700 cycles for the 64 x 64 products against some 2800 here.)  Within each
 // step of 8, k is taken in the order 0, 2, 4, 6, 1, 3, 5, 7, so that a lane's two values of L
 // are neighbours.  Six independent accumulators: the steps wait for nothing but their loads.
 KDA_DEV void tile_product(float* out, int os, float sign, const float* Lm, int ls, const float* Rm, int rs, int nk, int lane) {
@@ -623,8 +630,8 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
         }
     } else if (warp == 13) {
         // ---------------- MMAs: the warp computes together, one lane issues ----------------
-        // Per chunk 48 MMAs of some 70 cycles whatever their N: K S, T R and K^T V'' on the chain
-        // from state to state, Q S and (masked Q K^T) V' in the gaps that the rows' arithmetic leaves.
+        // Per chunk 48 MMAs of 41 (N = 32) or 47 (N = 64) cycles: K S, T R and K^T V'' on the chain from
+        // state to state, Q S and (masked Q K^T) V' in the gaps that the rows' arithmetic leaves.
         const uint32_t tmu = __shfl_sync(~0u, tm, 0), sb = __shfl_sync(~0u, tc::smem_u32(sm), 0);
         const uint32_t id64 = tc::idesc_bf16(128, 64, false, true), id32 = tc::idesc_bf16(128, 32, false, true),
                        idt = tc::idesc_bf16(128, 64, true, true);

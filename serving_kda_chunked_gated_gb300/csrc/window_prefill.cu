@@ -22,7 +22,15 @@
 //
 // V is the B operand straight from the TMA tile (MN-major), Q and K are K-major; no
 // thread touches an operand but for zeroing the unseen rows of edge tiles (0 x NaN).
+//
+// Two bounds meet: a round (both tiles' P V and Q K^T, d = 128) keeps the tensor core busy for
+// 2068 cycles, and its 2 x 128 x 128 exponentials the special-function units (16 a cycle) for
+// 2048.  Measured: 8192 tokens, 32 / 8 heads of 128, window 4096: 350 us, some 3800 cycles a
+// round (TMEM reads slow down while products run), 1.17 PFLOP/s; 131072 tokens, window 512:
+// 1.46 ms, where a unit has 5 rounds and its change (queries in, rows out) costs 5000 cycles.
 #include <math.h>
+
+#include <algorithm>
 
 #include "kda_common.cuh"
 #include "tcgen05.cuh"
@@ -294,7 +302,7 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
             const int t = warp - 13;
             uint32_t rd = 0, nu = 0, np = 0;       // rounds, units, softmax steps
             bool ok = true;
-                const uint32_t ra = uniform(tc::smem_u32(ring)), tmu = uniform(tm);
+            const uint32_t ra = uniform(tc::smem_u32(ring)), tmu = uniform(tm);
             const uint64_t qd = tc::sw128_desc(uniform(tc::smem_u32(sq)) + t * L::QB);
             auto qk = [&](uint32_t slot, int width) {
                 const uint32_t id = tc::idesc_bf16(128, width, false, false, p.neg != 0);
@@ -605,6 +613,7 @@ template <int D>
 static cudaError_t prefill_d(const kda_window_prefill_args& a, cudaStream_t s) {
     PfParams p;
     p.a = a;
+    p.a.window = std::min(a.window, a.Tk_total);       // as wide as any sequence: sums of positions stay in 32 bits
     const int G = a.Hq / a.Hkv;
     p.gp = G & -G;
     if (p.gp > 16) p.gp = 16;

@@ -107,7 +107,7 @@ def test_gdn_decode_refusals(kda_lib, kw, expect):
     (dict(rot=144), SHAPE), (dict(Hq=0, Hkv=0), SHAPE), (dict(Hq=-1), SHAPE), (dict(T=-1), SHAPE), (dict(num_pos=-1), SHAPE),
     (dict(q_stride=511), SHAPE), (dict(k_stride=100), SHAPE), (dict(q_stride=516), ALIGN), (dict(k=FAKE + 2), ALIGN),
     (dict(sin=FAKE + 4), ALIGN), (dict(dtype=7), DTYPE), (dict(q_out=FAKE, q_stride=1024), SHAPE),
-    (dict(T=1 << 30, Hq=1 << 10, q_stride=1 << 18), SHAPE),
+    (dict(T=1 << 30, Hq=1 << 10, q_stride=1 << 18), SHAPE), (dict(T=1, Hq=1 << 20, q_stride=1 << 27), SHAPE),
 ])
 def test_qk_norm_rope_refusals(kda_lib, kw, expect):
     a = _fill(_kda().QkNormRopeArgs(), T=5, Hq=4, Hkv=2, d=128, rot=128, num_pos=9, q_stride=512, k_stride=256, eps=1e-6,
