@@ -9,7 +9,7 @@
 // keeps STAGES tiles in flight.  Warps are merged through shared memory, CTAs that
 // share a (sequence, key head) through distributed shared memory of their cluster:
 // no workspace and no second launch.  256 sequences x 8 key heads of 128, window
-// 4096: 4.3 GB in 552 us, 7.8 TB/s.
+// 4096: 4.1 GB in 560 us, 7.3 TB/s (reads alone run above a copy's rate).
 #include "kda_common.cuh"
 
 #include <math.h>
