@@ -430,8 +430,9 @@ kda_status kda_kcp_apply(const float* M, float* X, const float* add, int H, int 
  * sequence has more than 24 tokens, the recurrence, which is faster there); the
  * workspace must hold kda_gdn_prefill_workspace_size() bytes, else
  * KDA_ERR_WORKSPACE.  Its first 4 bytes are the call's error word, read with
- * kda_get_last_device_error.  Final states carry float32 precision: every
- * product that reaches them splits its float32 operand into two bf16 parts.
+ * kda_get_last_device_error.  Every product that reaches a final state splits its
+ * float32 operand into two bf16 parts: states are within some 4e-6 of exact ones
+ * (relative L2), o within bf16 roundings of its weights, values and itself.
  * float32: the per-token recurrence on CUDA cores, no workspace.
  * kda_gdn_prefill_recurrent: the per-token recurrence for either type.
  * Rows of o outside every sequence do not exist (cu_seqlens ends at T_total);
