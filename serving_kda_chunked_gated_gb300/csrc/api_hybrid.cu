@@ -54,7 +54,7 @@ kda_status check(const kda_gdn_prefill_args* a) {
     if (a->qkv_dtype != KDA_BF16 && a->qkv_dtype != KDA_F32) return KDA_ERR_DTYPE;
     if (!a->cu_seqlens || !a->cu_seqlens_host || !a->A) return KDA_ERR_NULL;
     if (a->T_total > 0 && (!a->q || !a->k || !a->v || !a->z || !a->beta)) return KDA_ERR_NULL;
-    if (!a->o && !a->S_T) return KDA_ERR_NULL;
+    if (a->T_total > 0 && !a->o && !a->S_T) return KDA_ERR_NULL;
     if (any_misaligned({a->cu_seqlens, a->q, a->k, a->v, (const void*)a->z, (const void*)a->beta, (const void*)a->A,
                         (const void*)a->S0, a->o, (const void*)a->S_T}))
         return KDA_ERR_ALIGN;
@@ -78,7 +78,7 @@ size_t kda_gdn_prefill_workspace_size(const kda_gdn_prefill_args* a) {
 kda_status kda_gdn_prefill(const kda_gdn_prefill_args* a, void* stream) {
     const kda_status st = check(a);
     if (st != KDA_OK) return st;
-    if (a->num_seqs == 0) return KDA_OK;
+    if (a->num_seqs == 0 || (!a->o && !a->S_T)) return KDA_OK;      // no tokens and no state asked for
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (a->qkv_dtype == KDA_F32) return done(kda::gdn::launch_recurrent(*a, s));
     if (!a->workspace || a->workspace_bytes < kda::gdn::chunked_workspace_size(*a)) return KDA_ERR_WORKSPACE;

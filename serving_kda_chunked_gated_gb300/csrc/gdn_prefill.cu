@@ -55,23 +55,36 @@ constexpr int REC_THI = 0, REC_TLO = TRI, REC_A = 2 * TRI, REC_F = 3 * TRI;
 constexpr int REC = 3 * TRI + C * 16 + 128;   // + four factors per token + e^{g_C}
 constexpr int WS_HEAD = 256;                  // the error word's line
 
-// Scans of the longest sequences start first: with one of 4097 tokens among eight shorter ones it
-// otherwise starts when these are done.  The order is the host's, by value, for up to this many.
-constexpr int MAX_ORDER = 1024;
+// For up to this many sequences the host lays the work out, by value.  Scans of the longest start
+// first: one of 4097 tokens among eight shorter ones otherwise starts when these are done.
+// Beyond, every CTA adds up cu_seqlens itself.
+constexpr int MAX_LISTED = 1024;
 
 struct Params {
     kda_gdn_prefill_args a;
-    long chunks;
     uint32_t wait_limit;
-    int ordered;
-    uint16_t order[MAX_ORDER];
+    int listed;                               // whether what follows is filled in
+    uint32_t first[MAX_LISTED + 1];           // chunks before sequence n
+    uint16_t order[MAX_LISTED];               // sequences, longest first
 };
 
 // byte offset of 16-byte piece c (0 .. 7) of row r in a slab of 128-byte rows
 KDA_DEV uint32_t swz(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 
 // Sequence and position of chunk `idx`, counted over the sequences; by whole warps.
-KDA_DEV void chunk_at(const kda_gdn_prefill_args& a, long idx, int* seq, int* chunk) {
+KDA_DEV void chunk_at(const Params& p, long idx, int* seq, int* chunk) {
+    const kda_gdn_prefill_args& a = p.a;
+    if (p.listed) {
+        int lo = 0, hi = a.num_seqs;          // the last sequence with first <= idx (empty ones come before it)
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (p.first[mid] <= (uint32_t)idx) lo = mid;
+            else hi = mid;
+        }
+        *seq = lo;
+        *chunk = (int)(idx - p.first[lo]);
+        return;
+    }
     const int lane = threadIdx.x & 31;
     for (int base = 0; base < a.num_seqs; base += 32) {
         const int m = base + lane;
@@ -97,7 +110,9 @@ KDA_DEV void chunk_at(const kda_gdn_prefill_args& a, long idx, int* seq, int* ch
 }
 
 // chunks of the sequences before n; by whole warps
-KDA_DEV long chunks_before(const kda_gdn_prefill_args& a, int n) {
+KDA_DEV long chunks_before(const Params& p, int n) {
+    if (p.listed) return p.first[n];
+    const kda_gdn_prefill_args& a = p.a;
     long s = 0;
     for (int m = threadIdx.x & 31; m < n; m += 32) s += (a.cu_seqlens[m + 1] - a.cu_seqlens[m] + C - 1) / C;
 #pragma unroll
@@ -188,7 +203,7 @@ gdn_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
     const int hk = blockIdx.x % a.Hk, rep = a.Hv / a.Hk;
     const long idx = blockIdx.x / a.Hk;
     int n, ch;
-    chunk_at(a, idx, &n, &ch);
+    chunk_at(p, idx, &n, &ch);
     const int t0 = a.cu_seqlens[n] + ch * C, len = min(C, a.cu_seqlens[n + 1] - t0);
     const bool live = row < len;
 
@@ -521,7 +536,7 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int slice = blockIdx.x % (DH / COLS);
     const int h = blockIdx.x / (DH / COLS) % a.Hv;
-    const int place = blockIdx.x / (DH / COLS) / a.Hv, n = p.ordered ? p.order[place] : place;
+    const int place = blockIdx.x / (DH / COLS) / a.Hv, n = p.listed ? p.order[place] : place;
     const int hk = h / (a.Hv / a.Hk);
     const int t0 = a.cu_seqlens[n], T = a.cu_seqlens[n + 1] - t0;
     const int nc = (T + C - 1) / C;
@@ -550,7 +565,7 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tm = s_tmem;
-    const long base = chunks_before(a, n);
+    const long base = chunks_before(p, n);
     const uint8_t* recs = reinterpret_cast<const uint8_t*>(a.workspace) + WS_HEAD + (base * a.Hv + h) * (size_t)REC;
     const size_t rec_step = (size_t)a.Hv * REC;
 
@@ -890,12 +905,16 @@ size_t chunked_workspace_size(const kda_gdn_prefill_args& a) {
 cudaError_t launch_chunked(const kda_gdn_prefill_args& a, cudaStream_t s) {
     Params p;
     p.a = a;
-    p.chunks = count_chunks(a);
     p.wait_limit = wait_limit();
-    p.ordered = a.num_seqs > 1 && a.num_seqs <= MAX_ORDER;
-    if (p.ordered) {
+    const long chunks = count_chunks(a);
+    p.listed = a.num_seqs <= MAX_LISTED;
+    if (p.listed) {
         const int32_t* cu = a.cu_seqlens_host;
-        for (int n = 0; n < a.num_seqs; ++n) p.order[n] = (uint16_t)n;
+        p.first[0] = 0;
+        for (int n = 0; n < a.num_seqs; ++n) {
+            p.first[n + 1] = p.first[n] + (uint32_t)((cu[n + 1] - cu[n] + C - 1) / C);
+            p.order[n] = (uint16_t)n;
+        }
         std::stable_sort(p.order, p.order + a.num_seqs,
                          [cu](uint16_t x, uint16_t y) { return cu[x + 1] - cu[x] > cu[y + 1] - cu[y]; });
     }
@@ -909,14 +928,14 @@ cudaError_t launch_chunked(const kda_gdn_prefill_args& a, cudaStream_t s) {
     }
     if (e == cudaSuccess && longest <= 24) return launch_recurrent(a, s);
     CUtensorMap mq = {}, mk = {}, mv = {}, mo = {};
-    if (p.chunks > 0) {
+    if (chunks > 0) {
         if (e == cudaSuccess) e = make_map_heads(&mq, a.q, DH, a.Hk, a.T_total, (uint64_t)a.Hk * DH, 1, C);
         if (e == cudaSuccess) e = make_map_heads(&mk, a.k, DH, a.Hk, a.T_total, (uint64_t)a.Hk * DH, 1, C);
         if (e == cudaSuccess) e = make_map_heads(&mv, a.v, DH, a.Hv, a.T_total, (uint64_t)a.Hv * DH, 1, C, COLS);
         if (e == cudaSuccess && a.o) e = make_map_heads(&mo, a.o, DH, a.Hv, a.T_total, (uint64_t)a.Hv * DH, 1, C, COLS);
         if (e == cudaSuccess) e = cudaFuncSetAttribute(gdn_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, P_SMEM);
         if (e != cudaSuccess) return e;
-        gdn_prep_kernel<<<(unsigned)(p.chunks * a.Hk), PT, P_SMEM, s>>>(p, mq, mk);
+        gdn_prep_kernel<<<(unsigned)(chunks * a.Hk), PT, P_SMEM, s>>>(p, mq, mk);
         count_launches(1);
         e = cudaGetLastError();
     }

@@ -96,15 +96,20 @@ struct Unit {
     }
 };
 
-KDA_DEV Unit unit_at(const PfParams& p, long u) {
-    u = p.units - 1 - u;
+// A place in the list of query blocks: the 32 sequences from `base` on, with `behind` blocks in the
+// sequences after them.  It moves with the units: none is before the last one.
+struct Place {
+    int base, behind;
+};
+
+KDA_DEV Unit unit_at(const PfParams& p, long u, Place& at) {
     const int heads = p.a.Hkv * p.subs;
-    const int hs = (int)(u % heads);
-    long b = u / heads;                     // block of 2 qpt queries, counted over the sequences
+    const int hs = heads - 1 - (int)(u % heads);
+    const long back = u / heads;            // blocks of 2 qpt queries behind this one, over all sequences
     const int lane = threadIdx.x & 31, per = 2 * p.qpt;
-    int n = 0;
-    for (int base = 0;; base += 32) {       // 32 sequences at a time; ends: u < units
-        const int m = base + lane;
+    int n = 0, b = 0;                       // sequence, block in it
+    for (;;) {                              // ends: u < units
+        const int m = at.base + lane;
         const int len = m < p.a.num_seqs ? p.a.cu_seqlens[m + 1] - p.a.cu_seqlens[m] : 0;
         int pre = (len + per - 1) / per;
 #pragma unroll
@@ -112,24 +117,26 @@ KDA_DEV Unit unit_at(const PfParams& p, long u) {
             const int x = __shfl_up_sync(~0u, pre, o);
             if (lane >= o) pre += x;
         }
-        const unsigned hit = __ballot_sync(~0u, b < pre);
-        if (hit) {
-            const int f = __ffs(hit) - 1;
+        const int all = __shfl_sync(~0u, pre, 31);
+        if (back < (long)at.behind + all || at.base == 0) {
+            b = all - 1 - (int)(back - at.behind);
+            const unsigned hit = __ballot_sync(~0u, b < pre);
+            const int f = hit ? __ffs(hit) - 1 : 0;
             const int before = __shfl_sync(~0u, pre, f > 0 ? f - 1 : 0);
             if (f > 0) b -= before;
-            n = base + f;
+            n = at.base + f;
             break;
         }
-        b -= __shfl_sync(~0u, pre, 31);
-        if (base + 32 >= p.a.num_seqs) break;
+        at.behind += all;
+        at.base -= 32;
     }
     Unit x;
     const int c0 = p.a.cu_seqlens[n], c1 = p.a.cu_seqlens[n + 1];
     x.k0 = p.a.cu_seqlens_k[n];
     const int lk = p.a.cu_seqlens_k[n + 1] - x.k0;
-    x.q0 = c0 + (int)b * per;
+    x.q0 = c0 + b * per;
     x.q1 = min(c1, x.q0 + per);
-    x.p0 = lk - (c1 - c0) + (int)b * per;
+    x.p0 = lk - (c1 - c0) + b * per;
     x.hi = x.p0 + (x.q1 - x.q0) - 1;
     x.lo = max(0, x.p0 - p.a.window + 1);
     x.nsink = min(p.a.sinks, x.lo);
@@ -223,8 +230,9 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
             // ---------------- loads: Q of a unit, then K and V tiles through the ring ----------------
             uint32_t it = 0, edges = 0, nu = 0, nq = 0;     // items, zeroed tiles, units, Q loads so far
             bool ok = true, direct = true;         // direct: the last item counts on its round's barrier
+            Place place = {(p.a.num_seqs - 1) & ~31, 0};
             for (long u = blockIdx.x; u < p.units && ok; u += gridDim.x, ++nu) {
-                const Unit x = unit_at(p, u);
+                const Unit x = unit_at(p, u, place);
                 for (int i = 0; i < x.ntiles && ok; ++i) {
                     int j0, width;
                     x.tile(i, &j0, &width);

@@ -187,3 +187,30 @@ def test_decode_skips_slots_out_of_range_and_follows_prefill(kda_lib, cuda_dev):
     assert torch.equal(S, before) and (out == 3.0).all()
     o = kda.gdn_decode_step(**x, A=g["A"], state=S)
     _check(o, S, ro[at[0]], rS, lens)
+
+
+def test_prefill_many_sequences(kda_lib, cuda_dev):
+    """More sequences than the host lists for the kernels, empty ones and one of two chunks among them."""
+    import serving_kda_chunked_gated_gb300.kda as kda
+    for n in (1024, 1025):
+        lens = [(7 * i) % 13 for i in range(n)]
+        lens[n // 2], lens[-1], lens[0] = 131, 0, 30
+        d, cu = gdn_inputs(lens, 1, 1, seed=n)
+        d.pop("S0")
+        ro, rS = gdn_reference(**d, cu=cu)
+        o, S = kda.gdn_prefill(**_dev(d, cuda_dev), cu_seqlens=cu.to(cuda_dev), cu_seqlens_host=cu)
+        _check(o, S, ro, rS, lens)
+
+
+def test_prefill_no_tokens(kda_lib, cuda_dev):
+    """Only empty sequences: the states pass through, or nothing is asked for."""
+    import serving_kda_chunked_gated_gb300.kda as kda
+    bf, e = torch.bfloat16, lambda *s, dt=torch.float32: torch.empty(*s, dtype=dt, device=cuda_dev)     # noqa: E731
+    cu = torch.zeros(4, dtype=torch.int32)
+    q, k, v = e(0, 2, 128, dt=bf), e(0, 2, 128, dt=bf), e(0, 4, 128, dt=bf)
+    S0 = torch.randn(3, 4, 128, 128, device=cuda_dev)
+    for rec in (False, True):
+        args = (q, k, v, e(0, 4), e(0, 4), torch.zeros(4, device=cuda_dev), cu.to(cuda_dev), cu)
+        assert torch.equal(kda.gdn_prefill(*args, S0=S0, recurrent=rec)[1], S0)
+        assert (kda.gdn_prefill(*args, recurrent=rec)[1] == 0).all()
+        assert kda.gdn_prefill(*args, want_state=False, recurrent=rec)[0].numel() == 0

@@ -205,3 +205,59 @@ def test_decode_any_cluster_size(kda_lib, cuda_dev, N):
         ro[n], size[n] = w @ vc[n, rows, 0].double(), w @ vc[n, rows, 0].double().abs()
     check_window(o, ro, size, f"{N} sequences")
     assert torch.equal(kd.cpu(), kc) and torch.equal(vd.cpu(), vc)
+
+
+@pytest.mark.parametrize("N", [33, 64, 700])
+def test_prefill_many_sequences(kda_lib, cuda_dev, N):
+    """Packed batches of more than one group of 32 sequences, empty ones among them, some resumed."""
+    import serving_kda_chunked_gated_gb300.kda as kda
+    lens, hist = [(11 * i) % 23 for i in range(N)], [(5 * i) % 7 for i in range(N)]
+    lens[N // 2], lens[3], hist[-1] = 200, 0, 150
+    q, k, v, cu, cuk = _inputs(lens, hist, 2, 1, 64, seed=N)
+    ro, rl, size = window_reference(q, k, v, cu, cuk, 20, 2)
+    o, lse = kda.window_prefill(q.to(cuda_dev), k.to(cuda_dev), v.to(cuda_dev), 20, 2, cu.to(cuda_dev), cu, cuk.to(cuda_dev),
+                                cuk, want_lse=True)
+    check_window(o, ro, size)
+    _lse_ok(lse, rl, q, k, 64 ** -0.5)
+
+
+FIRST_CALL = """
+import torch, serving_kda_chunked_gated_gb300.kda as kda
+x = lambda *s, d=torch.bfloat16: torch.randn(*s, device="cuda").to(d)
+f = torch.float32
+q, k, v, kc, vc = x(3, 4, 128), x(3, 2, 128), x(3, 2, 128), x(3, 300, 2, 128), x(3, 300, 2, 128)
+pos = torch.tensor([1, 299, 1000], dtype=torch.int32, device="cuda")
+cos, sin, w, st, z, be = x(1001, 64, d=f), x(1001, 64, d=f), x(128, d=f), x(3, 2, 128, 128, d=f), x(3, 2, d=f), x(3, 2, d=f)
+cu = torch.tensor([0, 1, 3], dtype=torch.int32)
+cud, A = cu.cuda(), torch.zeros(2, device="cuda")
+lq, lk, lv, lz, lb = x(60, 2, 128), x(60, 2, 128), x(60, 2, 128), x(60, 2, d=f), x(60, 2, d=f)
+cl = torch.tensor([0, 20, 60], dtype=torch.int32)
+cld = cl.cuda()
+def step():
+    S = st.clone()
+    return [kda.window_decode(q, k, v, kc, vc, pos, 296, 4), *kda.qk_norm_rope(q, k, cos, sin, pos, w, w),
+            kda.gdn_decode_step(k, k, v, z, be, A, S), S, kda.window_prefill(q, k, v, 2, 1, cud, cu),
+            *kda.gdn_prefill(lq, lk, lv, lz, lb, A, cld, cl)]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    held = step()
+g.replay()
+torch.cuda.synchronize()
+first = [t.clone() for t in held]
+g.replay()
+eager = step()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) and torch.equal(a, c) for a, b, c in zip(first, held, eager))
+print("captured")
+"""
+
+
+def test_first_calls_captured(kda_lib, cuda_dev):
+    """A fresh process whose first call of every operator is a captured one: replays equal eager calls."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
