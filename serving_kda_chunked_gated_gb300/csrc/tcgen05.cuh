@@ -150,9 +150,10 @@ TC_DEV void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32
         :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(acc) : "memory");
 }
 // The same, A from TMEM (two 16-bit elements of K per 32-bit column), and the commit, for a
-// converged warp: all lanes compute the operands, one elected lane issues (always the same).  The operands then stay in uniform registers and
-// the issue costs 41, 48, 64 cycles at N = 32, 64, 128 (M = 128, K = 16); inside a
-// one-lane branch it takes 66, under a predicate from the lane number 83 for any N <= 128.
+// converged warp: all lanes compute the operands, one elected lane issues (always the same).
+// The operands then stay in uniform registers and the issue costs 41, 48, 64 cycles at
+// N = 32, 64, 128 (M = 128, K = 16); inside a one-lane branch it takes 66, under a predicate
+// from the lane number 83 for any N <= 128.
 TC_DEV void mma_f16_ss_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t acc) {
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"

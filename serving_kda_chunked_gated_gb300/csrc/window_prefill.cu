@@ -25,8 +25,8 @@
 //
 // Two bounds meet: a round (both tiles' P V and Q K^T, d = 128) keeps the tensor core busy for
 // 2068 cycles, and its 2 x 128 x 128 exponentials the special-function units (16 a cycle) for
-// 2048.  Measured: 8192 tokens, 32 / 8 heads of 128, window 4096: 350 us, some 3800 cycles a
-// round (TMEM reads slow down while products run), 1.17 PFLOP/s; 131072 tokens, window 512:
+// 2048.  Measured: 8192 tokens, 32 / 8 heads of 128, window 4096: 348 us, some 3800 cycles a
+// round (TMEM reads slow down while products run), 1.18 PFLOP/s; 131072 tokens, window 512:
 // 1.46 ms, where a unit has 5 rounds and its change (queries in, rows out) costs 5000 cycles.
 #include <math.h>
 
@@ -71,8 +71,7 @@ struct PfParams {
     uint32_t wait_limit;
 };
 
-// One unit's geometry, from its index; called by whole warps.  Units count down so
-// that a sequence's end, where the windows are full, comes first.
+// One unit's geometry, from its index; called by whole warps.
 struct Unit {
     int q0, q1;        // packed query rows [q0, q1) of the unit
     int p0;            // position of query q0 in its sequence
@@ -96,39 +95,65 @@ struct Unit {
     }
 };
 
-// A place in the list of query blocks: the 32 sequences from `base` on, with `behind` blocks in the
-// sequences after them.  It moves with the units: none is before the last one.
+// The unit of a CTA's turn r.  Units get cheaper as they go (below), and every other turn deals them
+// the other way round, which leaves the CTAs even: 4096 tokens, window 2048: 114 -> 105 us.
+KDA_DEV long unit_of(uint32_t r) {
+    const uint32_t g = gridDim.x, k = blockIdx.x;
+    return (long)r * g + (r & 1 ? g - 1 - k : k);
+}
+
+// A place in the list of query blocks (2 qpt queries each).  The list takes 32 sequences at a time,
+// the last ones first, and of these the blocks at the highest positions first, where windows
+// are full.  It moves with the units: none is before the last one.
 struct Place {
-    int base, behind;
+    int base;              // the sequences are base .. base + 31, one per lane:
+    int first, end;        // their blocks' levels, in blocks from position 0
+    int level, left;       // the level to come, blocks of these sequences from it down
+    long before;           // blocks in front of it
 };
 
+KDA_DEV void enter(const PfParams& p, Place& at) {
+    const int m = at.base + (int)(threadIdx.x & 31), per = 2 * p.qpt;
+    int len = 0, hist = 0;
+    if (m < p.a.num_seqs) {
+        len = p.a.cu_seqlens[m + 1] - p.a.cu_seqlens[m];
+        hist = p.a.cu_seqlens_k[m + 1] - p.a.cu_seqlens_k[m] - len;
+    }
+    const int blocks = (len + per - 1) / per;
+    at.first = hist / per;
+    at.end = at.first + blocks;
+    at.level = __reduce_max_sync(~0u, blocks ? at.end - 1 : 0);
+    at.left = __reduce_add_sync(~0u, blocks);
+}
+
 KDA_DEV Unit unit_at(const PfParams& p, long u, Place& at) {
-    const int heads = p.a.Hkv * p.subs;
-    const int hs = heads - 1 - (int)(u % heads);
-    const long back = u / heads;            // blocks of 2 qpt queries behind this one, over all sequences
-    const int lane = threadIdx.x & 31, per = 2 * p.qpt;
+    const int heads = p.a.Hkv * p.subs, per = 2 * p.qpt;
+    const int hs = (int)(u % heads);
+    const long idx = u / heads;             // block in the list
+    const int lane = threadIdx.x & 31;
     int n = 0, b = 0;                       // sequence, block in it
-    for (;;) {                              // ends: u < units
-        const int m = at.base + lane;
-        const int len = m < p.a.num_seqs ? p.a.cu_seqlens[m + 1] - p.a.cu_seqlens[m] : 0;
-        int pre = (len + per - 1) / per;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(~0u, pre, o);
-            if (lane >= o) pre += x;
+    for (;;) {
+        while (at.left == 0 && at.base > 0) {
+            at.base -= 32;
+            enter(p, at);
         }
-        const int all = __shfl_sync(~0u, pre, 31);
-        if (back < (long)at.behind + all || at.base == 0) {
-            b = all - 1 - (int)(back - at.behind);
-            const unsigned hit = __ballot_sync(~0u, b < pre);
-            const int f = hit ? __ffs(hit) - 1 : 0;
-            const int before = __shfl_sync(~0u, pre, f > 0 ? f - 1 : 0);
-            if (f > 0) b -= before;
+        if (at.left == 0) break;            // (not for u < units)
+        const unsigned here = __ballot_sync(~0u, at.first <= at.level && at.level < at.end);
+        if (here == 0) {                    // between two sequences' levels
+            at.level = __reduce_max_sync(~0u, at.first < at.end && at.end <= at.level ? at.end - 1 : 0);
+            continue;
+        }
+        const int rank = (int)(idx - at.before);
+        if (rank < __popc(here)) {
+            const bool mine = (here >> lane & 1u) && __popc(here & ((1u << lane) - 1)) == rank;
+            const int f = __ffs(__ballot_sync(~0u, mine)) - 1;
             n = at.base + f;
+            b = at.level - __shfl_sync(~0u, at.first, f);
             break;
         }
-        at.behind += all;
-        at.base -= 32;
+        at.before += __popc(here);
+        at.left -= __popc(here);
+        --at.level;
     }
     Unit x;
     const int c0 = p.a.cu_seqlens[n], c1 = p.a.cu_seqlens[n + 1];
@@ -230,8 +255,11 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
             // ---------------- loads: Q of a unit, then K and V tiles through the ring ----------------
             uint32_t it = 0, edges = 0, nu = 0, nq = 0;     // items, zeroed tiles, units, Q loads so far
             bool ok = true, direct = true;         // direct: the last item counts on its round's barrier
-            Place place = {(p.a.num_seqs - 1) & ~31, 0};
-            for (long u = blockIdx.x; u < p.units && ok; u += gridDim.x, ++nu) {
+            Place place;
+            place.base = (p.a.num_seqs - 1) & ~31;
+            place.before = 0;
+            enter(p, place);
+            for (long u; (u = unit_of(nu)) < p.units && ok; ++nu) {
                 const Unit x = unit_at(p, u, place);
                 for (int i = 0; i < x.ntiles && ok; ++i) {
                     int j0, width;
@@ -360,7 +388,7 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
             auto width_of = [&](const Tiles& r, int i) { return i == r.ntiles - 1 ? r.slast : i == r.nwin - 1 ? r.wlast : KT; };
             Tiles x = {0, 0, 0, 0};
             uint32_t vs = L::SLOTS - 1, ks = 0;    // slots of this round's values and keys
-            if ((long)blockIdx.x < p.units) {
+            if (unit_of(0) < p.units) {
                 ok = wait_warp(&u_full[0], 0, limit, abort) && wait_warp(&q_full, 0, limit, abort) &&
                      wait_warp(&full[0], 0, limit, abort) && my_turn(0);
                 tc::fence_after_sync();
@@ -375,8 +403,8 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
                 rd = 1;
             }
 #pragma unroll 1
-            for (long u = blockIdx.x; u < p.units && ok; u += gridDim.x, ++nu) {
-                const bool next_unit = u + gridDim.x < p.units;
+            for (; unit_of(nu) < p.units && ok; ++nu) {
+                const bool next_unit = unit_of(nu + 1) < p.units;
                 Tiles y = x;
 #pragma unroll 1
                 for (int i = 0; i < x.ntiles; ++i, ++np, ++rd) {
@@ -428,7 +456,7 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
         const int r = tid & 127;
         uint32_t nu = 0;
         bool ok = true;
-        for (long u = blockIdx.x; u < p.units && ok; u += gridDim.x, ++nu) {
+        for (; unit_of(nu) < p.units && ok; ++nu) {
             ok = wait_warp(&u_full[nu % UNITS], (nu / UNITS) & 1, limit, abort);
             if (!ok) break;
             const Unit x = s_unit[nu % UNITS];
@@ -480,7 +508,7 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
         const uint32_t to = tm + 256 + t * D + ((uint32_t)(warp & 3) << 21);
         uint32_t np = 0, nu = 0;
         bool ok = true;
-        for (long u = blockIdx.x; u < p.units && ok; u += gridDim.x, ++nu) {
+        for (; unit_of(nu) < p.units && ok; ++nu) {
             ok = wait_warp(&u_full[nu % UNITS], (nu / UNITS) & 1, limit, abort);
             if (!ok) break;
             const Unit x = s_unit[nu % UNITS];
