@@ -138,22 +138,23 @@ KDA_DEV Unit unit_at(const PfParams& p, long u, Place& at) {
             enter(p, at);
         }
         if (at.left == 0) break;            // (not for u < units)
-        const unsigned here = __ballot_sync(~0u, at.first <= at.level && at.level < at.end);
-        if (here == 0) {                    // between two sequences' levels
-            at.level = __reduce_max_sync(~0u, at.first < at.end && at.end <= at.level ? at.end - 1 : 0);
-            continue;
-        }
-        const int rank = (int)(idx - at.before);
-        if (rank < __popc(here)) {
-            const bool mine = (here >> lane & 1u) && __popc(here & ((1u << lane) - 1)) == rank;
+        // the sequences at this level, and down to which level they are the same ones
+        const bool at_it = at.first <= at.level && at.level < at.end;
+        const unsigned here = __ballot_sync(~0u, at_it);
+        const int low = __reduce_max_sync(~0u, at_it ? at.first : at.first < at.end && at.end <= at.level ? at.end : 0);
+        const int many = __popc(here), levels = at.level - low + 1;
+        const long rank = idx - at.before;
+        const int down = rank < (long)levels * many ? (int)rank / many : levels;
+        at.before += (long)down * many;
+        at.left -= down * many;
+        at.level -= down;
+        if (down < levels) {
+            const bool mine = at_it && __popc(here & ((1u << lane) - 1)) == (int)(idx - at.before);
             const int f = __ffs(__ballot_sync(~0u, mine)) - 1;
             n = at.base + f;
             b = at.level - __shfl_sync(~0u, at.first, f);
             break;
         }
-        at.before += __popc(here);
-        at.left -= __popc(here);
-        --at.level;
     }
     Unit x;
     const int c0 = p.a.cu_seqlens[n], c1 = p.a.cu_seqlens[n + 1];
