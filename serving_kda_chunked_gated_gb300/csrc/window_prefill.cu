@@ -64,7 +64,7 @@ struct PfParams {
     kda_window_prefill_args a;
     int gp, subs;                           // rows' heads per tile; head subgroups per key head
     int qpt;                                // queries per tile (128 / gp)
-    long units;
+    uint32_t units;                         // at most 2^31 - 1
     float c;                                // |scale| log2 e
     int neg;                                // scale < 0: S = -Q K^T
     int wide;                               // o is 32-byte aligned
@@ -97,9 +97,9 @@ struct Unit {
 
 // The unit of a CTA's turn r.  Units get cheaper as they go (below), and every other turn deals them
 // the other way round, which leaves the CTAs even: 4096 tokens, window 2048: 114 -> 105 us.
-KDA_DEV long unit_of(uint32_t r) {
+KDA_DEV uint32_t unit_of(uint32_t r) {
     const uint32_t g = gridDim.x, k = blockIdx.x;
-    return (long)r * g + (r & 1 ? g - 1 - k : k);
+    return r * g + (r & 1 ? g - 1 - k : k);
 }
 
 // A place in the list of query blocks (2 qpt queries each).  The list takes 32 sequences at a time,
@@ -108,30 +108,32 @@ KDA_DEV long unit_of(uint32_t r) {
 struct Place {
     int base;              // the sequences are base .. base + 31, one per lane:
     int first, end;        // their blocks' levels, in blocks from position 0
+    int q0, q1, k0, hist;  // packed query rows, first key row, keys before the queries
     int level, left;       // the level to come, blocks of these sequences from it down
-    long before;           // blocks in front of it
+    int before;            // blocks in front of it
 };
 
 KDA_DEV void enter(const PfParams& p, Place& at) {
     const int m = at.base + (int)(threadIdx.x & 31), per = 2 * p.qpt;
-    int len = 0, hist = 0;
+    at.q0 = at.q1 = at.k0 = at.hist = 0;
     if (m < p.a.num_seqs) {
-        len = p.a.cu_seqlens[m + 1] - p.a.cu_seqlens[m];
-        hist = p.a.cu_seqlens_k[m + 1] - p.a.cu_seqlens_k[m] - len;
+        at.q0 = p.a.cu_seqlens[m];
+        at.q1 = p.a.cu_seqlens[m + 1];
+        at.k0 = p.a.cu_seqlens_k[m];
+        at.hist = p.a.cu_seqlens_k[m + 1] - at.k0 - (at.q1 - at.q0);
     }
-    const int blocks = (len + per - 1) / per;
-    at.first = hist / per;
+    const int blocks = (at.q1 - at.q0 + per - 1) / per;
+    at.first = at.hist / per;
     at.end = at.first + blocks;
     at.level = __reduce_max_sync(~0u, blocks ? at.end - 1 : 0);
     at.left = __reduce_add_sync(~0u, blocks);
 }
 
-KDA_DEV Unit unit_at(const PfParams& p, long u, Place& at) {
-    const int heads = p.a.Hkv * p.subs, per = 2 * p.qpt;
-    const int hs = (int)(u % heads);
-    const long idx = u / heads;             // block in the list
+KDA_DEV Unit unit_at(const PfParams& p, uint32_t u, Place& at) {
+    const uint32_t heads = p.a.Hkv * p.subs;
+    const int hs = (int)(u % heads), idx = (int)(u / heads), per = 2 * p.qpt;      // idx: block in the list
     const int lane = threadIdx.x & 31;
-    int n = 0, b = 0;                       // sequence, block in it
+    int f = 0, b = 0;                       // lane of the sequence, block in it
     for (;;) {
         while (at.left == 0 && at.base > 0) {
             at.base -= 32;
@@ -143,26 +145,22 @@ KDA_DEV Unit unit_at(const PfParams& p, long u, Place& at) {
         const unsigned here = __ballot_sync(~0u, at_it);
         const int low = __reduce_max_sync(~0u, at_it ? at.first : at.first < at.end && at.end <= at.level ? at.end : 0);
         const int many = __popc(here), levels = at.level - low + 1;
-        const long rank = idx - at.before;
-        const int down = rank < (long)levels * many ? (int)rank / many : levels;
-        at.before += (long)down * many;
+        const int rank = idx - at.before, down = rank < levels * many ? rank / many : levels;
+        at.before += down * many;
         at.left -= down * many;
         at.level -= down;
         if (down < levels) {
-            const bool mine = at_it && __popc(here & ((1u << lane) - 1)) == (int)(idx - at.before);
-            const int f = __ffs(__ballot_sync(~0u, mine)) - 1;
-            n = at.base + f;
+            const bool mine = at_it && __popc(here & ((1u << lane) - 1)) == idx - at.before;
+            f = __ffs(__ballot_sync(~0u, mine)) - 1;
             b = at.level - __shfl_sync(~0u, at.first, f);
             break;
         }
     }
     Unit x;
-    const int c0 = p.a.cu_seqlens[n], c1 = p.a.cu_seqlens[n + 1];
-    x.k0 = p.a.cu_seqlens_k[n];
-    const int lk = p.a.cu_seqlens_k[n + 1] - x.k0;
-    x.q0 = c0 + b * per;
-    x.q1 = min(c1, x.q0 + per);
-    x.p0 = lk - (c1 - c0) + b * per;
+    x.k0 = __shfl_sync(~0u, at.k0, f);
+    x.q0 = __shfl_sync(~0u, at.q0, f) + b * per;
+    x.q1 = min(__shfl_sync(~0u, at.q1, f), x.q0 + per);
+    x.p0 = __shfl_sync(~0u, at.hist, f) + b * per;
     x.hi = x.p0 + (x.q1 - x.q0) - 1;
     x.lo = max(0, x.p0 - p.a.window + 1);
     x.nsink = min(p.a.sinks, x.lo);
@@ -260,7 +258,7 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
             place.base = (p.a.num_seqs - 1) & ~31;
             place.before = 0;
             enter(p, place);
-            for (long u; (u = unit_of(nu)) < p.units && ok; ++nu) {
+            for (uint32_t u; (u = unit_of(nu)) < p.units && ok; ++nu) {
                 const Unit x = unit_at(p, u, place);
                 for (int i = 0; i < x.ntiles && ok; ++i) {
                     int j0, width;
@@ -659,7 +657,7 @@ static cudaError_t prefill_d(const kda_window_prefill_args& a, cudaStream_t s) {
     long blocks = 0;
     for (int n = 0; n < a.num_seqs; ++n)
         blocks += (a.cu_seqlens_host[n + 1] - a.cu_seqlens_host[n] + 2 * p.qpt - 1) / (2 * p.qpt);
-    p.units = blocks * a.Hkv * p.subs;
+    p.units = (uint32_t)(blocks * a.Hkv * p.subs);
     if (p.units == 0) return cudaSuccess;
     // a zero scale keeps exp2(fma(-inf, c, ...)) at 0 for masked scores
     p.c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-37f);
@@ -676,8 +674,8 @@ static cudaError_t prefill_d(const kda_window_prefill_args& a, cudaStream_t s) {
     if (e == cudaSuccess) e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    const long grid = p.units < sms ? p.units : sms;
-    window_prefill_kernel<D><<<(unsigned)grid, PF_THREADS, PF<D>::SMEM, s>>>(p, mq, mk, mv);
+    const unsigned grid = std::min(p.units, (uint32_t)sms);
+    window_prefill_kernel<D><<<grid, PF_THREADS, PF<D>::SMEM, s>>>(p, mq, mk, mv);
     count_launches(1);
     return cudaGetLastError();
 }
