@@ -58,18 +58,18 @@ KDA_DEV float ld_peer(const float* p, uint32_t rank) {   // the float at this ad
     return v;
 }
 
-constexpr int DEC_WARPS = 8;
 constexpr int DEC_STAGES = 3;
 constexpr int DEC_KEYS = 16;     // keys per tile
 
-template <int D>
-constexpr int dec_smem() { return DEC_WARPS * DEC_STAGES * DEC_KEYS * D * 2 * 2; }
+template <int D, int WARPS>
+constexpr int dec_smem() { return WARPS * DEC_STAGES * DEC_KEYS * D * 2 * 2; }
 
-template <int D>
-__global__ void __launch_bounds__(DEC_WARPS * 32, 1)
+// 8 / WARPS CTAs share an SM
+template <int D, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 8 / WARPS)
 window_decode_kernel(kda_window_decode_args a, int mtiles) {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float s_m[DEC_WARPS][16], s_l[DEC_WARPS][16], s_M[16], s_L[16];
+    __shared__ float s_m[WARPS][16], s_l[WARPS][16], s_M[16], s_L[16];
     constexpr int TILE = DEC_KEYS * D * 2;          // bytes of one K (or V) tile
     constexpr int CH = D / 8;                       // 16-byte chunks per row
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -98,7 +98,7 @@ window_decode_kernel(kda_window_decode_args a, int mtiles) {
     uint8_t* mine = smem + warp * (DEC_STAGES * 2 * TILE);
     const uint32_t mine_u = su32(mine);
     const int ntiles = (total + DEC_KEYS - 1) / DEC_KEYS;
-    const int t0 = split * DEC_WARPS + warp, tstep = nsplit * DEC_WARPS;
+    const int t0 = split * WARPS + warp, tstep = nsplit * WARPS;
 
     // The new token is the last visible row; it is read from the inputs, so no CTA
     // depends on the cache row that is being written.
@@ -234,10 +234,10 @@ window_decode_kernel(kda_window_decode_args a, int mtiles) {
     if (tid < 16) {
         float M = -INFINITY, L = 0.f;
 #pragma unroll
-        for (int w = 0; w < DEC_WARPS; ++w) M = fmaxf(M, s_m[w][tid]);
+        for (int w = 0; w < WARPS; ++w) M = fmaxf(M, s_m[w][tid]);
         const float b = M == -INFINITY ? 0.f : M;
 #pragma unroll
-        for (int w = 0; w < DEC_WARPS; ++w) {
+        for (int w = 0; w < WARPS; ++w) {
             const float f = exp2f(s_m[w][tid] - b);
             L += f * s_l[w][tid];
             s_m[w][tid] = f;                              // from here on: the warp's weight
@@ -248,21 +248,21 @@ window_decode_kernel(kda_window_decode_args a, int mtiles) {
     __syncthreads();
     const int rows = min(16, G - mt * 16);
     float* acc = reinterpret_cast<float*>(smem);          // the CTA's rows replace warp 0's (same thread, same place)
-    for (int e = tid; e < rows * D; e += DEC_WARPS * 32) {
+    for (int e = tid; e < rows * D; e += WARPS * 32) {
         const int r = e / D;
         float x = 0.f;
 #pragma unroll
-        for (int w = 0; w < DEC_WARPS; ++w)
+        for (int w = 0; w < WARPS; ++w)
             x += s_m[w][r] * reinterpret_cast<const float*>(smem + w * (DEC_STAGES * 2 * TILE))[e];
         acc[e] = x;
     }
     uint16_t* out = reinterpret_cast<uint16_t*>(a.o) + ((size_t)n * a.Hq + (size_t)hk * G + mt * 16) * D;
     if (nsplit == 1) {
-        for (int e = tid; e < rows * D; e += DEC_WARPS * 32) out[e] = f_to_bf16(acc[e] / s_L[e / D]);
+        for (int e = tid; e < rows * D; e += WARPS * 32) out[e] = f_to_bf16(acc[e] / s_L[e / D]);
         return;
     }
     cluster_sync();
-    for (int e = split * (DEC_WARPS * 32) + tid; e < rows * D; e += nsplit * DEC_WARPS * 32) {
+    for (int e = split * (WARPS * 32) + tid; e < rows * D; e += nsplit * WARPS * 32) {
         const int r = e / D;
         float M = -INFINITY, x = 0.f, L = 0.f;
         for (uint32_t c = 0; c < nsplit; ++c) M = fmaxf(M, ld_peer(&s_M[r], c));
@@ -280,12 +280,12 @@ window_decode_kernel(kda_window_decode_args a, int mtiles) {
 // CTAs of a cluster at most (the portable size) and devices whose counts are kept
 constexpr int DEC_SPLIT = 8, DEC_DEVICES = 64;
 
-template <int D>
+template <int D, int WARPS>
 static void decode_shape(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, long units, int split, cudaStream_t s) {
     *cfg = {};
     cfg->gridDim = dim3((unsigned)(units * split));
-    cfg->blockDim = dim3(DEC_WARPS * 32);
-    cfg->dynamicSmemBytes = dec_smem<D>();
+    cfg->blockDim = dim3(WARPS * 32);
+    cfg->dynamicSmemBytes = dec_smem<D, WARPS>();
     cfg->stream = s;
     attr->id = cudaLaunchAttributeClusterDimension;
     attr->val.clusterDim.x = split;
@@ -306,37 +306,54 @@ static cudaError_t resident_clusters(int split, int* count) {
     if (keep && (*count = held[dev][split].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr;
-    decode_shape<D>(&cfg, &attr, 1, split, nullptr);
-    e = cudaOccupancyMaxActiveClusters(count, window_decode_kernel<D>, &cfg);
+    decode_shape<D, 8>(&cfg, &attr, 1, split, nullptr);
+    e = cudaOccupancyMaxActiveClusters(count, window_decode_kernel<D, 8>, &cfg);
     if (e == cudaSuccess && keep) held[dev][split].store(*count, std::memory_order_relaxed);
     return e;
+}
+
+template <int D, int WARPS>
+static cudaError_t decode_go(const kda_window_decode_args& a, int mtiles, long units, cudaStream_t s) {
+    cudaError_t e =
+        cudaFuncSetAttribute(window_decode_kernel<D, WARPS>, cudaFuncAttributeMaxDynamicSharedMemorySize, dec_smem<D, WARPS>());
+    if (e != cudaSuccess) return e;
+    int split = 1;
+    if constexpr (WARPS == 8) {
+        // CTAs per unit: as many as leave all clusters resident at once, at most one per 16-key tile of
+        // each warp.  Window of 4096, d = 128, us: 14 units 30.2 alone, 12.3 by fours, 9.6 by eights;
+        // 36 units 30.6, 12.9, but 27.0 by eights, whose clusters then come in turns; 100 units
+        // 35.6, 45.4 by twos.
+        const long most = ((long)a.sinks + a.window + DEC_KEYS * WARPS - 1) / (DEC_KEYS * WARPS);
+        for (int c = DEC_SPLIT; c > 1 && split == 1; --c) {
+            if (c > most || units * c > 152) continue;
+            int fit = 0;
+            if ((e = resident_clusters<D>(c, &fit)) != cudaSuccess) return e;
+            if (units <= fit) split = c;
+        }
+    }
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr;
+    decode_shape<D, WARPS>(&cfg, &attr, units, split, s);
+    e = cudaLaunchKernelEx(&cfg, window_decode_kernel<D, WARPS>, a, mtiles);
+    if (e != cudaSuccess) return e;
+    count_launches(1);
+    return cudaSuccess;
 }
 
 template <int D>
 static cudaError_t decode_d(const kda_window_decode_args& a, cudaStream_t s) {
     const int mtiles = (a.Hq / a.Hkv + 15) / 16;
-    const long units = (long)a.N * a.Hkv * mtiles;
-    cudaError_t e = cudaFuncSetAttribute(window_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, dec_smem<D>());
-    if (e != cudaSuccess) return e;
-    // CTAs per (sequence, key head): as many as leave all clusters resident at once, at most one
-    // per 16-key tile of each warp.  Window of 4096, d = 128, us: 14 units 30.2 alone, 12.3 by
-    // fours, 9.6 by eights; 36 units 30.6, 12.9, but 27.0 by eights, whose clusters then come
-    // in turns; 100 units 35.6, 45.4 by twos.
-    const long most = ((long)a.sinks + a.window + DEC_KEYS * DEC_WARPS - 1) / (DEC_KEYS * DEC_WARPS);
-    int split = 1;
-    for (int c = DEC_SPLIT; c > 1 && split == 1; --c) {
-        if (c > most || units * c > 152) continue;
-        int fit = 0;
-        if ((e = resident_clusters<D>(c, &fit)) != cudaSuccess) return e;
-        if (units <= fit) split = c;
-    }
-    cudaLaunchConfig_t cfg;
-    cudaLaunchAttribute attr;
-    decode_shape<D>(&cfg, &attr, units, split, s);
-    e = cudaLaunchKernelEx(&cfg, window_decode_kernel<D>, a, mtiles);
-    if (e != cudaSuccess) return e;
-    count_launches(1);
-    return cudaSuccess;
+    const long units = (long)a.N * a.Hkv * mtiles;          // (sequence, key head, 16 of its query heads)
+    // Eight warps an SM in all, in smaller CTAs where there are units enough to fill it with them: a
+    // CTA's start and end then pass beside others' loads.  d = 128, us with 8, 4, 2 warps: 152 units,
+    // window 4096: 50, 52, 76; 300 units, 2000: 51, 49, 52; 1160 units, 101 + 64 sinks: 31, 19, 14;
+    // 2048 units, 512: 109, 92, 91; 1024: 170, 160, 163; 4096: 587, 586, 607 (more pages of
+    // memory open at a time).
+    const long rows = (long)a.sinks + a.window;
+    if (units > 2 * 152 && rows <= 512) return decode_go<D, 2>(a, mtiles, units, s);
+    // also where eight warps would not have a tile each (82 units, 6 + 64 rows, d = 64: 3.6, 3.3, 3.2)
+    if (units > 152 || rows < 8 * DEC_KEYS) return decode_go<D, 4>(a, mtiles, units, s);
+    return decode_go<D, 8>(a, mtiles, units, s);
 }
 
 cudaError_t launch_decode(const kda_window_decode_args& a, cudaStream_t s) {

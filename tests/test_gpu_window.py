@@ -183,11 +183,13 @@ def test_decode_long_window_split_over_ctas(kda_lib, cuda_dev):
         check_window(o, (w @ V[rows, 0].double())[None], (w @ V[rows, 0].double().abs())[None], f"position {pos}")
 
 
-@pytest.mark.parametrize("N", [11, 15, 20, 24, 33, 40, 60, 77])
-def test_decode_any_cluster_size(kda_lib, cuda_dev, N):
-    """Batch sizes that give each sequence from eight CTAs down to one, at positions up to the last int32."""
+@pytest.mark.parametrize("N,W", [(11, 1100), (15, 1100), (20, 1100), (24, 1100), (33, 1100), (40, 1100), (60, 1100),
+                                 (77, 1100), (160, 300), (5, 40), (310, 30), (310, 500), (310, 600)])
+def test_decode_any_cluster_size(kda_lib, cuda_dev, N, W):
+    """Batch sizes that give each sequence from eight CTAs down to one and from eight warps to two, at
+    positions up to the last int32."""
     import serving_kda_chunked_gated_gb300.kda as kda
-    W, sinks, Hq, Hkv, d = 1100, 2, 3, 1, 64
+    sinks, Hq, Hkv, d = 2, 3, 1, 64
     g = torch.Generator().manual_seed(N)
     kc, vc = (torch.randn(N, W + sinks, Hkv, d, generator=g).to(torch.bfloat16) for _ in "kv")
     q, k, v = (torch.randn(N, h, d, generator=g).to(torch.bfloat16) for h in (Hq, Hkv, Hkv))
