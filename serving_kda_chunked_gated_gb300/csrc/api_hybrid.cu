@@ -80,7 +80,7 @@ kda_status kda_gdn_prefill(const kda_gdn_prefill_args* a, void* stream) {
     if (st != KDA_OK) return st;
     if (a->num_seqs == 0 || (!a->o && !a->S_T)) return KDA_OK;      // no tokens and no state asked for
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (a->qkv_dtype == KDA_F32) return done(kda::gdn::launch_recurrent(*a, s));
+    if (a->qkv_dtype == KDA_F32) return kda_gdn_prefill_recurrent(a, stream);
     if (!a->workspace || a->workspace_bytes < kda::gdn::chunked_workspace_size(*a)) return KDA_ERR_WORKSPACE;
     if (misaligned(a->workspace)) return KDA_ERR_ALIGN;
     return done(kda::gdn::launch_chunked(*a, s));
@@ -89,7 +89,9 @@ kda_status kda_gdn_prefill(const kda_gdn_prefill_args* a, void* stream) {
 kda_status kda_gdn_prefill_recurrent(const kda_gdn_prefill_args* a, void* stream) {
     const kda_status st = check(a);
     if (st != KDA_OK) return st;
-    return done(kda::gdn::launch_recurrent(*a, reinterpret_cast<cudaStream_t>(stream)));
+    kda_gdn_prefill_args r = *a;
+    r.workspace = nullptr;                // has none, whatever the field holds
+    return done(kda::gdn::launch_recurrent(r, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 kda_status kda_gdn_decode_step(const kda_gdn_decode_args* a, void* stream) {

@@ -52,7 +52,7 @@ constexpr int TILE = C * DH * 2;              // a K or Q tile: two slabs of 64 
 // half is zero), rows of 128 bytes in the 128-byte swizzle.
 constexpr int TRI = 16384 + 8192;
 constexpr int REC_THI = 0, REC_TLO = TRI, REC_A = 2 * TRI, REC_F = 3 * TRI;
-constexpr int REC = 3 * TRI + C * 16 + 128;   // + four factors per token + e^{g_C}
+constexpr int REC = 3 * TRI + C * 16 + 128;   // + four factors per token + e^{g_C} and the record's ERR_ bits
 constexpr int WS_HEAD = 256;                  // the error word's line
 
 // For up to this many sequences the host lays the work out, by value.  Scans of the longest start
@@ -193,7 +193,7 @@ gdn_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t loaded, done;
     __shared__ uint32_t s_tmem;
-    __shared__ int s_ok;
+    __shared__ int s_err;
     __shared__ float s_rk[C], s_rq[C], s_beta[C], s_part[4][C];
     __shared__ long long s_g[C], s_wsum[4];
     const kda_gdn_prefill_args& a = p.a;
@@ -208,10 +208,12 @@ gdn_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
     const bool live = row < len;
 
     if (tid == 0) {
+        // This grid's own errors go into its records, the scan adds them to the word.
+        if (blockIdx.x == 0) *reinterpret_cast<int*>(a.workspace) = 0;
         tc::mbar_init(&loaded, 1);
         tc::mbar_init(&done, 1);
         tc::mbar_fence_init();
-        s_ok = 1;
+        s_err = 0;
         tc::mbar_arrive_expect_tx(&loaded, 2 * TILE);
         for (int s = 0; s < 2; ++s) {
             tc::tma_load_3d(sm + s * 16384, &mk, s * 64, hk, t0, &loaded);
@@ -241,11 +243,10 @@ gdn_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
     auto wait_for = [&](uint64_t* bar) {
         if (tid == 0 && !tc::mbar_wait_bounded(bar, 0, p.wait_limit)) {
             const bool d = tc::mbar_wait_bounded(bar, 0, tc::WAIT_POLLS);    // give up, but not before what was issued
-            atomicOr(reinterpret_cast<int*>(a.workspace), d ? tc::ERR_WAIT : tc::ERR_WAIT | tc::ERR_DRAIN);
-            s_ok = 0;
+            s_err = d ? tc::ERR_WAIT : tc::ERR_WAIT | tc::ERR_DRAIN;
         }
         __syncthreads();
-        return s_ok != 0;
+        return s_err == 0;
     };
     bool ok = wait_for(&loaded);
     if (ok) {
@@ -292,13 +293,15 @@ gdn_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
             (quarter ? s_rq : s_rk)[row] = a.qk_l2norm ? rsqrtf(ss + 1e-6f) : 1.0f;
         }
     }
+    uint8_t* recs = reinterpret_cast<uint8_t*>(a.workspace) + WS_HEAD + (idx * a.Hv + hk * rep) * (size_t)REC;
+    for (int e = tid; !ok && e < rep; e += PT) *reinterpret_cast<int*>(recs + e * (size_t)REC + REC_F + C * 16 + 4) = s_err;
     float* X = reinterpret_cast<float*>(sm + P_X);        // the tiles have been consumed
     uint8_t* img = sm + P_Y;                              // the masked Q K^T on its way out, then Y
     float* W = reinterpret_cast<float*>(sm + P_W);        // W[b][j] = rk_j e^{g_(16 b - 1) - g_j}, j < 16 b
     constexpr float FIX = 4294967296.f, UNFIX = 1.f / 4294967296.f;
     for (int e = 0; ok && e < rep; ++e) {
         const int h = hk * rep + e;
-        uint8_t* rec = reinterpret_cast<uint8_t*>(a.workspace) + WS_HEAD + (idx * a.Hv + h) * (size_t)REC;
+        uint8_t* rec = recs + e * (size_t)REC;
         // sums of the log-decays (base 2), exact in 2^-32 fixed point.  A step below -4096 is
         // an exponential of 0 in any sum; a NaN travels with beta.
         if (quarter == 0) {
@@ -334,7 +337,7 @@ gdn_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
                 f = make_float4(beta, beta * eg * s_rk[row], exp2f((float)(gC - gi) * UNFIX) * s_rk[row],
                                 eg * s_rq[row] * a.scale);
             *reinterpret_cast<float4*>(rec + REC_F + row * 16) = f;
-            if (row == 0) *reinterpret_cast<float*>(rec + REC_F + C * 16) = exp2f((float)gC * UNFIX);
+            if (row == 0) *reinterpret_cast<float2*>(rec + REC_F + C * 16) = make_float2(exp2f((float)gC * UNFIX), 0.f);
         }
         if (tid == 0) tc::bulk_wait_read();       // the last head's image has left
         __syncthreads();
@@ -565,6 +568,7 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tm = s_tmem;
+    tc::wait_prerequisites();                 // prep's records
     const long base = chunks_before(p, n);
     const uint8_t* recs = reinterpret_cast<const uint8_t*>(a.workspace) + WS_HEAD + (base * a.Hv + h) * (size_t)REC;
     const size_t rec_step = (size_t)a.Hv * REC;
@@ -723,7 +727,7 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
         for (int c = 0; c < nc; ++c) {
             if ((c & 7) == 7 && any_of_128(*abort != 0)) break;    // all four warps or none: they share barriers
             const uint32_t ph = c & 1;
-            const float fw = __ldg(reinterpret_cast<const float*>(recs + c * rec_step + REC_F + row * 16 + 12));
+            const float fw = __ldcg(reinterpret_cast<const float*>(recs + c * rec_step + REC_F + row * 16 + 12));
             float o[32], x[32];
             // A V' is the chunk's last product, and the next one waits for these rows: a barrier that
             // could run two phases ahead of its reader (that of Q S) is not waited on here
@@ -788,10 +792,14 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
         // waits for loads in flight, is then as far as their latency.
         float4 f = make_float4(0.f, 0.f, 0.f, 0.f), fn = f;
         float gamma = 0.f, gn = 0.f;
+        int err = 0;                         // of the records
         auto fetch = [&](int c) {
             const uint8_t* rec = recs + c * rec_step;
-            fn = __ldg(reinterpret_cast<const float4*>(rec + REC_F + row * 16));
-            gn = __ldg(reinterpret_cast<const float*>(rec + REC_F + C * 16));
+            // (not the read-only path: the grid before may still be writing when this one starts)
+            fn = __ldcg(reinterpret_cast<const float4*>(rec + REC_F + row * 16));
+            const float2 ge = __ldcg(reinterpret_cast<const float2*>(rec + REC_F + C * 16));
+            gn = ge.x;
+            err |= __float_as_int(ge.y);
         };
         if (nc > 0) fetch(0);
         // R = beta (v - e^g rk K S) of chunk c; the values' place is zero again afterwards
@@ -877,6 +885,7 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
                 if (i + 1 < nc) fetch(i + 1);
             }
         }
+        if (tid == 0 && err) atomicOr(reinterpret_cast<int*>(a.workspace), err);
         if (a.S_T) {
 #pragma unroll
             for (int i = 0; i < 16; i += 4)
@@ -918,7 +927,6 @@ cudaError_t launch_chunked(const kda_gdn_prefill_args& a, cudaStream_t s) {
         std::stable_sort(p.order, p.order + a.num_seqs,
                          [cu](uint16_t x, uint16_t y) { return cu[x + 1] - cu[x] > cu[y + 1] - cu[y]; });
     }
-    cudaError_t e = cudaMemsetAsync(a.workspace, 0, 4, s);
     // Only a few tokens per sequence: a chunk takes its two kernels 36 us however full it is, the
     // recurrence 1 us per token (32 heads); 64 sequences of 16 heads 264 us, and 11 us per token.
     int longest = 0;
@@ -926,22 +934,32 @@ cudaError_t launch_chunked(const kda_gdn_prefill_args& a, cudaStream_t s) {
         const int len = a.cu_seqlens_host[n + 1] - a.cu_seqlens_host[n];
         longest = len > longest ? len : longest;
     }
-    if (e == cudaSuccess && longest <= 24) return launch_recurrent(a, s);
+    if (longest <= 24) return launch_recurrent(a, s);       // clears the error word
     CUtensorMap mq = {}, mk = {}, mv = {}, mo = {};
-    if (chunks > 0) {
-        if (e == cudaSuccess) e = make_map_heads(&mq, a.q, DH, a.Hk, a.T_total, (uint64_t)a.Hk * DH, 1, C);
-        if (e == cudaSuccess) e = make_map_heads(&mk, a.k, DH, a.Hk, a.T_total, (uint64_t)a.Hk * DH, 1, C);
-        if (e == cudaSuccess) e = make_map_heads(&mv, a.v, DH, a.Hv, a.T_total, (uint64_t)a.Hv * DH, 1, C, COLS);
-        if (e == cudaSuccess && a.o) e = make_map_heads(&mo, a.o, DH, a.Hv, a.T_total, (uint64_t)a.Hv * DH, 1, C, COLS);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(gdn_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, P_SMEM);
-        if (e != cudaSuccess) return e;
-        gdn_prep_kernel<<<(unsigned)(chunks * a.Hk), PT, P_SMEM, s>>>(p, mq, mk);
-        count_launches(1);
-        e = cudaGetLastError();
-    }
+    cudaError_t e = make_map_heads(&mq, a.q, DH, a.Hk, a.T_total, (uint64_t)a.Hk * DH, 1, C);
+    if (e == cudaSuccess) e = make_map_heads(&mk, a.k, DH, a.Hk, a.T_total, (uint64_t)a.Hk * DH, 1, C);
+    if (e == cudaSuccess) e = make_map_heads(&mv, a.v, DH, a.Hv, a.T_total, (uint64_t)a.Hv * DH, 1, C, COLS);
+    if (e == cudaSuccess && a.o) e = make_map_heads(&mo, a.o, DH, a.Hv, a.T_total, (uint64_t)a.Hv * DH, 1, C, COLS);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(gdn_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, P_SMEM);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(gdn_scan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S_SMEM);
     if (e != cudaSuccess) return e;
-    gdn_scan_kernel<<<(unsigned)((long)a.num_seqs * a.Hv * (DH / COLS)), ST, S_SMEM, s>>>(p, mq, mk, mv, mo);
+    gdn_prep_kernel<<<(unsigned)(chunks * a.Hk), PT, P_SMEM, s>>>(p, mq, mk);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    count_launches(1);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((long)a.num_seqs * a.Hv * (DH / COLS)));
+    cfg.blockDim = dim3(ST);
+    cfg.dynamicSmemBytes = S_SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    // The scan's start beside prep's end: 33 tokens 43.1 -> 40.2 us, 8192 306 -> 303.  (Started as soon as
+    // all of prep has, its CTAs are in the way of prep's last ones: 308.)
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, gdn_scan_kernel, p, mq, mk, mv, mo);
+    if (e != cudaSuccess) return e;
     count_launches(1);
     return cudaGetLastError();
 }

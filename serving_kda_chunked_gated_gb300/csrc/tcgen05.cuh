@@ -265,6 +265,10 @@ TC_DEV bool drain_phase(uint64_t* mbar, uint32_t n_issued) {
     return n_issued == 0 || mbar_wait_bounded(mbar, (n_issued - 1) & 1u, WAIT_POLLS);
 }
 
+// Programmatic dependent launch: a grid that may start while the one before ends waits here
+// for that one, its writes included.
+TC_DEV void wait_prerequisites() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Error word bits set by a kernel whose bounded wait ran out
 constexpr int ERR_WAIT = 1;    // a wait gave up: the call's outputs are invalid
 constexpr int ERR_DRAIN = 2;   // and the wait for work already issued gave up as well
