@@ -17,7 +17,7 @@ cudaError_t launch(const kda_qk_norm_rope_args& a, cudaStream_t s);
 }
 namespace win {
 cudaError_t launch_prefill(const kda_window_prefill_args& a, cudaStream_t s);
-cudaError_t launch_fill(const kda_window_prefill_args& a, cudaStream_t s);
+cudaError_t launch_fill(const kda_window_prefill_args& a, bool beside_prefill, cudaStream_t s);
 cudaError_t launch_decode(const kda_window_decode_args& a, cudaStream_t s);
 }  // namespace win
 }  // namespace kda
@@ -178,7 +178,7 @@ kda_status kda_window_prefill(const kda_window_prefill_args* a, void* stream) {
     if (a->num_seqs == 0) return KDA_OK;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = a->T_total > 0 ? kda::win::launch_prefill(*a, s) : cudaSuccess;
-    if (e == cudaSuccess && a->k_cache && a->Tk_total > 0) e = kda::win::launch_fill(*a, s);
+    if (e == cudaSuccess && a->k_cache && a->Tk_total > 0) e = kda::win::launch_fill(*a, a->T_total > 0, s);
     return done(e);
 }
 

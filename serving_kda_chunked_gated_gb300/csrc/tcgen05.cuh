@@ -265,8 +265,9 @@ TC_DEV bool drain_phase(uint64_t* mbar, uint32_t n_issued) {
     return n_issued == 0 || mbar_wait_bounded(mbar, (n_issued - 1) & 1u, WAIT_POLLS);
 }
 
-// Programmatic dependent launch: a grid that may start while the one before ends waits here
-// for that one, its writes included.
+// Programmatic dependent launch: a grid that may start while the one before ends (or once every
+// CTA of that one has said so) waits here for its end, its writes included.
+TC_DEV void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 TC_DEV void wait_prerequisites() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Error word bits set by a kernel whose bounded wait ran out

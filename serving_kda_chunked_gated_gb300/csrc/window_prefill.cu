@@ -218,6 +218,7 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     volatile int* abort = &s_abort;
 
+    if (p.a.k_cache) tc::launch_dependents();      // the cache fill, on the SMs that this grid leaves
     if (tid == 0) {
         for (int i = 0; i < ROUNDS; ++i) { tc::mbar_init(&full[i], 2); tc::mbar_init(&empty[i], 2); }
         for (int i = 0; i < UNITS; ++i) tc::mbar_init(&u_full[i], 1);
