@@ -28,10 +28,10 @@
 //
 // Neither is near HBM: prep is bound by the issue and latency of the inverse (some 19000 cycles
 // of an SM per chunk and value head), the scan by its chain K S -> R -> T R -> V'' -> K^T V'' -> S,
-// some 4550 cycles a chunk of which 1450 are MMAs, 1600 the rows' arithmetic and 1300 the
+// some 4450 cycles a chunk of which 1450 are MMAs, 1600 the rows' arithmetic and 1300 the
 // hand-overs between them; 32 columns rather than 64 or 128 because 32 heads then fill 128 SMs.
-// Measured: 131072 tokens, 16 key and 32 value heads, S0: 4.29 ms (30.5 M tokens/s); 8192
-// tokens, 32 / 32 heads: 0.30 ms, one half prep and one half scan.
+// Measured: 131072 tokens, 16 key and 32 value heads, S0: 4.20 ms (31.2 M tokens/s); 8192
+// tokens, 32 / 32 heads: 0.29 ms, one half prep and one half scan.
 #include <math.h>
 
 #include <algorithm>
