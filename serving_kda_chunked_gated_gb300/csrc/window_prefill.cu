@@ -56,6 +56,12 @@ struct PF {
     static constexpr int SB = KT * D * 2;           // bytes of one K or V tile (ring slot)
     static constexpr int SLOTS = D == 128 ? 5 : 9;
     static constexpr int SMEM = 2 * QB + SLOTS * SB + 1024;   // + alignment slack
+    // TMEM columns: S of both tiles, O of both, and P where there is room beside them: S of the next
+    // step is then formed while this step's weights are, and the tiles take no turns (16384 tokens, 24 / 8
+    // heads of 64, window 512: 165 -> 154 us; window 4096, where the exponentials decide, no
+    // change).  Otherwise P takes the place of S.
+    static constexpr bool EARLY = D == 64;
+    static constexpr int P0 = EARLY ? 384 : 0, PSTEP = EARLY ? 64 : 128;
 };
 
 __device__ int g_window_error;              // ERR_ bits of calls whose bounded waits gave up (sticky until read)
@@ -207,7 +213,7 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
     using L = PF<D>;
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t full[ROUNDS], empty[ROUNDS], edge, q_full, q_empty, s_full[2], p_full[2][2], o_full[2],
-        l_full[2], o_empty[2], u_full[UNITS], turn[2], drained;
+        l_full[2], o_empty[2], u_full[UNITS], turn[2], s_free[2], pv_done[2], drained;
     __shared__ Unit s_unit[UNITS];
     __shared__ float s_l[2][128];
     __shared__ uint32_t s_tmem;
@@ -228,7 +234,9 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&s_full[i], 1);
             tc::mbar_init(&turn[i], 1);
-            tc::mbar_init(&p_full[i][0], 4);       // warps
+            tc::mbar_init(&s_free[i], 4);          // warps
+            tc::mbar_init(&pv_done[i], 1);
+            tc::mbar_init(&p_full[i][0], 4);
             tc::mbar_init(&p_full[i][1], 4);
             tc::mbar_init(&o_full[i], 1);
             tc::mbar_init(&l_full[i], 4);
@@ -330,7 +338,7 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
             }
         } else if (warp < 15) {
             // ---------------- MMAs of tile t: the warp computes together, one lane issues ----------------
-            // The tiles take turns: A's products of a round, B's, A's of the next round, handed on by the
+            // d = 128: the tiles take turns: A's products of a round, B's, A's of the next round, handed on by the
             // barriers `turn`.  One tile's S is so ready while the other's products run, and the two
             // softmaxes stay half a round apart; with the products interleaved both S arrive together
             // and the softmaxes share the issue slots while the tensor core waits (4600 cycles a round).
@@ -356,18 +364,19 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
                 if (steps >= k0 + 4) {              // without a test between the products
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        tc::mma_f16_ts_elect(tmu + 256 + t * D, tmu + t * 128 + (k0 + k) * 8, vd + (k0 + k) * (2048 >> 4), id,
+                        tc::mma_f16_ts_elect(tmu + 256 + t * D, tmu + L::P0 + t * L::PSTEP + (k0 + k) * 8, vd + (k0 + k) * (2048 >> 4), id,
                                              !(first && k0 + k == 0));
                 } else {
 #pragma unroll 1
                     for (int k = k0; k < steps; ++k)
-                        tc::mma_f16_ts_elect(tmu + 256 + t * D, tmu + t * 128 + k * 8, vd + k * (2048 >> 4), id,
+                        tc::mma_f16_ts_elect(tmu + 256 + t * D, tmu + L::P0 + t * L::PSTEP + k * 8, vd + k * (2048 >> 4), id,
                                              !(first && k == 0));
                 }
             };
             // Round r of A waits for B's round r - 1, that of B for A's round r.
-            auto my_turn = [&](uint32_t r) { return t ? wait_warp(&turn[1], r & 1, limit, abort) : r == 0 || wait_warp(&turn[0], (r - 1) & 1, limit, abort); };
+            auto my_turn = [&](uint32_t r) { return L::EARLY ? true : t ? wait_warp(&turn[1], r & 1, limit, abort) : r == 0 || wait_warp(&turn[0], (r - 1) & 1, limit, abort); };
             auto hand_on = [&] {
+                if (L::EARLY) return;
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&turn[1 - t]);
             };
@@ -413,6 +422,14 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
                     ks = ks + 2 >= L::SLOTS ? ks + 2 - L::SLOTS : ks + 2;
                     const int steps = width_of(x, i) / 16;
                     ok = wait_warp(&full[rd % ROUNDS], (rd / ROUNDS) & 1, limit, abort);
+                    if (L::EARLY && !last) {           // S has been read: the next one
+                        ok = ok && wait_warp(&s_free[t], np & 1, limit, abort);
+                        tc::fence_after_sync();
+                        if (!ok) break;
+                        qk(ks, width_of(x, i + 1));
+                        tc::mma_commit_elect(&s_full[t]);
+                        if (i + 2 == x.ntiles) tc::mma_commit_elect(&q_empty);
+                    }
                     if (ok && i == 0 && nu > 0) ok = wait_warp(&o_empty[t], (nu - 1) & 1, limit, abort);
                     ok = ok && my_turn(rd) && wait_warp(&p_full[t][0], np & 1, limit, abort);
                     tc::fence_after_sync();
@@ -421,6 +438,7 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
                     tc::fence_after_sync();
                     if (ok) pv(vs, 1, steps, i == 0);
                     if (!ok) break;
+                    if (L::EARLY) tc::mma_commit_elect(&pv_done[t]);
                     if (last) {
                         tc::mma_commit_elect(&o_full[t]);
                         if (next_unit) {
@@ -430,14 +448,14 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
                             y = tiles_of(nu + 1);
                         }
                     }
-                    if (more) {
+                    if (L::EARLY ? last && more : more) {
                         qk(ks, last ? width_of(y, 0) : width_of(x, i + 1));
                         tc::mma_commit_elect(&s_full[t]);
                     }
                     hand_on();
                     tc::mma_commit_elect(&empty[rd % ROUNDS]);
                     // the S issued in this round was a unit's last: its Q may be overwritten
-                    if (last ? more && y.ntiles == 1 : i + 2 == x.ntiles) tc::mma_commit_elect(&q_empty);
+                    if (last ? more && y.ntiles == 1 : !L::EARLY && i + 2 == x.ntiles) tc::mma_commit_elect(&q_empty);
                 }
                 x = y;
             }
@@ -506,6 +524,7 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
         const int t = warp >> 2, r = tid & 127;
         const uint32_t ts = tm + t * 128 + ((uint32_t)(warp & 3) << 21);        // this warp's 32 lanes of S (and P)
         const uint32_t to = tm + 256 + t * D + ((uint32_t)(warp & 3) << 21);
+        const uint32_t tp = tm + L::P0 + t * L::PSTEP + ((uint32_t)(warp & 3) << 21);
         uint32_t np = 0, nu = 0;
         bool ok = true;
         for (; unit_of(nu) < p.units && ok; ++nu) {
@@ -564,7 +583,7 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
                         const __nv_bfloat162 h = __floats2bfloat162_rn(e0, e1);
                         w[c >> 1] = *reinterpret_cast<const uint32_t*>(&h);
                     }
-                    tc::tmem_st16u(ts + k * 16, w);
+                    tc::tmem_st16u(tp + k * 16, w);
                 };
                 // The row's reference is the largest score known before this tile (on the first tile: its
                 // own first half's), so the exponentials need not wait for the tile's maximum, nor for its
@@ -581,6 +600,14 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
                     if (32 < width) m = largest(1, m);
                     ref = m * p.c;
                 }
+                if (L::EARLY && np > 0) {              // P and O of the step before are the row's again
+                    ok = wait_warp(&pv_done[t], (np - 1) & 1, limit, abort);
+                    if (!ok) {
+                        tc::tmem_ld_wait();            // the second half of S is still on its way
+                        break;
+                    }
+                    tc::fence_after_sync();
+                }
                 for (bool again = false;; again = true) {
                     const float base = ref == -INFINITY ? 0.f : -ref;   // nothing seen yet: every weight is exp2(-inf) = 0
                     float n0 = 0.f, n1 = 0.f;
@@ -589,6 +616,10 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
                     if (!again) {
                         tc::tmem_ld_wait();
                         after_wait(s + 64, 64);
+                        if (L::EARLY) {
+                            tc::fence_before_sync();
+                            tc::mbar_arrive_warp(&s_free[t]);
+                        }
                         if (64 < width) mask(2);
                         if (96 < width) mask(3);
                         float m = largest(0, -INFINITY);
