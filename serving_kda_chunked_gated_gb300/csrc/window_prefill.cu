@@ -595,11 +595,9 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
                 if (64 < width) tc::tmem_ld64(ts + 64, s + 64);
                 mask(0);
                 if (32 < width) mask(1);
-                if (i == 0) {
-                    float m = largest(0, -INFINITY);
-                    if (32 < width) m = largest(1, m);
-                    ref = m * p.c;
-                }
+                float m01 = largest(0, -INFINITY);     // of the first half: in the tile's maximum, too (2 %)
+                if (32 < width) m01 = largest(1, m01);
+                if (i == 0) ref = m01 * p.c;
                 if (L::EARLY && np > 0) {              // P and O of the step before are the row's again
                     ok = wait_warp(&pv_done[t], (np - 1) & 1, limit, abort);
                     if (!ok) {
@@ -622,8 +620,7 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
                         }
                         if (64 < width) mask(2);
                         if (96 < width) mask(3);
-                        float m = largest(0, -INFINITY);
-                        if (32 < width) m = largest(1, m);
+                        float m = m01;
                         if (64 < width) m = largest(2, m);
                         if (96 < width) m = largest(3, m);
                         m *= p.c;
