@@ -25,9 +25,10 @@
 //
 // Two bounds meet: a round (both tiles' P V and Q K^T, d = 128) keeps the tensor core busy for
 // 2068 cycles, and its 2 x 128 x 128 exponentials the special-function units (16 a cycle) for
-// 2048.  Measured: 8192 tokens, 32 / 8 heads of 128, window 4096: 334 us, some 3700 cycles a
-// round (TMEM reads slow down while products run), 1.23 PFLOP/s; 131072 tokens, window 512:
-// 1.41 ms, where a unit has 5 rounds and its change (queries in, rows out) costs another.
+// 2048.  Measured: 8192 tokens, 32 / 8 heads of 128, window 4096: 331 us, some 3600 cycles a
+// round (TMEM reads slow down while products run, instructions arrive late), 1.24 PFLOP/s; 131072
+// tokens, window 512: 1.39 ms, where a unit has 5 rounds and its change (queries in, rows out)
+// costs another.
 #include <math.h>
 
 #include <algorithm>
