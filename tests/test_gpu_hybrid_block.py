@@ -124,3 +124,44 @@ def test_prompts_then_tokens(kda_lib, cuda_dev):
         for h in range(HQ):
             assert rel(got_w[n][:, h], rw[:, h]) < TOL and rel(got_w[n][lens[n]:, h], rw[lens[n]:, h]) < TOL
     assert (state_pool[[1, 4]] == 0).all() and (kc[[1, 4]] == 0).all()
+
+
+def test_two_streams_at_once(kda_lib, cuda_dev):
+    """Every mixer on two streams at the same time, workspaces apart: the bits of one call after another."""
+    import serving_kda_chunked_gated_gb300.kda as kda
+    bf = torch.bfloat16
+
+    def inputs(seed, lens):
+        g = torch.Generator().manual_seed(seed)
+        r = lambda *s: torch.randn(*s, generator=g)                                          # noqa: E731
+        T = sum(lens)
+        cu = torch.tensor([0] + list(torch.tensor(lens).cumsum(0)), dtype=torch.int32)
+        d = dict(q=r(T, 8, 128).to(bf), k=r(T, 4, 128).to(bf), v=r(T, 8, 128).to(bf), z=r(T, 8) - 3, beta=torch.sigmoid(r(T, 8)),
+                 A=torch.zeros(8), cos=r(T, 64), sin=r(T, 64), pos=torch.arange(T, dtype=torch.int32), cu=cu,
+                 kc=torch.zeros(len(lens), 210, 4, 128).to(bf), vc=torch.zeros(len(lens), 210, 4, 128).to(bf),
+                 last=torch.tensor(lens, dtype=torch.int32), ws=torch.zeros(1 << 25, dtype=torch.uint8))
+        return {n: x.to(cuda_dev) for n, x in d.items()}, cu
+
+    def run(d, cu, stream):
+        n = len(cu) - 1
+        o, S = kda.gdn_prefill(d["k"], d["k"], d["v"], d["z"], d["beta"], d["A"], d["cu"], cu, workspace=d["ws"], stream=stream)
+        q, k = kda.qk_norm_rope(d["q"], d["k"], d["cos"], d["sin"], d["pos"], stream=stream)
+        w = kda.window_prefill(q, k, k, 200, 10, d["cu"], cu, k_cache=d["kc"], v_cache=d["vc"], stream=stream)
+        kda.gdn_decode_step(k[:n], k[:n], d["v"][:n], d["z"][:n], d["beta"][:n], d["A"], S, stream=stream)
+        x = kda.window_decode(q[:n], k[:n], k[:n], d["kc"], d["vc"], d["last"], 200, 10, stream=stream)
+        return [o, S, q, k, w, x, d["kc"], d["vc"]]
+
+    sets = [([700, 30, 129], 1), ([64, 900], 2)]
+    alone = []
+    for lens, seed in sets:
+        alone.append([t.clone() for t in run(*inputs(seed, lens), torch.cuda.current_stream())])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(4):
+        data = [inputs(seed, lens) for lens, seed in sets]
+        torch.cuda.synchronize()
+        both = [run(*d, s) for d, s in zip(data, streams)]
+        torch.cuda.synchronize()
+        for got, want in zip(both, alone):
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert all(kda.device_error(d["ws"]) == kda.KDA_OK for d, _ in data) and kda.device_error(None) == kda.KDA_OK
