@@ -165,3 +165,46 @@ def test_two_streams_at_once(kda_lib, cuda_dev):
         for got, want in zip(both, alone):
             assert all(torch.equal(a, b) for a, b in zip(got, want))
         assert all(kda.device_error(d["ws"]) == kda.KDA_OK for d, _ in data) and kda.device_error(None) == kda.KDA_OK
+
+
+def test_offsets_past_32_bits(kda_lib, cuda_dev):
+    """State pools, ring caches and packed projections whose last elements lie behind 2^32 bytes (and
+    2^31 elements): the same bits as from small ones."""
+    import serving_kda_chunked_gated_gb300.kda as kda
+    bf = torch.bfloat16
+    g = torch.Generator().manual_seed(3)
+    r = lambda *s: torch.randn(*s, generator=g).to(cuda_dev)                                 # noqa: E731
+    # delta rule: the last slot of a pool of 2^17 + 1 states of 64 KiB (8.6 GB)
+    slots = 2 ** 17 + 1
+    q, k, v, z, beta, A = r(1, 1, 128).to(bf), r(1, 1, 128).to(bf), r(1, 1, 128).to(bf), r(1, 1), torch.sigmoid(r(1, 1)), r(1)
+    small = r(1, 1, 128, 128)
+    pool = torch.empty(slots, 1, 128, 128, device=cuda_dev)
+    pool[-1] = small[0]
+    at = torch.tensor([slots - 1], dtype=torch.int32, device=cuda_dev)
+    assert torch.equal(kda.gdn_decode_step(q, k, v, z, beta, A, pool, slots=at), kda.gdn_decode_step(q, k, v, z, beta, A, small))
+    assert torch.equal(pool[-1], small[0])
+    del pool
+    # window: positions near the end of rings of 2^21 + 300 rows of 8 heads of 128 (4.3 GB each)
+    W, rows = 250, 2 ** 21 + 300
+    q, k, v, hist = r(1, 16, 128).to(bf), r(1, 8, 128).to(bf), r(1, 8, 128).to(bf), r(W - 1, 8, 128).to(bf)
+    want = None
+    for n, pos in ((W, W - 1), (rows, rows - 1)):
+        kc, vc = (torch.empty(1, n, 8, 128, dtype=bf, device=cuda_dev) for _ in "kv")
+        kc[0, pos - W + 1:pos], vc[0, pos - W + 1:pos] = hist, -hist
+        o = kda.window_decode(q, k, v, kc, vc, torch.tensor([pos], dtype=torch.int32, device=cuda_dev), W)
+        assert torch.equal(kc[0, pos], k[0]) and torch.equal(vc[0, pos], v[0])
+        want = o if want is None else want
+        assert torch.equal(o, want)
+        del kc, vc
+    # norm and rotation, window prefill: tokens 2^31 + 64 elements apart
+    far = torch.empty(2 ** 31 + 4096, dtype=bf, device=cuda_dev)
+    step = 2 ** 31 + 64
+    tok = r(2, 16 + 2 + 2, 128).to(bf)
+    heads = lambda a, n: torch.as_strided(far, (2, n, 128), (step, 128, 1), a * 128)         # noqa: E731
+    heads(0, 20).copy_(tok)
+    cos, sin, pos = r(4, 64), r(4, 64), torch.tensor([1, 3], dtype=torch.int32, device=cuda_dev)
+    got = kda.qk_norm_rope(heads(0, 16), heads(16, 2), cos, sin, pos)
+    ref = kda.qk_norm_rope(tok[:, :16].contiguous(), tok[:, 16:18].contiguous(), cos, sin, pos)
+    assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+    got = kda.window_prefill(heads(0, 16), heads(16, 2), heads(18, 2), 5)
+    assert torch.equal(got, kda.window_prefill(*(x.contiguous() for x in (tok[:, :16], tok[:, 16:18], tok[:, 18:])), 5))
