@@ -3,12 +3,12 @@
 // validation and dispatch.  Nothing is enqueued when validation fails.
 #include <math.h>
 
+#include "gdn.cuh"
 #include "kda_common.cuh"
 
 namespace kda {
 namespace gdn {
 cudaError_t launch_decode(const kda_gdn_decode_args& a, cudaStream_t s);
-cudaError_t launch_recurrent(const kda_gdn_prefill_args& a, cudaStream_t s);
 size_t chunked_workspace_size(const kda_gdn_prefill_args& a);
 cudaError_t launch_chunked(const kda_gdn_prefill_args& a, cudaStream_t s);
 }  // namespace gdn
@@ -91,7 +91,9 @@ kda_status kda_gdn_prefill_recurrent(const kda_gdn_prefill_args* a, void* stream
     if (st != KDA_OK) return st;
     kda_gdn_prefill_args r = *a;
     r.workspace = nullptr;                // has none, whatever the field holds
-    return done(kda::gdn::launch_recurrent(r, reinterpret_cast<cudaStream_t>(stream)));
+    kda::gdn::Sequences all;
+    all.count = 0;
+    return done(kda::gdn::launch_recurrent(r, all, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 kda_status kda_gdn_decode_step(const kda_gdn_decode_args* a, void* stream) {

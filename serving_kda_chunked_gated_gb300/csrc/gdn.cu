@@ -7,7 +7,9 @@
 // The columns of S (value channels) are independent of one another, so a state
 // can be cut into column slices of COLS channels, one CTA each: nothing is
 // exchanged between the slices, only k, q (2 x 128 values) are read again.
+#include "gdn.cuh"
 #include "kda_common.cuh"
+#include "tcgen05.cuh"
 
 namespace kda {
 namespace gdn {
@@ -148,13 +150,12 @@ KDA_DEV float load1(const void* p, size_t i) {
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(NT)
-gdn_recurrent_kernel(kda_gdn_prefill_args a) {
+KDA_DEV void recurrence(const kda_gdn_prefill_args& a, const Sequences& which) {
     constexpr int COLS = 32, NS = D / COLS;
     using L = Slice<COLS>;
     const int slice = blockIdx.x % NS;
     const int h = (blockIdx.x / NS) % a.Hv;
-    const int n = blockIdx.x / NS / a.Hv;
+    const int place = blockIdx.x / NS / a.Hv, n = which.count ? which.seq[place] : place;
     const int hk = h / (a.Hv / a.Hk);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int cg = tid % L::CG, rg = tid / L::CG;
@@ -223,13 +224,28 @@ gdn_recurrent_kernel(kda_gdn_prefill_args a) {
     }
 }
 
-cudaError_t launch_recurrent(const kda_gdn_prefill_args& a, cudaStream_t s) {
-    const long blocks = (long)a.num_seqs * a.Hv * 4;
+template <bool BF16>
+__global__ void __launch_bounds__(NT)
+gdn_recurrent_kernel(const __grid_constant__ kda_gdn_prefill_args a, const __grid_constant__ Sequences which) {
+    recurrence<BF16>(a, which);
+    tc::wait_prerequisites();       // beside the scan of other sequences: this grid's end is not to come first
+}
+
+cudaError_t launch_recurrent(const kda_gdn_prefill_args& a, const Sequences& which, cudaStream_t s) {
+    const long blocks = (long)(which.count ? which.count : a.num_seqs) * a.Hv * 4;
     if (blocks == 0) return cudaSuccess;
-    if (a.qkv_dtype == KDA_BF16) gdn_recurrent_kernel<true><<<(unsigned)blocks, NT, 0, s>>>(a);
-    else gdn_recurrent_kernel<false><<<(unsigned)blocks, NT, 0, s>>>(a);
-    count_launches(1);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(NT);
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = which.count ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, a.qkv_dtype == KDA_BF16 ? gdn_recurrent_kernel<true> : gdn_recurrent_kernel<false>, a, which);
+    if (e == cudaSuccess) count_launches(1);
+    return e;
 }
 
 }  // namespace gdn

@@ -36,6 +36,7 @@
 
 #include <algorithm>
 
+#include "gdn.cuh"
 #include "kda_common.cuh"
 #include "tcgen05.cuh"
 #include "tma_host.cuh"
@@ -55,17 +56,25 @@ constexpr int REC_THI = 0, REC_TLO = TRI, REC_A = 2 * TRI, REC_F = 3 * TRI;
 constexpr int REC = 3 * TRI + C * 16 + 128;   // + four factors per token + e^{g_C} and the record's ERR_ bits
 constexpr int WS_HEAD = 256;                  // the error word's line
 
-// For up to this many sequences the host lays the work out, by value.  Scans of the longest start
-// first: one of 4097 tokens among eight shorter ones otherwise starts when these are done.
-// Beyond, every CTA adds up cu_seqlens itself.
-constexpr int MAX_LISTED = 1024;
+// For up to MAX_LISTED sequences the host lays the work out.  Scans of the longest start first: one of
+// 4097 tokens among eight shorter ones otherwise starts when these are done.  Beyond, every CTA
+// adds up cu_seqlens itself.
+//
+// A chunk takes its two kernels 36 us however full it is, and where the GPU is full 240 ns for each value
+// head; the recurrence 1 us a token, and where the GPU is full 20 ns for each state and 11 for each of its
+// tokens.  So batches of at most SHORT tokens a sequence take the recurrence, and so do such sequences
+// in a listed batch with longer ones where the estimates say so, in a launch of their own beside the
+// scan's last CTAs: 200 sequences of one token and one of 2000, 32 heads: 1490 us all in chunks, 239 so;
+// one of 9 and one of 6433: 244, 261.
+constexpr int SHORT = 24;
 
 struct Params {
     kda_gdn_prefill_args a;
     uint32_t wait_limit;
+    int tail;                                 // a launch for the short sequences follows the scan
     int listed;                               // whether what follows is filled in
-    uint32_t first[MAX_LISTED + 1];           // chunks before sequence n
-    uint16_t order[MAX_LISTED];               // sequences, longest first
+    uint32_t first[MAX_LISTED + 1];           // chunks before sequence n (a short one has none)
+    uint16_t order[MAX_LISTED];               // the sequences with chunks, longest first
 };
 
 // byte offset of 16-byte piece c (0 .. 7) of row r in a slab of 128-byte rows
@@ -568,6 +577,7 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tm = s_tmem;
+    if (p.tail) tc::launch_dependents();
     tc::wait_prerequisites();                 // prep's records
     const long base = chunks_before(p, n);
     const uint8_t* recs = reinterpret_cast<const uint8_t*>(a.workspace) + WS_HEAD + (base * a.Hv + h) * (size_t)REC;
@@ -905,36 +915,42 @@ static long count_chunks(const kda_gdn_prefill_args& a) {
     return s;
 }
 
-cudaError_t launch_recurrent(const kda_gdn_prefill_args& a, cudaStream_t s);
-
 size_t chunked_workspace_size(const kda_gdn_prefill_args& a) {
     return WS_HEAD + (size_t)count_chunks(a) * a.Hv * REC;
 }
 
 cudaError_t launch_chunked(const kda_gdn_prefill_args& a, cudaStream_t s) {
+    const int32_t* cu = a.cu_seqlens_host;
+    const auto len = [cu](int n) { return cu[n + 1] - cu[n]; };
     Params p;
+    Sequences few;                            // the short ones
     p.a = a;
     p.wait_limit = wait_limit();
-    const long chunks = count_chunks(a);
     p.listed = a.num_seqs <= MAX_LISTED;
+    few.count = 0;
+    long chunks = count_chunks(a);
+    int scans = a.num_seqs, longest = 0;
+    for (int n = 0; n < a.num_seqs; ++n) longest = std::max(longest, len(n));
+    if (longest <= SHORT) return launch_recurrent(a, few, s);       // all of them; clears the error word
     if (p.listed) {
-        const int32_t* cu = a.cu_seqlens_host;
+        long shorts = 0, tokens = 0;
+        int most = 0;                         // tokens of a short one
+        for (int n = 0; n < a.num_seqs; ++n)
+            if (len(n) <= SHORT) { ++shorts; tokens += len(n); most = std::max(most, len(n)); }
+        const double chunked = 0.24 * shorts * a.Hv, apart = 4 + std::max((double)most, (0.02 * shorts + 0.011 * tokens) * a.Hv);   // us
+        const int least = apart < chunked ? SHORT + 1 : 0;
         p.first[0] = 0;
+        scans = 0;
         for (int n = 0; n < a.num_seqs; ++n) {
-            p.first[n + 1] = p.first[n] + (uint32_t)((cu[n + 1] - cu[n] + C - 1) / C);
-            p.order[n] = (uint16_t)n;
+            const bool in_chunks = len(n) >= least;
+            p.first[n + 1] = p.first[n] + (in_chunks ? (uint32_t)((len(n) + C - 1) / C) : 0);
+            if (in_chunks) p.order[scans++] = (uint16_t)n;
+            else few.seq[few.count++] = (uint16_t)n;
         }
-        std::stable_sort(p.order, p.order + a.num_seqs,
-                         [cu](uint16_t x, uint16_t y) { return cu[x + 1] - cu[x] > cu[y + 1] - cu[y]; });
+        std::stable_sort(p.order, p.order + scans, [len](uint16_t x, uint16_t y) { return len(x) > len(y); });
+        chunks = p.first[a.num_seqs];
     }
-    // Only a few tokens per sequence: a chunk takes its two kernels 36 us however full it is, the
-    // recurrence 1 us per token (32 heads); 64 sequences of 16 heads 264 us, and 11 us per token.
-    int longest = 0;
-    for (int n = 0; n < a.num_seqs; ++n) {
-        const int len = a.cu_seqlens_host[n + 1] - a.cu_seqlens_host[n];
-        longest = len > longest ? len : longest;
-    }
-    if (longest <= 24) return launch_recurrent(a, s);       // clears the error word
+    p.tail = few.count > 0;
     CUtensorMap mq = {}, mk = {}, mv = {}, mo = {};
     cudaError_t e = make_map_heads(&mq, a.q, DH, a.Hk, a.T_total, (uint64_t)a.Hk * DH, 1, C);
     if (e == cudaSuccess) e = make_map_heads(&mk, a.k, DH, a.Hk, a.T_total, (uint64_t)a.Hk * DH, 1, C);
@@ -947,7 +963,7 @@ cudaError_t launch_chunked(const kda_gdn_prefill_args& a, cudaStream_t s) {
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     count_launches(1);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((long)a.num_seqs * a.Hv * (DH / COLS)));
+    cfg.gridDim = dim3((unsigned)((long)scans * a.Hv * (DH / COLS)));
     cfg.blockDim = dim3(ST);
     cfg.dynamicSmemBytes = S_SMEM;
     cfg.stream = s;
@@ -961,7 +977,10 @@ cudaError_t launch_chunked(const kda_gdn_prefill_args& a, cudaStream_t s) {
     e = cudaLaunchKernelEx(&cfg, gdn_scan_kernel, p, mq, mk, mv, mo);
     if (e != cudaSuccess) return e;
     count_launches(1);
-    return cudaGetLastError();
+    if (!few.count) return cudaSuccess;
+    kda_gdn_prefill_args rest = a;
+    rest.workspace = nullptr;                 // the error word is the others'
+    return launch_recurrent(rest, few, s);
 }
 
 }  // namespace gdn

@@ -214,3 +214,29 @@ def test_prefill_no_tokens(kda_lib, cuda_dev):
         assert torch.equal(kda.gdn_prefill(*args, S0=S0, recurrent=rec)[1], S0)
         assert (kda.gdn_prefill(*args, recurrent=rec)[1] == 0).all()
         assert kda.gdn_prefill(*args, want_state=False, recurrent=rec)[0].numel() == 0
+
+
+@pytest.mark.parametrize("gate", ["softplus", "bounded"])
+def test_prefill_short_sequences_beside_long_ones(kda_lib, cuda_dev, gate):
+    """One-token sequences packed with prompts (the former by the recurrence, beside the latter's scan):
+    states in place, and what a captured call leaves on its second replay."""
+    import serving_kda_chunked_gated_gb300.kda as kda
+    lens = [1] * 20 + [200, 0, 24, 25] + [1] * 20 + [129, 3]
+    d, cu = gdn_inputs(lens, 2, 4, seed=5)
+    S0 = d.pop("S0")
+    ro, rS = gdn_reference(**d, cu=cu, S0=S0, gate=gate)
+    g, cud, S = _dev(d, cuda_dev), cu.to(cuda_dev), S0.to(cuda_dev)
+    ws = torch.empty(1 << 26, dtype=torch.uint8, device=cuda_dev).fill_(255)
+    out = {"o": torch.empty_like(g["v"]), "S_T": S}
+    call = lambda: kda.gdn_prefill(**g, cu_seqlens=cud, cu_seqlens_host=cu, gate=gate, S0=S, out=out, workspace=ws)     # noqa: E731
+    call()
+    assert kda.device_error(ws) == kda.KDA_OK
+    _check(out["o"], S, ro, rS, lens)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for _ in range(2):
+        S.copy_(S0)
+        graph.replay()
+        _check(out["o"], S, ro, rS, lens)
+    assert kda.device_error(ws) == kda.KDA_OK
