@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import threading
 
 import torch
 
@@ -304,14 +305,39 @@ def prefill_raw(args: PrefillArgs, stream=None, recurrent: bool = False):
 
 
 PREFILL_MIN_WORKSPACE = 256   # smallest workspace of the tensor-core path (single-pass schedule)
-_WS_CACHE = {}                # prefill(workspace="cache"): one buffer per device
+_WS_CACHE = {}                # workspace="cache": one buffer per device, stream and host thread
+
+
+def _cache_key(dev):
+    """What the calls that share a cached buffer have in common: they follow one another on
+    one stream.  Calls of two host threads may interleave their kernels on it."""
+    return dev.type, dev.index, torch.cuda.current_stream(dev).cuda_stream, threading.get_ident()
+
+
+def _cached_workspace(dev, need):
+    """The workspace="cache" buffer of ``dev``'s current stream and this thread, grown on demand:
+    it was allocated on that stream, so a buffer that is replaced goes back to it, behind its last use.
+    During a capture a buffer of the graph's own pool instead: a cached one could be
+    replaced, and its memory handed on, while the graph still replays."""
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _cached_workspace(dev, need)
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    key = _cache_key(dev)
+    ws = _WS_CACHE.get(key)
+    if ws is None or ws.numel() < need:
+        _WS_CACHE[key] = ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    return ws
 
 
 def cached_workspace(dev):
-    """The buffer ``prefill(workspace="cache")`` uses on ``dev`` (None before the
-    first such call)."""
+    """The buffer that workspace="cache" uses on ``dev``'s current stream in this thread
+    (None before the first such call)."""
     dev = torch.device(dev)
-    return _WS_CACHE.get((dev.type, dev.index if dev.index is not None else torch.cuda.current_device()))
+    if dev.index is None:
+        dev = torch.device(dev.type, torch.cuda.current_device())
+    return _WS_CACHE.get(_cache_key(dev))
 
 
 def release_workspace_cache():
@@ -408,13 +434,10 @@ def prefill(q, k, v, z, beta, A, cu_seqlens=None, S0=None, g_in=None, norm_w=Non
         if need > 0:
             # a caller's workspace is used as given: its size picks the schedule
             # (>= need: chunk-parallel; >= PREFILL_MIN_WORKSPACE: single pass);
-            # "cache" reuses one buffer per device, grown on demand
+            # "cache" reuses one buffer per device, stream and thread, grown on demand
             if isinstance(workspace, str) and workspace == "cache":
-                key = (dev.type, dev.index)
-                ws = _WS_CACHE.get(key)
-                if ws is None or ws.numel() < need:
-                    _WS_CACHE[key] = ws = torch.empty(need, dtype=torch.uint8, device=dev)
-                workspace = ws
+                with torch.cuda.stream(stream):       # (None: the current one)
+                    workspace = _cached_workspace(dev, need)
             elif workspace is None:
                 workspace = torch.empty(need, dtype=torch.uint8, device=dev)
             args.workspace = workspace.data_ptr()
@@ -681,14 +704,6 @@ def _gate_code(gate):
     return GATES[gate]
 
 
-def _cached_workspace(dev, need):
-    key = (dev.type, dev.index)
-    ws = _WS_CACHE.get(key)
-    if ws is None or ws.numel() < need:
-        _WS_CACHE[key] = ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    return ws
-
-
 @_on_stream
 def gdn_prefill(q, k, v, z, beta, A, cu_seqlens=None, cu_seqlens_host=None, S0=None, g_min=-5.0, scale=1.0,
                 qk_l2norm=True, want_o=True, want_state=True, out=None, recurrent=False, workspace=None,
@@ -700,8 +715,8 @@ def gdn_prefill(q, k, v, z, beta, A, cu_seqlens=None, cu_seqlens_host=None, S0=N
     per-token recurrence); z, beta: [T, Hv] f32; A: [Hv] f32; cu_seqlens int32 [N+1]
     on the device (None = one sequence) and its host copy; S0 [N, Hv, 128, 128] f32
     or None.  out: {"o": ..., "S_T": ...} to write into.  workspace as for ``prefill``
-    (a uint8 tensor, None, or "cache": one buffer per device, for calls that follow
-    one another on one stream).  Returns (o, S_T).
+    (a uint8 tensor; None: one for this call; or "cache": a buffer kept for the calls of
+    this thread on this stream, while a graph is captured one of its own).  Returns (o, S_T).
     """
     dev = _cuda_device(q, "q")
     T, Hk, dk = q.shape

@@ -1,0 +1,146 @@
+"""workspace="cache": which calls share a buffer (no GPU: torch's stream queries are replaced), and
+what the calls compute on the GPU when streams, threads and captured graphs use it side by side."""
+import threading
+import types
+
+import pytest
+import torch
+
+from hybrid_testutil import gdn_inputs
+
+
+@pytest.fixture
+def fake(monkeypatch):
+    """The current stream and whether it is being captured, as the test sets them."""
+    import serving_kda_chunked_gated_gb300.kda as kda
+    now = types.SimpleNamespace(kda=kda, stream=0, capturing=False, dev=torch.device("cpu"))
+    monkeypatch.setattr(kda, "_WS_CACHE", {})
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: None)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: types.SimpleNamespace(cuda_stream=now.stream))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: now.capturing)
+    return now
+
+
+def test_one_buffer_for_each_stream(fake):
+    get = lambda n: fake.kda._cached_workspace(fake.dev, n)                  # noqa: E731
+    a = get(100)
+    assert get(50) is a and get(100) is a
+    fake.stream = 7
+    b = get(100)
+    assert b is not a and b.data_ptr() != a.data_ptr()
+    assert get(200) is not b and get(10).numel() == 200
+    fake.stream = 0
+    assert get(100) is a                         # untouched by the other stream's growth
+
+
+def test_one_buffer_for_each_thread(fake):
+    """Two threads may interleave their kernels on one stream."""
+    mine, other = fake.kda._cached_workspace(fake.dev, 100), []
+    t = threading.Thread(target=lambda: other.append(fake.kda._cached_workspace(fake.dev, 100)))
+    t.start()
+    t.join()
+    assert other[0].data_ptr() != mine.data_ptr()
+
+
+def test_captured_calls_keep_away_from_the_cache(fake):
+    a = fake.kda._cached_workspace(fake.dev, 100)
+    fake.capturing = True
+    b, c = (fake.kda._cached_workspace(fake.dev, 100) for _ in range(2))
+    assert len({x.data_ptr() for x in (a, b, c)}) == 3
+    big = fake.kda._cached_workspace(fake.dev, 1000)
+    fake.capturing = False
+    assert fake.kda._cached_workspace(fake.dev, 100) is a and big.numel() == 1000
+
+
+def _call(kda, g, cu, cu_host, **kw):
+    return kda.gdn_prefill(**g, cu_seqlens=cu, cu_seqlens_host=cu_host, workspace="cache", **kw)
+
+
+def _gdn(lens, seed, dev):
+    d, cu = gdn_inputs(lens, 4, 8, seed=seed)
+    return {k: x.to(dev) for k, x in d.items()}, cu.to(dev), cu
+
+
+@pytest.mark.gpu
+def test_two_streams_and_a_thread(kda_lib, cuda_dev):
+    """Calls on two streams, and of two threads on one stream, at the same time: the bits of calls alone."""
+    import serving_kda_chunked_gated_gb300.kda as kda
+    sets = [_gdn(lens, seed, cuda_dev) for seed, lens in enumerate(([900, 30, 129], [64, 1100]))]
+    alone = [_call(kda, *s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            got[i].append(_call(kda, *sets[i], stream=s))
+    torch.cuda.synchronize()
+
+    def work(i):
+        for _ in range(20):
+            got[i].append(_call(kda, *sets[i], stream=streams[0]))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert len(got[i]) == 25
+        assert all(torch.equal(a, b) for r in got[i] for a, b in zip(r, alone[i]))
+    kda.release_workspace_cache()
+
+
+@pytest.mark.gpu
+def test_graph_then_a_larger_call_then_replay(kda_lib, cuda_dev):
+    """A captured call, a larger eager one, other tensors over whatever memory that gave back, a replay."""
+    import serving_kda_chunked_gated_gb300.kda as kda
+    kda.release_workspace_cache()
+    small, large = _gdn([400], 5, cuda_dev), _gdn([3000, 700], 6, cuda_dev)
+    want, want_l = _call(kda, *small), _call(kda, *large)
+    kda.release_workspace_cache()
+    _call(kda, *small)                                     # the cache holds a buffer that the graph could have taken
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, S = _call(kda, *small)
+        o2, S2 = _call(kda, *small)                        # two calls of one capture
+    got = _call(kda, *large)
+    filler = [torch.full((1 << 20,), float("nan"), device=cuda_dev) for _ in range(64)]
+    for _ in range(2):
+        for x in (o, S, o2, S2):
+            x.zero_()
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip((o, S, o2, S2), want + want))
+    assert all(torch.equal(a, b) for a, b in zip(got, want_l))
+    assert all(torch.isnan(x).all() for x in filler)
+    kda.release_workspace_cache()
+
+
+@pytest.mark.gpu
+def test_prefill_of_the_channel_gated_rule(kda_lib, cuda_dev):
+    """``prefill`` takes its cached buffer the same way."""
+    import serving_kda_chunked_gated_gb300.kda as kda
+    kda.release_workspace_cache()
+    g = torch.Generator().manual_seed(2)
+
+    def inputs(T):
+        r = lambda *s: torch.randn(*s, generator=g)        # noqa: E731
+        q, k, v = (r(T, 4, 128).to(torch.bfloat16) for _ in range(3))
+        cu = torch.tensor([0, T], dtype=torch.int32)
+        return [x.to(cuda_dev) for x in (q, k, v, r(T, 4, 128), torch.sigmoid(r(T, 4)), torch.zeros(4), cu)]
+
+    sets = [inputs(500), inputs(1300)]
+    alone = [kda.prefill(*x) for x in sets]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[kda.prefill(*x, workspace="cache", stream=s) for x, s in zip(sets, streams)] for _ in range(4)]
+    torch.cuda.synchronize()
+    for r in got:
+        for have, want in zip(r, alone):
+            assert torch.equal(have[0], want[0]) and torch.equal(have[1], want[1])
+    assert kda.cached_workspace(cuda_dev) is None          # nothing ran on this stream
+    with torch.cuda.stream(streams[1]):
+        assert kda.device_error(kda.cached_workspace(cuda_dev)) == kda.KDA_OK
+    kda.release_workspace_cache()
