@@ -314,20 +314,21 @@ def _cache_key(dev):
     return dev.type, dev.index, torch.cuda.current_stream(dev).cuda_stream, threading.get_ident()
 
 
-def _cached_workspace(dev, need):
+def _cached_workspace(dev, need, cache=None):
     """The workspace="cache" buffer of ``dev``'s current stream and this thread, grown on demand:
     it was allocated on that stream, so a buffer that is replaced goes back to it, behind its last use.
     During a capture a buffer of the graph's own pool instead: a cached one could be
     replaced, and its memory handed on, while the graph still replays."""
     if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            return _cached_workspace(dev, need)
+            return _cached_workspace(dev, need, cache)
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(need, dtype=torch.uint8, device=dev)
+    cache = _WS_CACHE if cache is None else cache
     key = _cache_key(dev)
-    ws = _WS_CACHE.get(key)
+    ws = cache.get(key)
     if ws is None or ws.numel() < need:
-        _WS_CACHE[key] = ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        cache[key] = ws = torch.empty(need, dtype=torch.uint8, device=dev)
     return ws
 
 
@@ -345,7 +346,7 @@ def release_workspace_cache():
     _WS_CACHE.clear()
 
 
-_STAGING = {}                 # prefill_from_host: one staging buffer per device
+_STAGING = {}                 # prefill_from_host: one staging buffer per device, stream and host thread
 
 
 def prefill_from_host(q, k, v, z, beta, A, S0=None, g_in=None, norm_w=None, out=None, slab=16384,
@@ -356,8 +357,8 @@ def prefill_from_host(q, k, v, z, beta, A, S0=None, g_in=None, norm_w=None, out=
     the compute.  q, k, v, g_in [T, H, d] bf16 (or f32), z [T, H, d] f32, beta
     [T, H], A [H], S0 [1, H, d, d] or None, all host tensors; out = (o, y, S_T)
     host tensors (y None without g_in), allocated pinned when None.  The device
-    staging comes from a per-device cache.  Returns (o, S_T, y) on the host
-    once the call's stream has completed.
+    staging comes from a cache per device, stream and host thread.  Returns
+    (o, S_T, y) on the host once the call's stream has completed.
     """
     T, H, d = q.shape
     dv = v.shape[2]
@@ -380,10 +381,8 @@ def prefill_from_host(q, k, v, z, beta, A, S0=None, g_in=None, norm_w=None, out=
     need = int(lib.kda_prefill_from_host_staging_size(ctypes.byref(a), int(slab)))
     if need == 0:
         raise ValueError("kda_prefill_from_host: unsupported slab or shape")
-    key = (dev.type, dev.index)
-    st = _STAGING.get(key)
-    if st is None or st.numel() < need:
-        _STAGING[key] = st = torch.empty(need, dtype=torch.uint8, device=dev)
+    with torch.cuda.stream(stream):       # (None: the current one)
+        st = _cached_workspace(dev, need, _STAGING)
     s = stream if stream is not None else torch.cuda.current_stream(dev)
     _check(lib.kda_prefill_from_host(ctypes.byref(a), int(slab), st.data_ptr(), st.numel(), _stream(s)),
            "kda_prefill_from_host")

@@ -52,6 +52,39 @@ def test_captured_calls_keep_away_from_the_cache(fake):
     assert fake.kda._cached_workspace(fake.dev, 100) is a and big.numel() == 1000
 
 
+def test_host_prefill_staging_follows_the_same_rule(fake, monkeypatch):
+    """``prefill_from_host``: calls on two streams, and a stream given in the call, have staging buffers of their own."""
+    kda, used = fake.kda, []
+    monkeypatch.setattr(kda, "_STAGING", {})
+    lib = types.SimpleNamespace(kda_prefill_from_host_staging_size=lambda a, slab: 64,
+                                kda_prefill_from_host=lambda a, slab, at, n, s: used.append(at) or 0)
+    monkeypatch.setattr(kda, "load_library", lambda: lib)
+    monkeypatch.setattr(torch, "device", lambda *a: fake.dev)
+
+    class given:                                           # torch.cuda.stream(s): s is current within
+        def __init__(self, s):
+            self.s = s
+
+        def __enter__(self):
+            self.was, fake.stream = fake.stream, fake.stream if self.s is None else self.s.cuda_stream
+
+        def __exit__(self, *a):
+            fake.stream = self.was
+
+    monkeypatch.setattr(torch.cuda, "stream", given)
+    x = torch.zeros(4, 1, 128, dtype=torch.bfloat16)
+    f = torch.zeros(4, 1, 128)
+    call = lambda **kw: kda.prefill_from_host(x, x, x, f, f, f, out=(x, None, f), slab=64, **kw)     # noqa: E731
+    call()
+    fake.stream = 7
+    call()
+    call(stream=types.SimpleNamespace(cuda_stream=9))
+    fake.stream = 0
+    call()
+    call(stream=types.SimpleNamespace(cuda_stream=9))
+    assert used[0] == used[3] and used[2] == used[4] and len(set(used)) == 3
+
+
 def _call(kda, g, cu, cu_host, **kw):
     return kda.gdn_prefill(**g, cu_seqlens=cu, cu_seqlens_host=cu_host, workspace="cache", **kw)
 
