@@ -381,12 +381,26 @@ def prefill_from_host(q, k, v, z, beta, A, S0=None, g_in=None, norm_w=None, out=
     need = int(lib.kda_prefill_from_host_staging_size(ctypes.byref(a), int(slab)))
     if need == 0:
         raise ValueError("kda_prefill_from_host: unsupported slab or shape")
-    with torch.cuda.stream(stream):       # (None: the current one)
-        st = _cached_workspace(dev, need, _STAGING)
+    st = _temporary(stream, lambda: _cached_workspace(dev, need, _STAGING))
     s = stream if stream is not None else torch.cuda.current_stream(dev)
     _check(lib.kda_prefill_from_host(ctypes.byref(a), int(slab), st.data_ptr(), st.numel(), _stream(s)),
            "kda_prefill_from_host")
     return o_h, S_h, y_h
+
+
+def _temporary(stream, make):
+    """``make()`` with ``stream`` (None: the current one) current: what a call allocates for itself
+    belongs to the stream that uses it, so that its memory is given on behind that use only."""
+    with torch.cuda.stream(stream):
+        return make()
+
+
+def _bounds(cu_seqlens, T, dev, stream):
+    """Sequence bounds on the device (None: one sequence of T tokens) and their host copy."""
+    if cu_seqlens is not None:
+        return cu_seqlens, cu_seqlens.to("cpu")
+    cu_host = torch.tensor([0, T], dtype=torch.int32)
+    return _temporary(stream, lambda: cu_host.to(dev)), cu_host
 
 
 def snapshot_count(cu_seqlens_host, interval: int) -> int:
@@ -408,9 +422,7 @@ def prefill(q, k, v, z, beta, A, cu_seqlens=None, S0=None, g_in=None, norm_w=Non
     T, H, dk = q.shape
     dv = v.shape[2]
     dev = q.device
-    if cu_seqlens is None:
-        cu_seqlens = torch.tensor([0, T], dtype=torch.int32, device=dev)
-    cu_host = cu_seqlens.to("cpu")
+    cu_seqlens, cu_host = _bounds(cu_seqlens, T, dev, stream)
     N = cu_host.numel() - 1
     o = (out["o"] if out else torch.empty((T, H, dv), dtype=q.dtype, device=dev)) if want_o else None
     S_T = (out["S_T"] if out else torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)) \
@@ -435,10 +447,9 @@ def prefill(q, k, v, z, beta, A, cu_seqlens=None, S0=None, g_in=None, norm_w=Non
             # (>= need: chunk-parallel; >= PREFILL_MIN_WORKSPACE: single pass);
             # "cache" reuses one buffer per device, stream and thread, grown on demand
             if isinstance(workspace, str) and workspace == "cache":
-                with torch.cuda.stream(stream):       # (None: the current one)
-                    workspace = _cached_workspace(dev, need)
+                workspace = _temporary(stream, lambda: _cached_workspace(dev, need))
             elif workspace is None:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+                workspace = _temporary(stream, lambda: torch.empty(need, dtype=torch.uint8, device=dev))
             args.workspace = workspace.data_ptr()
             args.workspace_bytes = workspace.numel() * workspace.element_size()
     prefill_raw(args, stream=stream, recurrent=recurrent)
@@ -464,13 +475,11 @@ def prefill_records(q, k, v, z, beta, A, cu_seqlens=None, g_min=-5.0, qk_l2norm=
     """Plan + prep of the chunk-parallel prefill through ``kda_prefill_records``."""
     T, H, dk = q.shape
     dev = q.device
-    if cu_seqlens is None:
-        cu_seqlens = torch.tensor([0, T], dtype=torch.int32, device=dev)
-    cu_host = cu_seqlens.to("cpu")
+    cu_seqlens, cu_host = _bounds(cu_seqlens, T, dev, stream)
     args = make_prefill_args(q, k, v, z, beta, A, cu_seqlens, cu_host, None, g_min=g_min,
                              qk_l2norm=qk_l2norm, gate=gate)
     need = prefill_workspace_size(args)
-    ws = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    ws = _temporary(stream, lambda: torch.empty(max(need, 1), dtype=torch.uint8, device=dev))
     args.workspace, args.workspace_bytes = ws.data_ptr(), ws.numel()
     _check(load_library().kda_prefill_records(ctypes.byref(args), _stream(stream)), "kda_prefill_records")
     return Records(args, (q, k, v, z, beta, A, cu_seqlens, cu_host), ws, (T, H, dk, v.shape[2], cu_host.numel() - 1))
@@ -563,9 +572,7 @@ def short_conv(x, weight, bias=None, cu_seqlens=None, state_in=None, want_state=
     T, C = x.shape
     W = weight.shape[1]
     dev = x.device
-    if cu_seqlens is None:
-        cu_seqlens = torch.tensor([0, T], dtype=torch.int32, device=dev)
-    cu_host = cu_seqlens.to("cpu")
+    cu_seqlens, cu_host = _bounds(cu_seqlens, T, dev, stream)
     N = cu_host.numel() - 1
     y = torch.empty_like(x)
     state_out = torch.empty((N, W - 1, C), dtype=torch.float32, device=dev) if (want_state and W > 1) else None

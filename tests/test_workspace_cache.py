@@ -18,6 +18,18 @@ def fake(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: None)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: types.SimpleNamespace(cuda_stream=now.stream))
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: now.capturing)
+
+    class given:                                           # torch.cuda.stream(s): s is current within
+        def __init__(self, s):
+            self.s = s
+
+        def __enter__(self):
+            self.was, now.stream = now.stream, now.stream if self.s is None else self.s.cuda_stream
+
+        def __exit__(self, *a):
+            now.stream = self.was
+
+    monkeypatch.setattr(torch.cuda, "stream", given)
     return now
 
 
@@ -61,17 +73,6 @@ def test_host_prefill_staging_follows_the_same_rule(fake, monkeypatch):
     monkeypatch.setattr(kda, "load_library", lambda: lib)
     monkeypatch.setattr(torch, "device", lambda *a: fake.dev)
 
-    class given:                                           # torch.cuda.stream(s): s is current within
-        def __init__(self, s):
-            self.s = s
-
-        def __enter__(self):
-            self.was, fake.stream = fake.stream, fake.stream if self.s is None else self.s.cuda_stream
-
-        def __exit__(self, *a):
-            fake.stream = self.was
-
-    monkeypatch.setattr(torch.cuda, "stream", given)
     x = torch.zeros(4, 1, 128, dtype=torch.bfloat16)
     f = torch.zeros(4, 1, 128)
     call = lambda **kw: kda.prefill_from_host(x, x, x, f, f, f, out=(x, None, f), slab=64, **kw)     # noqa: E731
@@ -83,6 +84,32 @@ def test_host_prefill_staging_follows_the_same_rule(fake, monkeypatch):
     call()
     call(stream=types.SimpleNamespace(cuda_stream=9))
     assert used[0] == used[3] and used[2] == used[4] and len(set(used)) == 3
+
+
+@pytest.mark.parametrize("workspace", [None, "cache"])
+def test_temporaries_belong_to_the_stream_that_uses_them(fake, monkeypatch, workspace):
+    """What a call with stream= allocates and drops again (bounds, workspace): on another stream's pool
+    the next call could have it while this one still runs."""
+    kda, made = fake.kda, []
+    empty, to, tensor = torch.empty, torch.Tensor.to, torch.tensor
+
+    def note(kind, x):
+        made.append((kind, x.dtype, fake.stream))
+        return x
+
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: note("empty", empty(*a, **k)))
+    monkeypatch.setattr(torch, "tensor", lambda *a, **k: note("device" if "device" in k else "host", tensor(*a, **k)))
+    monkeypatch.setattr(torch.Tensor, "to", lambda x, *a, **k: note("host" if a == ("cpu",) else "device", to(x, *a, **k)))
+    monkeypatch.setattr(kda, "load_library", lambda: types.SimpleNamespace(
+        kda_prefill_records=lambda *a: 0, kda_short_conv=lambda *a: 0, kda_prefill=lambda *a: 0,
+        kda_prefill_workspace_size=lambda a: 64))
+    x, f = torch.zeros(4, 1, 128, dtype=torch.bfloat16), torch.zeros(4, 1, 128)
+    s = types.SimpleNamespace(cuda_stream=9)
+    kda.prefill(x, x, x, f, f, f, workspace=workspace, stream=s)
+    kda.prefill_records(x, x, x, f, f, f, stream=s)
+    kda.short_conv(f[:, 0], f[:, 0], stream=s)
+    temporary = [m for m in made if m[1] == torch.uint8 or (m[0] == "device" and m[1] == torch.int32)]
+    assert len(temporary) == 5 and all(m[2] == 9 for m in temporary), made
 
 
 def _call(kda, g, cu, cu_host, **kw):
@@ -177,3 +204,23 @@ def test_prefill_of_the_channel_gated_rule(kda_lib, cuda_dev):
     with torch.cuda.stream(streams[1]):
         assert kda.device_error(kda.cached_workspace(cuda_dev)) == kda.KDA_OK
     kda.release_workspace_cache()
+
+
+@pytest.mark.gpu
+def test_streams_given_with_no_bounds_and_no_workspace(kda_lib, cuda_dev):
+    """Calls on two streams in turn, each with its own length: bounds and workspaces that the call makes itself."""
+    import serving_kda_chunked_gated_gb300.kda as kda
+    g = torch.Generator().manual_seed(3)
+    sets = []
+    for T in (300, 1700, 64):
+        r = lambda *s: torch.randn(*s, generator=g)        # noqa: E731
+        q, k, v = (r(T, 4, 128).to(torch.bfloat16) for _ in range(3))
+        sets.append([x.to(cuda_dev) for x in (q, k, v, r(T, 4, 128), torch.sigmoid(r(T, 4)), torch.zeros(4), r(512, 4))])
+    conv = lambda x, **kw: kda.short_conv(x[0].flatten(1), x[6], **kw)       # noqa: E731
+    alone = [[*kda.prefill(*x[:6])[:2], *conv(x)] for x in sets]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[[*kda.prefill(*x[:6], stream=s)[:2], *conv(x, stream=s)] for x, s in zip(sets, streams)] for _ in range(6)]
+    torch.cuda.synchronize()
+    for r in got:
+        assert all(torch.equal(a, b) for have, want in zip(r, alone) for a, b in zip(have, want))
