@@ -557,6 +557,11 @@ kda_status kda_qk_norm_rope(const kda_qk_norm_rope_args* args, void* stream);
  * min(sinks, len) and its last `window` positions, into slot slots[n] (or n; distinct).
  * Other rows keep what they held.  A slot outside [0, num_slots) is skipped.
  * The caches must not overlap any other argument.
+ *
+ * error: a device word (int32, zero before its first call) that takes this call's error
+ * report, or NULL: the library's word on this device, which all such calls share.  It
+ * stays set until kda_get_last_device_error(error, stream) reads it; callers that give
+ * each stream a word of its own learn whose wait gave up.
  */
 typedef struct {
     int num_seqs;
@@ -579,6 +584,7 @@ typedef struct {
     void* v_cache;
     const int32_t* slots;
     int num_slots, cache_rows;
+    int32_t* error;
 } kda_window_prefill_args;
 
 kda_status kda_window_prefill(const kda_window_prefill_args* args, void* stream);
@@ -623,13 +629,17 @@ kda_status kda_window_decode(const kda_window_decode_args* args, void* stream);
  *
  * kda_get_last_device_error waits for the work queued on `stream`, then reads
  * and clears the error word of `workspace` (the workspace the prefill calls
- * used), or, with workspace == NULL, those of the fixed array kda_prefill_noalloc
- * uses on the current device and of kda_window_prefill (which needs no workspace;
- * its word stays set until it is read).  Returns KDA_OK when no wait gave up,
+ * used, or the word given to kda_window_prefill), or, with workspace == NULL,
+ * those of the fixed array kda_prefill_noalloc uses on the current device and of the
+ * kda_window_prefill calls without a word of their own (it stays set until it is
+ * read).  Returns KDA_OK when no wait gave up,
  * KDA_ERR_TIMEOUT when one did, KDA_ERR_CUDA when the read failed.  It
  * allocates nothing.  Call it on the stream of the prefill calls (or after
- * synchronising them); calls on other streams that use the same workspace
- * must not run concurrently.
+ * synchronising them); calls on other streams that use the same workspace or
+ * word must not run concurrently.  Window prefills on the shared word may: it is
+ * read and cleared in one atomic step, so a report that comes up meanwhile is in
+ * this answer or in the next, and in one only (that of whichever caller reads
+ * first).
  */
 kda_status kda_get_last_device_error(void* workspace, void* stream);
 

@@ -5,6 +5,7 @@
 #include <string.h>
 
 #include <atomic>
+#include <mutex>
 
 #include "kda_common.cuh"
 #include "tcgen05.cuh"
@@ -58,6 +59,26 @@ static kda_status cuda_fail(cudaError_t e) {
 
 static bool misaligned(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u); }
 
+// Reads and clears the window prefills' shared word in one step: a kernel on another stream may set
+// a bit at any time, and between a copy and a memset it would be lost.  The bits go to the host through
+// one place on each device, which one caller at a time uses, on a stream of its own.
+static __device__ int g_taken;
+static std::mutex g_taken_lock;
+static __global__ void take_kernel(int* word) { g_taken = atomicExch(word, 0); }
+
+static cudaError_t take_window_error(int32_t* bits) {
+    void *word = nullptr, *taken = nullptr;
+    cudaError_t e = kda::win::error_word(&word);
+    if (e == cudaSuccess) e = cudaGetSymbolAddress(&taken, g_taken);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> one(g_taken_lock);
+    take_kernel<<<1, 1, 0, cudaStreamPerThread>>>(static_cast<int*>(word));
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = cudaMemcpyAsync(bits, taken, sizeof(*bits), cudaMemcpyDeviceToHost, cudaStreamPerThread);
+    const cudaError_t done = cudaStreamSynchronize(cudaStreamPerThread);
+    return e != cudaSuccess ? e : done;
+}
+
 extern "C" {
 
 const char* kda_status_str(kda_status s) {
@@ -84,19 +105,13 @@ kda_status kda_get_last_device_error(void* workspace, void* stream) {
     cudaError_t e = cudaSuccess;
     if (!word && (e = kda::noalloc_scratch_address(&word)) != cudaSuccess) return cuda_fail(e);
     if (misaligned(word)) return KDA_ERR_ALIGN;
-    int32_t h = 0;
+    int32_t h = 0, w = 0;
     if ((e = cudaMemcpyAsync(&h, word, sizeof(h), cudaMemcpyDeviceToHost, s)) != cudaSuccess) return cuda_fail(e);
     if ((e = cudaMemsetAsync(word, 0, sizeof(h), s)) != cudaSuccess) return cuda_fail(e);
-    int32_t w = 0;
-    void* window = nullptr;
-    if (!workspace) {   // the window prefill has no workspace: its word is the library's too
-        if ((e = kda::win::error_word(&window)) != cudaSuccess) return cuda_fail(e);
-        if ((e = cudaMemcpyAsync(&w, window, sizeof(w), cudaMemcpyDeviceToHost, s)) != cudaSuccess) return cuda_fail(e);
-        if ((e = cudaMemsetAsync(window, 0, sizeof(w), s)) != cudaSuccess) return cuda_fail(e);
-    }
     if ((e = cudaStreamSynchronize(s)) != cudaSuccess) return cuda_fail(e);
-    h |= w;
-    return h ? KDA_ERR_TIMEOUT : KDA_OK;
+    // the window prefill has no workspace: its word is the library's too
+    if (!workspace && (e = take_window_error(&w)) != cudaSuccess) return cuda_fail(e);
+    return (h | w) ? KDA_ERR_TIMEOUT : KDA_OK;
 }
 
 uint32_t kda_debug_set_wait_limit(uint32_t polls) { return g_wait_limit.exchange(polls); }

@@ -166,7 +166,7 @@ kda_status kda_window_prefill(const kda_window_prefill_args* a, void* stream) {
     if (a->Tk_total > 0 && (!a->k || !a->v)) return KDA_ERR_NULL;
     if (!a->k_cache != !a->v_cache) return KDA_ERR_NULL;
     if (any_misaligned({a->cu_seqlens, a->cu_seqlens_k, a->q, a->k, a->v, (const void*)a->o, (const void*)a->lse,
-                        (const void*)a->k_cache, (const void*)a->v_cache, (const void*)a->slots}))
+                        (const void*)a->k_cache, (const void*)a->v_cache, (const void*)a->slots, (const void*)a->error}))
         return KDA_ERR_ALIGN;
     const int32_t *cq = a->cu_seqlens_host, *ck = a->cu_seqlens_k_host;
     if (!seqlens_ok(cq, a->num_seqs, a->T_total) || !seqlens_ok(ck, a->num_seqs, a->Tk_total)) return KDA_ERR_SEQLENS;

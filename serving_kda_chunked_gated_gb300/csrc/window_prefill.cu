@@ -65,7 +65,7 @@ struct PF {
     static constexpr int P0 = EARLY ? 384 : 0, PSTEP = EARLY ? 64 : 128;
 };
 
-__device__ int g_window_error;              // ERR_ bits of calls whose bounded waits gave up (sticky until read)
+__device__ int g_window_error;              // ERR_ bits of calls without a word of their own (sticky until read)
 
 struct PfParams {
     kda_window_prefill_args a;
@@ -76,6 +76,7 @@ struct PfParams {
     int neg;                                // scale < 0: S = -Q K^T
     int wide;                               // o is 32-byte aligned
     uint32_t wait_limit;
+    KDA_DEV int* error() const { return a.error ? a.error : &g_window_error; }
 };
 
 // One unit's geometry, from its index; called by whole warps.
@@ -335,7 +336,7 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
                     tc::mbar_arrive(&full[whole % ROUNDS]);
                     d = tc::mbar_wait_bounded(&full[whole % ROUNDS], (whole / ROUNDS) & 1, tc::WAIT_POLLS) && d;
                 }
-                atomicOr(&g_window_error, d ? tc::ERR_WAIT : tc::ERR_WAIT | tc::ERR_DRAIN);
+                atomicOr(p.error(), d ? tc::ERR_WAIT : tc::ERR_WAIT | tc::ERR_DRAIN);
             }
         } else if (warp < 15) {
             // ---------------- MMAs of tile t: the warp computes together, one lane issues ----------------
@@ -465,7 +466,7 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
             tc::mma_commit_elect(&drained);
             if (lane == 0) {
                 const bool d = tc::mbar_wait_bounded(&drained, 0, tc::WAIT_POLLS);
-                if (!ok || !d) atomicOr(&g_window_error, d ? tc::ERR_WAIT : tc::ERR_WAIT | tc::ERR_DRAIN);
+                if (!ok || !d) atomicOr(p.error(), d ? tc::ERR_WAIT : tc::ERR_WAIT | tc::ERR_DRAIN);
             }
             __syncwarp();
         }

@@ -130,6 +130,7 @@ class WindowPrefillArgs(ctypes.Structure):
         ("q_stride", ctypes.c_long), ("k_stride", ctypes.c_long), ("v_stride", ctypes.c_long),
         ("scale", ctypes.c_float), ("o", _vp), ("lse", _vp),
         ("k_cache", _vp), ("v_cache", _vp), ("slots", _vp), ("num_slots", ctypes.c_int), ("cache_rows", ctypes.c_int),
+        ("error", _vp),
     ]
 
 
@@ -216,8 +217,9 @@ def launch_count() -> int:
 
 def device_error(workspace=None, stream=None) -> int:
     """``kda_get_last_device_error``: waits for ``stream``, then reads and clears
-    the error word of ``workspace`` (a prefill workspace tensor), or of the
-    array ``kda_prefill_noalloc`` uses when ``workspace`` is None.  Returns
+    the error word of ``workspace`` (a prefill workspace tensor, or the ``error`` of
+    ``window_prefill``), or, when ``workspace`` is None, of the array
+    ``kda_prefill_noalloc`` uses and of window prefills without one.  Returns
     KDA_OK (0) or KDA_ERR_TIMEOUT (9); raises on any other status."""
     st = load_library().kda_get_last_device_error(_p(workspace), _stream(stream))
     if st not in (KDA_OK, KDA_ERR_TIMEOUT):
@@ -824,7 +826,8 @@ def _caches(k_cache, v_cache, Hkv, d, dev):
 
 @_on_stream
 def window_prefill(q, k, v, window, sinks=0, cu_seqlens=None, cu_seqlens_host=None, cu_seqlens_k=None,
-                   cu_seqlens_k_host=None, scale=None, want_lse=False, k_cache=None, v_cache=None, slots=None, out=None):
+                   cu_seqlens_k_host=None, scale=None, want_lse=False, k_cache=None, v_cache=None, slots=None, out=None,
+                   error=None):
     """Causal attention through a sliding window with sinks over packed sequences,
     through ``kda_window_prefill``.
 
@@ -834,7 +837,9 @@ def window_prefill(q, k, v, window, sinks=0, cu_seqlens=None, cu_seqlens_host=No
     queries, cu_seqlens_k the keys (None: the same bounds; a sequence's queries are
     the last of its keys).  scale: d ** -0.5 by default.  k_cache, v_cache
     [num_slots, rows >= sinks + window, Hkv, d] bf16 receive the rows that
-    ``window_decode`` goes on from, in slot slots[n] (or n).
+    ``window_decode`` goes on from, in slot slots[n] (or n).  error: an int32 tensor of one
+    zero that takes the call's error report, for ``device_error(error)``, apart from the other
+    callers' (None: the word that ``device_error(None)`` reads).
     Returns o, or (o, lse [T, Hq] f32) with want_lse.
     """
     dev = _cuda_device(q, "q")
@@ -861,7 +866,7 @@ def window_prefill(q, k, v, window, sinks=0, cu_seqlens=None, cu_seqlens_host=No
         N, T, Tk, Hq, Hkv, d, window, sinks, KDA_BF16, cu.data_ptr(), cu_host.data_ptr(), cuk.data_ptr(),
         cuk_host.data_ptr(), qp, kp, vp, qs, ks, vs, d ** -0.5 if scale is None else scale,
         _dense("out", o, (T, Hq, d), bf, dev), lse.data_ptr() if want_lse else None, kc, vc,
-        _dense("slots", slots, (N,), torch.int32, dev), num_slots, rows)
+        _dense("slots", slots, (N,), torch.int32, dev), num_slots, rows, _dense("error", error, (1,), torch.int32, dev))
     _launch("kda_window_prefill", a, dev)
     return (o, lse) if want_lse else o
 

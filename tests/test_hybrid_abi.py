@@ -185,3 +185,11 @@ def test_binding_refuses_what_the_kernels_cannot_read():
         kda._cu_pair(torch.zeros(3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), 0, dev)
     with pytest.raises(kda.KDAError, match="given together"):
         kda._caches(x, None, 2, 128, dev)
+
+
+def test_window_prefill_error_word(kda_lib):
+    """A caller's own error word: checked like every pointer."""
+    kda = _kda()
+    cu = np.array([0, 3, 8], dtype=np.int32)
+    assert kda_lib.kda_window_prefill(ctypes.byref(_window(cu, cu, error=FAKE + 4)), None) == ALIGN
+    assert ("error", ctypes.c_void_p) in kda.WindowPrefillArgs._fields_
