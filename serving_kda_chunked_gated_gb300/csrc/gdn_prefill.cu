@@ -307,19 +307,20 @@ gdn_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
     float* X = reinterpret_cast<float*>(sm + P_X);        // the tiles have been consumed
     uint8_t* img = sm + P_Y;                              // the masked Q K^T on its way out, then Y
     float* W = reinterpret_cast<float*>(sm + P_W);        // W[b][j] = rk_j e^{g_(16 b - 1) - g_j}, j < 16 b
-    constexpr float FIX = 4294967296.f, UNFIX = 1.f / 4294967296.f;
+    constexpr float FIX = 1099511627776.f, UNFIX = 1.f / 1099511627776.f;      // 2^40
     for (int e = 0; ok && e < rep; ++e) {
         const int h = hk * rep + e;
         uint8_t* rec = recs + e * (size_t)REC;
-        // sums of the log-decays (base 2), exact in 2^-32 fixed point.  A step below -4096 is
-        // an exponential of 0 in any sum; a NaN travels with beta.
+        // sums of the log-decays (base 2) in fixed point: a step is rounded to 2^-41 (to nearest: a
+        // cut would make every state last longer), the sums are exact, below 2^59.  A step below
+        // -4096 is an exponential of 0 in any sum; a NaN travels with beta.
         if (quarter == 0) {
             long long g = 0;
             float beta = 0.f;
             if (live) {
                 const float x = log_decay_mode(zn, __expf(__ldg(a.A + h)), a.g_min, a.gate_mode) * 1.4426950408889634f;
                 beta = x == x ? bn : x;
-                g = (long long)(fminf(fmaxf(x, -4096.f), 4096.f) * FIX);
+                g = __float2ll_rn(fminf(fmaxf(x, -4096.f), 4096.f) * FIX);
             }
             if (e + 1 < rep) fetch(e + 1);
 #pragma unroll
@@ -346,7 +347,12 @@ gdn_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
                 f = make_float4(beta, beta * eg * s_rk[row], exp2f((float)(gC - gi) * UNFIX) * s_rk[row],
                                 eg * s_rq[row] * a.scale);
             *reinterpret_cast<float4*>(rec + REC_F + row * 16) = f;
-            if (row == 0) *reinterpret_cast<float2*>(rec + REC_F + C * 16) = make_float2(exp2f((float)gC * UNFIX), 0.f);
+            if (row == 0) {
+                // The state is multiplied by e^{g_C} once a chunk.  exp2f is low by 0.5 to 2e-8 on average
+                // just below 0, which a state that hardly decays would add up; 1 + expm1 rounds without a bias.
+                const float x = (float)gC * UNFIX, t = x * 0.6931471805599453f;
+                *reinterpret_cast<float2*>(rec + REC_F + C * 16) = make_float2(t > -0.25f ? 1.0f + expm1f(t) : exp2f(x), 0.f);
+            }
         }
         if (tid == 0) tc::bulk_wait_read();       // the last head's image has left
         __syncthreads();

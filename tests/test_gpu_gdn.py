@@ -240,3 +240,29 @@ def test_prefill_short_sequences_beside_long_ones(kda_lib, cuda_dev, gate):
         graph.replay()
         _check(out["o"], S, ro, rS, lens)
     assert kda.device_error(ws) == kda.KDA_OK
+
+
+@pytest.mark.parametrize("near_whole", [False, True])
+def test_prefill_slow_decay_over_half_a_million_tokens(kda_lib, cuda_dev, near_whole):
+    """Without writes (beta 0) the state is S0 times the product of all decays, and a bias of any step shows:
+    steps of some 1e-6, 4096 chunks.  near_whole: steps just below a multiple of 2^-32 (base 2).
+
+    Tolerance: a chunk's factor is rounded by 2^-25 and the state's update by 2^-24 at most, uniformly
+    distributed and independent over 4096 chunks: 64 sqrt(1 / 3) (2^-24 + 2^-25) = 3.3e-6; the gate's
+    float32 log-decay is within 2^-19 (its exponential's 2 + |1.2 z| units in the last place), of a total
+    of 0.6: 1.2e-6.  Together below TOL_S."""
+    import serving_kda_chunked_gated_gb300.kda as kda
+    T = 1 << 19
+    g = torch.Generator().manual_seed(23)
+    z = -18 + 6 * torch.rand(2 * T if not near_whole else 12 * T, generator=g)
+    if near_whole:
+        step = torch.log1p(z.double().exp()) / torch.log(torch.tensor(2.0, dtype=torch.float64)) * 2.0 ** 32
+        z = z[step - step.floor() > 0.8]
+    z = z[:T]
+    assert len(z) == T
+    S0 = torch.randn(1, 1, 128, 128, generator=g)
+    x = torch.randn(T, 1, 128, generator=g).to(torch.bfloat16).to(cuda_dev)
+    zero = torch.zeros(T, 1, device=cuda_dev)
+    _, S = kda.gdn_prefill(x, x, x, z[:, None].to(cuda_dev), zero, torch.zeros(1, device=cuda_dev), S0=S0.to(cuda_dev))
+    want = S0.double() * torch.exp(-torch.log1p(z.double().exp()).sum())
+    assert rel(S, want) < TOL_S, rel(S, want)
