@@ -76,7 +76,6 @@ struct PfParams {
     int neg;                                // scale < 0: S = -Q K^T
     int wide;                               // o is 32-byte aligned
     uint32_t wait_limit;
-    KDA_DEV int* error() const { return a.error ? a.error : &g_window_error; }
 };
 
 // One unit's geometry, from its index; called by whole warps.
@@ -336,7 +335,7 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
                     tc::mbar_arrive(&full[whole % ROUNDS]);
                     d = tc::mbar_wait_bounded(&full[whole % ROUNDS], (whole / ROUNDS) & 1, tc::WAIT_POLLS) && d;
                 }
-                atomicOr(p.error(), d ? tc::ERR_WAIT : tc::ERR_WAIT | tc::ERR_DRAIN);
+                atomicOr(p.a.error, d ? tc::ERR_WAIT : tc::ERR_WAIT | tc::ERR_DRAIN);
             }
         } else if (warp < 15) {
             // ---------------- MMAs of tile t: the warp computes together, one lane issues ----------------
@@ -466,7 +465,7 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
             tc::mma_commit_elect(&drained);
             if (lane == 0) {
                 const bool d = tc::mbar_wait_bounded(&drained, 0, tc::WAIT_POLLS);
-                if (!ok || !d) atomicOr(p.error(), d ? tc::ERR_WAIT : tc::ERR_WAIT | tc::ERR_DRAIN);
+                if (!ok || !d) atomicOr(p.a.error, d ? tc::ERR_WAIT : tc::ERR_WAIT | tc::ERR_DRAIN);
             }
             __syncwarp();
         }
@@ -675,6 +674,8 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
     if (warp == 13) tc::tmem_dealloc(tm, 512);
 }
 
+cudaError_t error_word(void** out) { return cudaGetSymbolAddress(out, g_window_error); }
+
 template <int D>
 static cudaError_t prefill_d(const kda_window_prefill_args& a, cudaStream_t s) {
     PfParams p;
@@ -701,6 +702,8 @@ static cudaError_t prefill_d(const kda_window_prefill_args& a, cudaStream_t s) {
     if (e == cudaSuccess) e = make_map_heads(&mv, a.v, D, a.Hkv, a.Tk_total, a.v_stride, 1, KT);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(window_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, PF<D>::SMEM);
+    void* shared = nullptr;
+    if (e == cudaSuccess && !a.error && (e = error_word(&shared)) == cudaSuccess) p.a.error = static_cast<int32_t*>(shared);
     int dev = 0, sms = 0;
     if (e == cudaSuccess) e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -714,8 +717,6 @@ static cudaError_t prefill_d(const kda_window_prefill_args& a, cudaStream_t s) {
 cudaError_t launch_prefill(const kda_window_prefill_args& a, cudaStream_t s) {
     return a.d == 64 ? prefill_d<64>(a, s) : prefill_d<128>(a, s);
 }
-
-cudaError_t error_word(void** out) { return cudaGetSymbolAddress(out, g_window_error); }
 
 }  // namespace win
 }  // namespace kda
