@@ -9,7 +9,7 @@
 // keeps STAGES tiles in flight.  Warps are merged through shared memory, CTAs that
 // share a (sequence, key head) through distributed shared memory of their cluster:
 // no workspace and no second launch.  256 sequences x 8 key heads of 128, window
-// 4096: 4.1 GB in 560 us, 7.3 TB/s (reads alone run above a copy's rate).
+// 4096: 4.1 GB in 577 us, 7.1 TB/s (reads alone run above a copy's rate).
 #include "kda_common.cuh"
 #include "tcgen05.cuh"
 
@@ -45,6 +45,11 @@ KDA_DEV void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
 KDA_DEV uint32_t pack2(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
+}
+// x = hi + lo, both bf16: pairs packed with the lower index in the low half
+KDA_DEV void split2(float x0, float x1, uint32_t* hi, uint32_t* lo) {
+    *hi = pack2(x0, x1);
+    *lo = pack2(x0 - __uint_as_float(*hi << 16), x1 - __uint_as_float(*hi & 0xffff0000u));
 }
 KDA_DEV uint32_t cluster_rank() { uint32_t r; asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r)); return r; }
 KDA_DEV uint32_t cluster_size() { uint32_t r; asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r)); return r; }
@@ -205,8 +210,16 @@ window_decode_kernel(kda_window_decode_args a, int mtiles) {
             l0 += s[j][0] + s[j][1];
             l1 += s[j][2] + s[j][3];
         }
-        // weights in [0, 1] rounded to bf16 for the product; their sum keeps float32
-        const uint32_t p[4] = {pack2(s[0][0], s[0][1]), pack2(s[0][2], s[0][3]), pack2(s[1][0], s[1][1]), pack2(s[1][2], s[1][3])};
+        // Weights in [0, 1] as two bf16 parts (2^-17 left): o is then off by its own rounding alone, 1.7e-3,
+        // rather than 2.1e-3 with one part.  256 sequences, window 4096, us with one part and two: 32/8 heads
+        // of 128 586, 589; of 64 307, 316; window 512, 16/8 of 128: 88, 90; 64 sequences, 32 query heads to
+        // a key head (arithmetic counts there): 60, 68.
+        uint32_t p[4], pl[4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            split2(s[j][0], s[j][1], &p[2 * j], &pl[2 * j]);
+            split2(s[j][2], s[j][3], &p[2 * j + 1], &pl[2 * j + 1]);
+        }
         const int vrow = (lane & 7) + (((lane >> 3) & 1) << 3), vch = lane >> 4;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
@@ -214,6 +227,8 @@ window_decode_kernel(kda_window_decode_args a, int mtiles) {
             ldsm4t(b, vb + vrow * (D * 2) + (((2 * k + vch) ^ (vrow & 7)) << 4));
             mma16816(o[2 * k], p, b[0], b[1]);
             mma16816(o[2 * k + 1], p, b[2], b[3]);
+            mma16816(o[2 * k], pl, b[0], b[1]);
+            mma16816(o[2 * k + 1], pl, b[2], b[3]);
         }
         if (++stage == DEC_STAGES) stage = 0;
         __syncwarp();          // the tile is read before its stage is filled again

@@ -263,3 +263,21 @@ def test_first_calls_captured(kda_lib, cuda_dev):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("N,Hq,Hkv,d,W", [(3, 4, 2, 128, 400), (40, 24, 4, 64, 900), (200, 8, 8, 128, 300), (400, 16, 1, 64, 200)])
+def test_decode_rounds_once(kda_lib, cuda_dev, N, Hq, Hkv, d, W):
+    """The weights keep 16 bits: what is left against 64 bits is the output's own rounding (2^-8 of it at
+    most), 2^-17 of every weight in two bf16 parts, and 2^-17 of it from its score (below 8 in size, at most
+    eight float32 steps of 2^-23 each)."""
+    import serving_kda_chunked_gated_gb300.kda as kda
+    g = torch.Generator(device=cuda_dev).manual_seed(N)
+    r = lambda *s: torch.randn(*s, generator=g, device=cuda_dev).to(torch.bfloat16)      # noqa: E731
+    q, k, v, kc, vc = r(N, Hq, d), r(N, Hkv, d), r(N, Hkv, d), r(N, W, Hkv, d), r(N, W, Hkv, d)
+    pos = torch.full((N,), 5 * W + 3, dtype=torch.int32, device=cuda_dev)
+    o = kda.window_decode(q, k, v, kc, vc, pos, W)
+    K, V = (x.double().transpose(1, 2) for x in (kc, vc))                                # rows in any order: all are seen
+    w = torch.softmax(q.double().unflatten(1, (Hkv, Hq // Hkv)) @ K.transpose(-1, -2) * d ** -0.5, -1)
+    want, size = (w @ V).flatten(1, 2), (w @ V.abs()).flatten(1, 2)
+    bound = 2.0 ** -8 * want.abs() + 2.0 ** -16 * size + 1e-30
+    assert ((o.double() - want).abs() <= bound).all(), ((o.double() - want).abs() / bound).max()
