@@ -432,9 +432,13 @@ kda_status kda_kcp_apply(const float* M, float* X, const float* add, int H, int 
  * KDA_ERR_WORKSPACE.  Its first 4 bytes are the call's error word, read with
  * kda_get_last_device_error.  Every product that reaches a final state splits its
  * float32 operand into two bf16 parts: states are within some 4e-6 of exact ones
- * (relative L2), o within bf16 roundings of its weights, values and itself.
+ * (relative L2; what S0 left in them takes a float32 rounding, 2^-24 at most, at every
+ * chunk, so half a million tokens of slow decay add about 3e-6), o within bf16 roundings
+ * of its weights (the masked Q K^T), of the values it weighs and of itself, 2.8e-3 in all.
  * float32: the per-token recurrence on CUDA cores, no workspace.
- * kda_gdn_prefill_recurrent: the per-token recurrence for either type.
+ * kda_gdn_prefill_recurrent: the per-token recurrence for either type.  It rounds the
+ * state to float32 at every token, as the step does: over tens of thousands of tokens
+ * that decay by less than 1e-6 each the roundings add up (1.4e-4 over 32768).
  * Rows of o outside every sequence do not exist (cu_seqlens ends at T_total);
  * non-finite values of one sequence never reach another (within one, they may reach
  * earlier tokens of their 128-token chunk in kda_gdn_prefill).
@@ -548,6 +552,9 @@ kda_status kda_qk_norm_rope(const kda_qk_norm_rope_args* args, void* stream);
  * no query sees are never used, whatever they hold.  A non-finite value that some
  * query of a sequence sees may also reach outputs of queries near it that do not (a
  * weight of 0 times it); other sequences it never reaches.
+ * Scores, maxima and sums are float32; the weights are rounded to bf16 (2^-8 of each
+ * at most) for their product with v and o to bf16 at the end, 2.3e-3 relative in all
+ * where o's own rounding is 1.7e-3.
  *
  * Caches (optional, k_cache and v_cache together): [num_slots, cache_rows, Hkv, d]
  * bf16, cache_rows >= sinks + window.  Position p of a sequence lives in row
@@ -596,6 +603,7 @@ kda_status kda_window_prefill(const kda_window_prefill_args* args, void* stream)
  *   positions [N] int32: the position of the new token (= tokens before it);
  *   caches as above, the rows of earlier visible positions already written;
  *   slots [N] int32 or NULL (row n), distinct.
+ * Weights keep 16 bits or more: o is off by little but its own rounding to bf16.
  * A sequence whose slot lies outside [0, num_slots), or whose position is
  * negative, is skipped: its o row and the caches are left as they were.
  */

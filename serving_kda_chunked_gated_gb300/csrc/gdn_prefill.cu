@@ -12,8 +12,9 @@
 // and Q are MMA operands as they come from memory, bf16 without a rounding: only S, T, R
 // and V'' are float32, and each is fed as two bf16 parts (x = hi + lo, 2^-17 left): states
 // come out within 4e-6 of exact ones, relative (a third part would need more shared memory than
-// there is).  Exponents are differences of exact sums (64-bit fixed point): a decay of e^-600
-// over the chunk costs the short ones nothing.  Only the product behind o alone, masked Q K^T
+// there is); its float32 update adds up to 2^-24 a chunk, which shows where thousands of chunks
+// decay slowly.  Exponents are differences of exact sums (64-bit fixed point) of steps rounded to
+// 2^-41: a decay of e^-600 over the chunk costs the short ones nothing.  Only the product behind o alone, masked Q K^T
 // times V', has both operands rounded to bf16, as attention weights and values are: o is then
 // within 2.8e-3, of which its own rounding is 1.7e-3.  V' in two parts brings 2.2e-3 and
 // costs 14 % (4.30 -> 4.90 ms): that product delays the next K S.
