@@ -655,6 +655,13 @@ def _heads(name, t, shape, dtype, dev):
     return t.data_ptr(), (st[0] if n > 1 else h * d)
 
 
+def _int32(name, x):
+    """``x``, once it fits the entry point's int: ctypes would keep its low 32 bits."""
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise KDAError(f"{name} must fit 32 bits, got {x}")
+    return x
+
+
 def _launch(name, args, dev):
     """The entry point ``name`` on the current stream of the tensors' device."""
     fn = getattr(_lib or load_library(), name)
@@ -805,7 +812,7 @@ def qk_norm_rope(q, k, cos, sin, positions, q_weight=None, k_weight=None, eps=1e
     qp, qs = _heads("q", q, (T, Hq, d), dt, dev)
     kp, ks = _heads("k", k, (T, Hkv, d), dt, dev)
     a = QkNormRopeArgs(
-        T, Hq, Hkv, d, 2 * half, cos.shape[0], _dtype_code(q), qp, kp, qs, ks,
+        T, Hq, Hkv, d, 2 * half, _int32("the number of positions", cos.shape[0]), _dtype_code(q), qp, kp, qs, ks,
         _dense("q_weight", q_weight, (d,), f32, dev), _dense("k_weight", k_weight, (d,), f32, dev), eps,
         _dense("cos", cos, (cos.shape[0], half), f32, dev), _dense("sin", sin, (cos.shape[0], half), f32, dev),
         _dense("positions", positions, (T,), torch.int32, dev), 1 if interleaved else 0,
@@ -863,8 +870,8 @@ def window_prefill(q, k, v, window, sinks=0, cu_seqlens=None, cu_seqlens_host=No
     vp, vs = _heads("v", v, (Tk, Hkv, d), bf, dev)
     kc, vc, num_slots, rows = _caches(k_cache, v_cache, Hkv, d, dev)
     a = WindowPrefillArgs(
-        N, T, Tk, Hq, Hkv, d, window, sinks, KDA_BF16, cu.data_ptr(), cu_host.data_ptr(), cuk.data_ptr(),
-        cuk_host.data_ptr(), qp, kp, vp, qs, ks, vs, d ** -0.5 if scale is None else scale,
+        N, T, Tk, Hq, Hkv, d, _int32("window", window), _int32("sinks", sinks), KDA_BF16, cu.data_ptr(),
+        cu_host.data_ptr(), cuk.data_ptr(), cuk_host.data_ptr(), qp, kp, vp, qs, ks, vs, d ** -0.5 if scale is None else scale,
         _dense("out", o, (T, Hq, d), bf, dev), lse.data_ptr() if want_lse else None, kc, vc,
         _dense("slots", slots, (N,), torch.int32, dev), num_slots, rows, _dense("error", error, (1,), torch.int32, dev))
     _launch("kda_window_prefill", a, dev)
@@ -887,7 +894,8 @@ def window_decode(q, k, v, k_cache, v_cache, positions, window, sinks=0, slots=N
     vp, vs = _heads("v", v, (N, Hkv, d), bf, dev)
     kc, vc, num_slots, rows = _caches(k_cache, v_cache, Hkv, d, dev)
     a = WindowDecodeArgs(
-        N, Hq, Hkv, d, window, sinks, KDA_BF16, qp, kp, vp, qs, ks, vs, d ** -0.5 if scale is None else scale, kc, vc,
+        N, Hq, Hkv, d, _int32("window", window), _int32("sinks", sinks), KDA_BF16, qp, kp, vp, qs, ks, vs,
+        d ** -0.5 if scale is None else scale, kc, vc,
         _dense("positions", positions, (N,), torch.int32, dev), _dense("slots", slots, (N,), torch.int32, dev),
         num_slots, rows, _dense("out", o, (N, Hq, d), bf, dev))
     _launch("kda_window_decode", a, dev)

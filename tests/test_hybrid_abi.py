@@ -193,3 +193,25 @@ def test_window_prefill_error_word(kda_lib):
     cu = np.array([0, 3, 8], dtype=np.int32)
     assert kda_lib.kda_window_prefill(ctypes.byref(_window(cu, cu, error=FAKE + 4)), None) == ALIGN
     assert ("error", ctypes.c_void_p) in kda.WindowPrefillArgs._fields_
+
+
+def test_sizes_past_32_bits_are_refused():
+    """A window of 2^32 + 8 is not a window of 8, nor a table of 2^32 + 5 positions one of 5 (meta tensors
+    stand for the GPU's: the binding stops before it looks at their memory)."""
+    kda = _kda()
+
+    class Cuda(torch.Tensor):
+        is_cuda = True
+
+    x = lambda *s, d=torch.bfloat16: torch.empty(*s, dtype=d, device="meta").as_subclass(Cuda)       # noqa: E731
+    cu = torch.tensor([0, 4], dtype=torch.int32)
+    cud = x(2, d=torch.int32)
+    for big in (2 ** 32 + 8, 2 ** 31, -2 ** 32 + 8):
+        for kw in (dict(window=big), dict(window=8, sinks=big)):
+            with pytest.raises(kda.KDAError, match="32 bits"):
+                kda.window_prefill(x(4, 2, 64), x(4, 1, 64), x(4, 1, 64), cu_seqlens=cud, cu_seqlens_host=cu, **kw)
+            with pytest.raises(kda.KDAError, match="32 bits"):
+                kda.window_decode(x(4, 2, 64), x(4, 1, 64), x(4, 1, 64), x(4, 9, 1, 64), x(4, 9, 1, 64), x(4, d=torch.int32), **kw)
+    table = torch.empty(1, 8, device="meta").expand(2 ** 32 + 5, 8).as_subclass(Cuda)
+    with pytest.raises(kda.KDAError, match="32 bits"):
+        kda.qk_norm_rope(x(4, 2, 64), x(4, 1, 64), table, table, x(4, d=torch.int32))
