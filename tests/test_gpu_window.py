@@ -281,3 +281,41 @@ def test_decode_rounds_once(kda_lib, cuda_dev, N, Hq, Hkv, d, W):
     want, size = (w @ V).flatten(1, 2), (w @ V.abs()).flatten(1, 2)
     bound = 2.0 ** -8 * want.abs() + 2.0 ** -16 * size + 1e-30
     assert ((o.double() - want).abs() <= bound).all(), ((o.double() - want).abs() / bound).max()
+
+
+def _reference_on(dev, q, k, v, cu_q, cu_k, window, sinks):
+    """window_reference on the GPU, head by head: (o, lse, size) in 64 bits."""
+    Hq, Hkv, d = q.shape[1], k.shape[1], q.shape[2]
+    o, size = torch.zeros(q.shape, dtype=torch.float64), torch.zeros(q.shape, dtype=torch.float64)
+    lse = torch.zeros(q.shape[:2], dtype=torch.float64)
+    for n in range(len(cu_q) - 1):
+        a, b, ka, kb = int(cu_q[n]), int(cu_q[n + 1]), int(cu_k[n]), int(cu_k[n + 1])
+        p = torch.arange(kb - ka - (b - a), kb - ka, device=dev)[:, None]
+        j = torch.arange(kb - ka, device=dev)
+        see = (j <= p) & ((j > p - window) | (j < sinks))
+        for h in range(Hq):
+            K, V = (x[ka:kb, h // (Hq // Hkv)].to(dev).double() for x in (k, v))
+            s = (q[a:b, h].to(dev).double() @ K.T * d ** -0.5).masked_fill(~see, float("-inf"))
+            r = torch.logsumexp(s, -1, keepdim=True)
+            w = (s - r).exp()
+            o[a:b, h], size[a:b, h], lse[a:b, h] = (w @ V).cpu(), (w @ V.abs()).cpu(), r[:, 0].cpu()
+    return o, lse, size
+
+
+@pytest.mark.parametrize("lens,hist,Hq,Hkv,d,window,sinks", [
+    # tiles of 8 and 16 heads, the cap at 16 (32 and 48 query heads to a key head)
+    ([300, 1, 70], [0, 90, 33], 8, 1, 128, 100, 5), ([300, 1, 70], [0, 90, 33], 16, 1, 128, 100, 5),
+    ([200, 37], [0, 300], 32, 1, 64, 150, 0), ([200, 37], [0, 300], 64, 2, 128, 129, 130), ([77], [10], 48, 1, 64, 40, 3),
+    ([513], [0], 16, 2, 64, 300, 1), ([130], [700], 24, 3, 128, 500, 20),
+    # six units and more for each CTA, of two tiles to ten, with heads of 128 and of 64
+    ([1500, 333, 40], [0, 700, 0], 128, 8, 128, 300, 20), ([5000], [0], 64, 8, 128, 1000, 0),
+    ([3000, 1100], [0, 129], 64, 8, 64, 700, 64),
+])
+def test_prefill_wide_groups_and_many_units(kda_lib, cuda_dev, lens, hist, Hq, Hkv, d, window, sinks):
+    import serving_kda_chunked_gated_gb300.kda as kda
+    q, k, v, cu, cuk = _inputs(lens, hist, Hq, Hkv, d, seed=Hq + d)
+    ro, rl, size = _reference_on(cuda_dev, q, k, v, cu, cuk, window, sinks)
+    o, lse = kda.window_prefill(q.to(cuda_dev), k.to(cuda_dev), v.to(cuda_dev), window, sinks, cu.to(cuda_dev), cu,
+                                cuk.to(cuda_dev), cuk, want_lse=True)
+    check_window(o, ro, size)
+    _lse_ok(lse, rl, q, k, d ** -0.5)
