@@ -92,3 +92,32 @@ def test_zero_row_and_empty(kda_lib, cuda_dev):
     e = torch.zeros(0, 3, 64, device=cuda_dev)
     qo, ko = kda.qk_norm_rope(e, e, cos, sin, torch.zeros(0, dtype=torch.int32, device=cuda_dev))
     assert qo.shape == (0, 3, 64)
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,d,rot", [
+    (6000, 5, 1, 64, 64), (5000, 7, 5, 64, 32), (4000, 8, 2, 48, 16), (3000, 5, 1, 128, 128), (3000, 7, 5, 128, 64),
+    (2500, 6, 2, 128, 128), (2500, 13, 3, 96, 32), (3000, 16, 8, 128, 128), (1500, 5, 1, 256, 256), (1500, 7, 5, 256, 64),
+    (1200, 14, 6, 200, 48), (2000, 0, 9, 128, 128), (2000, 9, 0, 64, 64),
+])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_long_batches_with_partial_head_groups(kda_lib, cuda_dev, T, Hq, Hkv, d, rot, dtype, interleaved):
+    """Batches long enough that a lane group takes four or eight heads (all widths), head counts that
+    leave the last group of q or k partly empty: every row, and nothing behind the outputs."""
+    import serving_kda_chunked_gated_gb300.kda as kda
+    g = torch.Generator(device=cuda_dev).manual_seed(T + d)
+    r = lambda *s: torch.randn(*s, generator=g, device=cuda_dev)                         # noqa: E731
+    x = r(T, (Hq + Hkv) * d).to(dtype)
+    heads = lambda y, H: y.unflatten(1, (H, d)) if H else y.new_empty(T, 0, d)           # noqa: E731
+    q, k = heads(x[:, :Hq * d], Hq), heads(x[:, Hq * d:], Hkv)
+    pos = torch.randint(0, 900, (T,), generator=g, device=cuda_dev).to(torch.int32)
+    cos, sin = (t.to(cuda_dev) for t in _tables(900, rot))
+    qw, kw = 1 + 0.2 * r(d), 1 + 0.2 * r(d)
+    room = [torch.full(((T * H + 16) * d,), 7.0, dtype=dtype, device=cuda_dev) for H in (Hq, Hkv)]
+    out = tuple(b[:T * H * d].view(T, H, d) for b, H in zip(room, (Hq, Hkv)))
+    kda.qk_norm_rope(q, k, cos, sin, pos, q_weight=qw, k_weight=kw, interleaved=interleaved, out=out)
+    assert all((b[T * H * d:] == 7.0).all() for b, H in zip(room, (Hq, Hkv)))
+    for got, src, w in ((out[0], q, qw), (out[1], k, kw)):
+        if src.shape[1]:
+            ref, size = rope_reference(src.cpu(), w.cpu(), cos.cpu(), sin.cpu(), pos.cpu(), interleaved)
+            _ok(got, ref, size, dtype)
