@@ -266,3 +266,26 @@ def test_prefill_slow_decay_over_half_a_million_tokens(kda_lib, cuda_dev, near_w
     _, S = kda.gdn_prefill(x, x, x, z[:, None].to(cuda_dev), zero, torch.zeros(1, device=cuda_dev), S0=S0.to(cuda_dev))
     want = S0.double() * torch.exp(-torch.log1p(z.double().exp()).sum())
     assert rel(S, want) < TOL_S, rel(S, want)
+
+
+@pytest.mark.parametrize("T,Hk,Hv,gate,z_mean", [(20000, 1, 2, "softplus", -3.0), (20000, 1, 2, "bounded", -1.5),
+                                                 (9001, 1, 1, "softplus", -9.0)])
+def test_prefill_hundreds_of_chunks(kda_lib, cuda_dev, T, Hk, Hv, gate, z_mean):
+    """The error does not grow with the chunks: long prompts, ordinary and slow decay, against 64 bits."""
+    import serving_kda_chunked_gated_gb300.kda as kda
+    d, cu = gdn_inputs([T], Hk, Hv, seed=T, z_mean=z_mean)
+    ro, rS = gdn_reference(**d, cu=cu, gate=gate)
+    o, S = kda.gdn_prefill(**_dev(d, cuda_dev), cu_seqlens=cu.to(cuda_dev), gate=gate)
+    _check(o, S, ro, rS, [T])
+
+
+@pytest.mark.parametrize("lens,Hk,Hv,gate", [([3000], 1, 2, "softplus"), ([1, 700, 0, 129, 24], 2, 6, "bounded")])
+def test_prefill_float32_long_and_packed(kda_lib, cuda_dev, lens, Hk, Hv, gate):
+    """Tolerance as for the states: float32 throughout, an output rounds to 2^-24."""
+    import serving_kda_chunked_gated_gb300.kda as kda
+    d, cu = gdn_inputs(lens, Hk, Hv, seed=lens[0], dtype=torch.float32)
+    ro, rS = gdn_reference(**d, cu=cu, gate=gate)
+    for recurrent in (False, True):
+        o, S = kda.gdn_prefill(**_dev(d, cuda_dev), cu_seqlens=cu.to(cuda_dev), cu_seqlens_host=cu, gate=gate,
+                               recurrent=recurrent)
+        _check(o, S, ro, rS, lens, tol_o=TOL_S)
