@@ -426,8 +426,10 @@ kda_status kda_kcp_apply(const float* M, float* X, const float* add, int H, int 
  *   o may be NULL when only the final states are wanted.
  * Hv a multiple of Hk.  cu_seqlens / cu_seqlens_host as for kda_prefill.
  *
- * kda_gdn_prefill, bf16: the chunked form (128-token chunks, tensor cores; sequences of
- * at most 24 tokens may take the recurrence, where that is faster); the
+ * kda_gdn_prefill, bf16: the chunked form (128-token chunks, tensor cores).  A batch
+ * without sequences of more than 24 tokens takes the recurrence; in a batch of at most
+ * 1024 sequences with longer ones those of up to 24 tokens take it where an estimate
+ * finds that faster; past 1024 they each take a chunk (split such batches).  The
  * workspace must hold kda_gdn_prefill_workspace_size() bytes, else
  * KDA_ERR_WORKSPACE.  Its first 4 bytes are the call's error word, read with
  * kda_get_last_device_error.  Every product that reaches a final state splits its

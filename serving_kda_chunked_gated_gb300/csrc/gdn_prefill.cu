@@ -59,14 +59,18 @@ constexpr int WS_HEAD = 256;                  // the error word's line
 
 // For up to MAX_LISTED sequences the host lays the work out.  Scans of the longest start first: one of
 // 4097 tokens among eight shorter ones otherwise starts when these are done.  Beyond, every CTA
-// adds up cu_seqlens itself.
+// adds up cu_seqlens itself, and every sequence goes in chunks: the lists are kernel arguments.
 //
-// A chunk takes its two kernels 36 us however full it is, and where the GPU is full 240 ns for each value
+// A chunk takes its two kernels 33 us however full it is, and where the GPU is full 240 ns for each value
 // head; the recurrence 1 us a token, and where the GPU is full 20 ns for each state and 11 for each of its
-// tokens.  So batches of at most SHORT tokens a sequence take the recurrence, and so do such sequences
-// in a listed batch with longer ones where the estimates say so, in a launch of their own beside the
-// scan's last CTAs: 200 sequences of one token and one of 2000, 32 heads: 1490 us all in chunks, 239 so;
-// one of 9 and one of 6433: 244, 261.
+// tokens.  So batches of at most SHORT tokens a sequence take the recurrence.  Chunks and recurrence, 32
+// heads, us: 1 sequence of 4 tokens 33, 7, of 24 33, 26; 256 of 4 1812, 402, of 20 1822, 1670, of 24
+// 1818, 1985; 1000 of 24 7065, 7655; 4 heads, 1000 of 24 910, 975: from 22 tokens on the recurrence of a full GPU
+// is up to 9 % behind, that of an idle one ahead.  Such sequences in a listed batch with longer ones take it
+// where the estimates say so, in a launch of their own beside the scan's last CTAs: 200 sequences of one
+// token and one of 2000, 32 heads: 1490 us all in chunks, 239 so; one of 9 and one of 6433: 244, 261; 1023
+// of one token and one of 2000: 7234, 841.  The list's end is a step: 1024 of one token and one
+// of 2000, not listed any more, take 8451.
 constexpr int SHORT = 24;
 
 struct Params {
