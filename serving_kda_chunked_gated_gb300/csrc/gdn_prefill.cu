@@ -53,7 +53,7 @@ constexpr int TILE = C * DH * 2;              // a K or Q tile: two slabs of 64 
 // slab of columns 0 .. 63 and the lower half of its slab of columns 64 .. 127 (the upper
 // half is zero), rows of 128 bytes in the 128-byte swizzle.
 constexpr int TRI = 16384 + 8192;
-constexpr int REC_THI = 0, REC_TLO = TRI, REC_P = 2 * TRI, REC_F = 3 * TRI;
+constexpr int REC_THI = 0, REC_TLO = TRI, REC_A = 2 * TRI, REC_F = 3 * TRI;
 constexpr int REC = 3 * TRI + C * 16 + 128;   // + four factors per token + e^{g_C} and the record's ERR_ bits
 constexpr int WS_HEAD = 256;                  // the error word's line
 
@@ -150,7 +150,7 @@ KDA_DEV void split2(float x0, float x1, uint32_t* hi, uint32_t* lo) {
 constexpr int PT = 512;                       // threads
 constexpr int XS = 140;                       // row stride of the inverse's float matrix
 constexpr int YS = 68;                        // and of the merges' intermediate one
-constexpr int P_X = 0, P_Y = P_X + C * XS * 4, P_W = P_Y + TRI, P_D = P_W + 8 * C * 4, P_END = P_D + 8 * 256 * 4;
+constexpr int P_X = 0, P_Y = P_X + C * XS * 4, P_W = P_Y + TRI, P_END = P_W + 8 * C * 4;
 constexpr int P_SMEM = P_END + 1024;
 static_assert(64 * YS * 4 <= TRI && 2 * TILE <= P_Y, "the intermediate matrix shares the record part's place, the tiles the inverse's");
 
@@ -167,80 +167,38 @@ KDA_DEV void split_tf32(float x, float* hi, float* lo) {
 // shared-memory reads, 3700 cycles for the 64 x 64 products against some 2800 here.)  Within each
 // step of 8, k is taken in the order 0, 2, 4, 6, 1, 3, 5, 7, so that a lane's two values of L
 // are neighbours.  Six independent accumulators: the steps wait for nothing but their loads.
-struct Acc { float v[2][3][4] = {}; };
-KDA_DEV void tile_step(Acc& acc, const float* l, int ls, const float* r0, int rs) {      // 8 of k
-    float ah[4], al[4];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const float2 x = *reinterpret_cast<const float2*>(l + q * 8 * ls);
-        split_tf32(x.x, &ah[q], &al[q]);
-        split_tf32(x.y, &ah[q + 2], &al[q + 2]);
-    }
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-        float bh[2], bl[2];
-        const float* r = r0 + n * 8;
-        split_tf32(r[0], &bh[0], &bl[0]);
-        split_tf32(r[rs], &bh[1], &bl[1]);
-        tc::mma_m16n8k8_tf32(acc.v[n][0], ah, bh);
-        tc::mma_m16n8k8_tf32(acc.v[n][1], al, bh);
-        tc::mma_m16n8k8_tf32(acc.v[n][2], ah, bl);
-    }
-}
 KDA_DEV void tile_product(float* out, int os, float sign, const float* Lm, int ls, const float* Rm, int rs, int nk, int lane) {
     const int g = lane >> 2, t = lane & 3;
-    Acc acc;
+    float acc[2][3][4] = {};
     const float* l0 = Lm + g * ls + 2 * t;
     const float* r0 = Rm + 2 * t * rs + g;
 #pragma unroll 2
-    for (int k = 0; k < nk; ++k) tile_step(acc, l0 + k * 8, ls, r0 + k * 8 * rs, rs);
+    for (int k = 0; k < nk; ++k) {
+        float ah[4], al[4];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const float2 x = *reinterpret_cast<const float2*>(l0 + q * 8 * ls + k * 8);
+            split_tf32(x.x, &ah[q], &al[q]);
+            split_tf32(x.y, &ah[q + 2], &al[q + 2]);
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            float bh[2], bl[2];
+            const float* r = r0 + k * 8 * rs + n * 8;
+            split_tf32(r[0], &bh[0], &bl[0]);
+            split_tf32(r[rs], &bh[1], &bl[1]);
+            tc::mma_m16n8k8_tf32(acc[n][0], ah, bh);
+            tc::mma_m16n8k8_tf32(acc[n][1], al, bh);
+            tc::mma_m16n8k8_tf32(acc[n][2], ah, bl);
+        }
+    }
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
         float v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = sign * (acc.v[n][0][i] + (acc.v[n][1][i] + acc.v[n][2][i]));
+        for (int i = 0; i < 4; ++i) v[i] = sign * (acc[n][0][i] + (acc[n][1][i] + acc[n][2][i]));
         *reinterpret_cast<float2*>(out + g * os + n * 8 + 2 * t) = make_float2(v[0], v[1]);
         *reinterpret_cast<float2*>(out + (g + 8) * os + n * 8 + 2 * t) = make_float2(v[2], v[3]);
-    }
-}
-
-// The masked Q K^T, float32, waits for T where the inverse's matrix has nothing: its block (i, j), j < i,
-// as block (j, i) of X, the diagonal blocks in their own 16 x 16 places (columns 0 .. 7 and 8 .. 15
-// change places in every other pair of rows, against bank conflicts).
-KDA_DEV int diag_at(int r, int c) { return r * 16 + (c ^ ((r & 2) << 2)); }
-
-// Warps' tiles of P, (row, column) blocks as two octal digits, at most three; tile (i, j) is i - j + 1 products.
-constexpr uint32_t tiles(int a, int b = -1, int c = -1) {
-    return (64 | a) | (b < 0 ? 0u : (64u | b) << 7) | (c < 0 ? 0u : (64u | c) << 14);
-}
-__constant__ const uint32_t P_TILES[16] = {
-    tiles(070), tiles(060, 033), tiles(071, 044), tiles(050, 065), tiles(061, 076), tiles(072, 000, 055),
-    tiles(040, 021, 066), tiles(051, 032, 077), tiles(062, 043), tiles(073, 054), tiles(030, 042), tiles(041, 053),
-    tiles(052, 064), tiles(063, 075), tiles(074, 010, 011), tiles(020, 031, 022)};
-
-// Block (i, j) of P = (masked Q K^T) T into its image, bf16, by one warp.
-KDA_DEV void p_tile(uint8_t* img, const float* X, const float* Dg, int i, int j, int lane) {
-    const int g = lane >> 2, t = lane & 3;
-    Acc acc;
-#pragma unroll 1
-    for (int k = j; k < i; ++k) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-            tile_step(acc, X + (16 * k + g) * XS + 16 * i + 8 * e + 2 * t, XS, X + (16 * k + 8 * e + 2 * t) * XS + 16 * j + g, XS);
-    }
-#pragma unroll
-    for (int e = 0; e < 2; ++e)      // (rows g and g + 8 have their halves in the same order)
-        tile_step(acc, Dg + i * 256 + diag_at(g, 8 * e) + 2 * t, 16, X + (16 * i + 8 * e + 2 * t) * XS + 16 * j + g, XS);
-    uint8_t* dst = img + (j < 4 ? 0 : 16384 - 64 * 128);
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-        float v[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = acc.v[n][0][q] + (acc.v[n][1][q] + acc.v[n][2][q]);
-        const __nv_bfloat162 h0 = __floats2bfloat162_rn(v[0], v[1]), h1 = __floats2bfloat162_rn(v[2], v[3]);
-        const int piece = (j & 3) * 2 + n;
-        *reinterpret_cast<uint32_t*>(dst + swz(16 * i + g, piece) + 4 * t) = *reinterpret_cast<const uint32_t*>(&h0);
-        *reinterpret_cast<uint32_t*>(dst + swz(16 * i + g + 8, piece) + 4 * t) = *reinterpret_cast<const uint32_t*>(&h1);
     }
 }
 
@@ -352,8 +310,7 @@ gdn_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
     uint8_t* recs = reinterpret_cast<uint8_t*>(a.workspace) + WS_HEAD + (idx * a.Hv + hk * rep) * (size_t)REC;
     for (int e = tid; !ok && e < rep; e += PT) *reinterpret_cast<int*>(recs + e * (size_t)REC + REC_F + C * 16 + 4) = s_err;
     float* X = reinterpret_cast<float*>(sm + P_X);        // the tiles have been consumed
-    uint8_t* img = sm + P_Y;                              // Y, then P on its way out
-    float* Dg = reinterpret_cast<float*>(sm + P_D);       // diagonal blocks of the masked Q K^T
+    uint8_t* img = sm + P_Y;                              // the masked Q K^T on its way out, then Y
     float* W = reinterpret_cast<float*>(sm + P_W);        // W[b][j] = rk_j e^{g_(16 b - 1) - g_j}, j < 16 b
     constexpr float FIX = 1099511627776.f, UNFIX = 1.f / 1099511627776.f;      // 2^40
     for (int e = 0; ok && e < rep; ++e) {
@@ -404,8 +361,8 @@ gdn_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
         }
         if (tid == 0) tc::bulk_wait_read();       // the last head's image has left
         __syncthreads();
-        // A and the masked Q K^T into X: 16 x 16 blocks on and below the diagonal, column block quarter or
-        // quarter + 4 of the row
+        // A into X and the masked Q K^T into its image: 16 x 16 blocks on and below the diagonal,
+        // column block quarter or quarter + 4 of the row
         {
             const int b = row >> 4;
             const float u = b ? exp2f((float)(gi - s_g[16 * b - 1]) * UNFIX) : 0.f;     // e^{g_i - g_(16 b - 1)}
@@ -415,26 +372,28 @@ gdn_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
 #pragma unroll 1
             for (int cb = quarter; cb < 8; cb += 4) {
                 if (cb >= 4 && (warp & 3) < 2) break;        // rows 0 .. 63 have no columns behind 63
+                uint8_t* dst = img + (cb < 4 ? 0 : 16384 - 64 * 128);
+                const int piece = (cb & 3) * 2;
                 float G[16], P[16];
                 tc::tmem_ld16(lane0 + cb * 16, G);
                 tc::tmem_ld16(lane0 + 128 + cb * 16, P);
                 tc::tmem_ld_wait();
+                uint32_t q[8] = {0, 0, 0, 0, 0, 0, 0, 0};
                 if (cb < b) {
                     // below the diagonal nothing is masked, and rows behind the sequence have ka = qa = 0
                     // over zeroed (finite) products
-                    float* low = X + row * XS + cb * 16;
-                    float* up = X + (cb * 16 + (row & 15)) * XS + b * 16;
 #pragma unroll
                     for (int c = 0; c < 16; c += 4) {
                         const float4 w = *reinterpret_cast<const float4*>(W + b * C + cb * 16 + c);
-                        *reinterpret_cast<float4*>(low + c) =
+                        *reinterpret_cast<float4*>(X + row * XS + cb * 16 + c) =
                             make_float4(kau * (w.x * G[c]), kau * (w.y * G[c + 1]), kau * (w.z * G[c + 2]), kau * (w.w * G[c + 3]));
-                        *reinterpret_cast<float4*>(up + c) =
-                            make_float4(qau * (w.x * P[c]), qau * (w.y * P[c + 1]), qau * (w.z * P[c + 2]), qau * (w.w * P[c + 3]));
+                        const __nv_bfloat162 h0 = __floats2bfloat162_rn(qau * (w.x * P[c]), qau * (w.y * P[c + 1]));
+                        const __nv_bfloat162 h1 = __floats2bfloat162_rn(qau * (w.z * P[c + 2]), qau * (w.w * P[c + 3]));
+                        q[c >> 1] = *reinterpret_cast<const uint32_t*>(&h0);
+                        q[(c >> 1) + 1] = *reinterpret_cast<const uint32_t*>(&h1);
                     }
                 } else if (cb == b) {
                     // masked places by selection, not by a product with 0
-                    float* dg = Dg + b * 256;
 #pragma unroll
                     for (int c = 0; c < 16; c += 4) {
                         float x[4], y[4];
@@ -446,13 +405,22 @@ gdn_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
                             y[i] = j <= row && live ? qa * w * P[c + i] : 0.f;
                         }
                         *reinterpret_cast<float4*>(X + row * XS + cb * 16 + c) = make_float4(x[0], x[1], x[2], x[3]);
-                        *reinterpret_cast<float4*>(dg + diag_at(row & 15, c)) = make_float4(y[0], y[1], y[2], y[3]);
+                        const __nv_bfloat162 h0 = __floats2bfloat162_rn(y[0], y[1]), h1 = __floats2bfloat162_rn(y[2], y[3]);
+                        q[c >> 1] = *reinterpret_cast<const uint32_t*>(&h0);
+                        q[(c >> 1) + 1] = *reinterpret_cast<const uint32_t*>(&h1);
                     }
                 }
+                *reinterpret_cast<uint4*>(dst + swz(row, piece)) = make_uint4(q[0], q[1], q[2], q[3]);
+                *reinterpret_cast<uint4*>(dst + swz(row, piece + 1)) = make_uint4(q[4], q[5], q[6], q[7]);
                 __syncwarp();
             }
+            tc::fence_proxy_async();
         }
         __syncthreads();
+        if (tid == 0) {
+            tc::bulk_store(rec + REC_A, img, TRI);
+            tc::bulk_commit();
+        }
         // inverses of the diagonal blocks: lane c < 16 of warp b solves for column c of block b
         if (warp >= 8) {
             float* B = X + (warp - 8) * 16 * XS + (warp - 8) * 16;
@@ -478,6 +446,7 @@ gdn_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
                 for (int i = 0; i < 16; ++i) B[i * XS + lane] = x[i];
             }
         }
+        if (tid == 0) tc::bulk_wait_read();       // the image becomes Y
         __syncthreads();
         // Merges to blocks of 32, 64, 128 in 16 x 16 tiles, a warp each: Y = B X, then - Z Y with Z the
         // lower block's inverse.  X and Z are lower triangular: k from the tile's column on, and up
@@ -496,16 +465,6 @@ gdn_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
                              Y + m * s * YS + 16 * i, YS, 2 * (j + 1), lane);
             __syncthreads();
         }
-        // P = (masked Q K^T) T: 36 tiles of 1 to 8 block products, 8 to a warp at most; the image's blocks
-        // above the diagonal are zero
-#pragma unroll 1
-        for (uint32_t list = P_TILES[warp]; list; list >>= 7) p_tile(img, X, Dg, (list >> 3) & 7, list & 7, lane);
-        if (warp >= 4) {
-            const int z = warp - 4, m = z % 6, i = m < 3 ? 0 : m < 5 ? 1 : 2, j = m < 3 ? m + 1 : m < 5 ? m - 1 : 3;
-            uint8_t* dst = img + (z < 6 ? 0 : 16384);
-            *reinterpret_cast<uint4*>(dst + swz(16 * i + (lane & 15), 2 * j + (lane >> 4))) = make_uint4(0, 0, 0, 0);
-        }
-        tc::fence_proxy_async();
         // T = hi + lo, 16 bytes of each per thread and step; blocks above the diagonal are zero
         for (int i = tid; i < (C + 64) * 8; i += PT) {
             const int c = i & 7, rr = i >> 3;
@@ -523,10 +482,6 @@ gdn_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
             *reinterpret_cast<uint4*>(rec + REC_TLO + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
         __syncthreads();
-        if (tid == 0) {
-            tc::bulk_store(rec + REC_P, img, TRI);
-            tc::bulk_commit();
-        }
     }
     if (tid == 0) tc::bulk_wait_all();
     tc::fence_before_sync();
@@ -539,15 +494,27 @@ gdn_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
 // ---------------------------------------------------------------------------
 constexpr int COLS = 32;                      // value columns per CTA
 constexpr int ST = 448;                       // warps 0-7 state rows, 8-11 output rows, 12 loads, 13 MMAs
-constexpr int S_K = 0, S_Q = 2 * TILE, S_THI = 3 * TILE, S_TLO = S_THI + 32768, S_P = S_TLO + 32768,
-              S_S = S_P + 32768, S_R = S_S + 16384, S_END = S_R + 16384;
+constexpr int S_K = 0, S_Q = 2 * TILE, S_THI = 3 * TILE, S_TLO = S_THI + 32768, S_A = S_TLO + 32768,
+              S_S = S_A + 32768, S_R = S_S + 16384, S_END = S_R + 16384;
 constexpr int S_SMEM = S_END + 1024;
-// The zero half-slabs of two triangular operands are lent out while no MMA reads them and
-// zeroed again by their readers (both are 128 rows of 64 bytes, 64-byte swizzle): T's high part
-// takes the chunk's values v until R is formed, P the output rows on their way out.
-constexpr int S_VIN = S_THI + 16384, S_O = S_P + 16384;
+// The zero half-slabs of the triangular operands are lent out while no MMA reads them and
+// zeroed again by their readers (all are 128 rows of 64 bytes, 64-byte swizzle): T's high part
+// takes the chunk's values v until R is formed, its low part V' in bf16 (the masked product's
+// operand) from T R on, the masked Q K^T the output rows on their way out.
+constexpr int S_VIN = S_THI + 16384, S_V = S_TLO + 16384, S_O = S_A + 16384;
 // TMEM columns (Q S twice: the outputs of a chunk are read while the next one's are formed)
-constexpr int D_KS = 0, D_TR = 64, D_KV = 128, D_PR = 192, D_QS = 256, D_COLS = 512;
+constexpr int D_KS = 0, D_TR = 64, D_KV = 128, D_AV = 192, D_QS = 256, D_COLS = 512;
+
+// descriptor of the 128 x 32 MN-major operand with 64-byte rows (64-byte swizzle)
+KDA_DEV uint64_t sw64_desc_mn(uint32_t addr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((addr >> 4) & 0x3FFFu);
+    d |= (uint64_t)1 << 16;                            // one 32-element block: unused
+    d |= (uint64_t)((512u >> 4) & 0x3FFFu) << 32;      // 8-row K groups
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)4 << 61;                            // 64-byte swizzle
+    return d;
+}
 
 // byte offset of 16-byte piece c (0 .. 3) of row r in rows of 64 bytes
 KDA_DEV uint32_t swz64(int r, int c) { return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4)); }
@@ -583,8 +550,8 @@ __global__ void __launch_bounds__(ST, 1)
 gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                 const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo) {
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t k_full[2], k_empty[2], q_full, t_full, p_full, v_full, edge, s_ready, r_ready, v_ready,
-        o_free, ks_done, qs_done, tr_done, kv_done, pr_done, drained;
+    __shared__ __align__(8) uint64_t k_full[2], k_empty[2], q_full, t_full, a_full, v_full, edge, s_ready, r_ready, v_ready,
+        ks_done, qs_done, tr_done, kv_done, av_done, drained;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     const kda_gdn_prefill_args& a = p.a;
@@ -600,13 +567,12 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
     volatile int* abort = &s_abort;
 
     if (tid == 0) {
-        uint64_t* ones[] = {&k_full[0], &k_full[1], &k_empty[0], &k_empty[1], &q_full, &t_full, &p_full, &v_full, &edge, &ks_done,
-                            &qs_done, &tr_done, &kv_done, &pr_done, &drained};
+        uint64_t* ones[] = {&k_full[0], &k_full[1], &k_empty[0], &k_empty[1], &q_full, &t_full, &a_full, &v_full, &edge, &ks_done,
+                            &qs_done, &tr_done, &kv_done, &av_done, &drained};
         for (uint64_t* b : ones) tc::mbar_init(b, 1);
         tc::mbar_init(&s_ready, 8);         // warps
-        tc::mbar_init(&r_ready, 8);
-        tc::mbar_init(&v_ready, 8);
-        tc::mbar_init(&o_free, 4);
+        tc::mbar_init(&r_ready, 8 + 4);
+        tc::mbar_init(&v_ready, 8 + 4);
         tc::mbar_fence_init();
         s_abort = 0;
     }
@@ -635,7 +601,7 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
             wait_go(bar, parity, limit, abort);
             return !__any_sync(~0u, *abort);
         };
-        uint32_t nk0 = 0, nk1 = 0, nq = 0, nt = 0, np = 0, ne = 0;    // phases begun per barrier
+        uint32_t nk0 = 0, nk1 = 0, nq = 0, nt = 0, na = 0, ne = 0;    // phases begun per barrier
         for (int c = 0; c < nc; ++c) {
             if (__any_sync(~0u, *abort)) break;
             const uint8_t* rec = recs + c * rec_step;
@@ -680,11 +646,11 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
                 tc::bulk_load(sm + S_TLO + 16384 + 8192, rec + REC_TLO + 16384, 8192, &t_full);
             }
             ++nt;
-            if (c >= 1 && !wait_all(&pr_done, (c - 1) & 1)) break;
+            if (c >= 1 && !wait_all(&av_done, (c - 1) & 1)) break;
             if (lane == 0) {
-                tc::mbar_arrive_expect_tx(&p_full, TRI);
-                tc::bulk_load(sm + S_P, rec + REC_P, 16384, &p_full);
-                tc::bulk_load(sm + S_P + 16384 + 8192, rec + REC_P + 16384, 8192, &p_full);
+                tc::mbar_arrive_expect_tx(&a_full, TRI);
+                tc::bulk_load(sm + S_A, rec + REC_A, 16384, &a_full);
+                tc::bulk_load(sm + S_A + 16384 + 8192, rec + REC_A + 16384, 8192, &a_full);
                 // two chunks ahead into L2: this slice's values, and its share of what all slices read
                 if (c + 2 < nc) {
                     const uint8_t* far = rec + 2 * rec_step;
@@ -696,20 +662,20 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
                     else tc::bulk_prefetch(far + REC_F, C * 16 + 128);
                 }
             }
-            ++np;
+            ++na;
         }
         // the last phase of every load has landed before the CTA leaves
         if (lane == 0) {
             const bool d = tc::drain_phase(&edge, ne) && tc::drain_phase(&k_full[0], nk0) && tc::drain_phase(&k_full[1], nk1) &&
                            tc::drain_phase(&q_full, nq) && tc::drain_phase(&t_full, nt) && tc::drain_phase(&v_full, nt) &&
-                           tc::drain_phase(&p_full, np);
+                           tc::drain_phase(&a_full, na);
             if (*abort || !d)
                 atomicOr(reinterpret_cast<int*>(a.workspace), d ? tc::ERR_WAIT : tc::ERR_WAIT | tc::ERR_DRAIN);
         }
     } else if (warp == 13) {
         // ---------------- MMAs: the warp computes together, one lane issues ----------------
         // Per chunk 48 MMAs of 41 (N = 32) or 47 (N = 64) cycles: K S, T R and K^T V'' on the chain from
-        // state to state, Q S and P R in the gaps that the rows' arithmetic leaves.
+        // state to state, Q S and (masked Q K^T) V' in the gaps that the rows' arithmetic leaves.
         const uint32_t tmu = __shfl_sync(~0u, tm, 0), sb = __shfl_sync(~0u, tc::smem_u32(sm), 0);
         const uint32_t id64 = tc::idesc_bf16(128, 64, false, true), id32 = tc::idesc_bf16(128, 32, false, true),
                        idt = tc::idesc_bf16(128, 64, true, true);
@@ -720,23 +686,26 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
             for (int k = 0; k < 8; ++k)
                 tc::mma_f16_ss_elect(d, ad + (((k >> 2) * 16384 + (k & 3) * 32) >> 4), bd + k * (step >> 4), id, acc || k > 0);
         };
-        // Turn i: K^T V'' of chunk i - 1, then K S, Q S, T R and P R of chunk i.  The way back to the
-        // loop's top (some 500 cycles of instruction fetch) so falls into the wait for V'', not between a
-        // state and the next K S.
+        // Turn i: K^T V'' and (masked Q K^T) V' of chunk i - 1, then K S, Q S and T R of chunk i.  The
+        // way back to the loop's top (some 500 cycles of instruction fetch) so falls into the
+        // wait for V'', not between a state and the next K S.
 #pragma unroll 1
         for (int i = 0; i <= nc; ++i) {
             if ((i & 7) == 7 && __any_sync(~0u, *abort)) break;
             if (i > 0) {
                 const uint32_t ph = (i - 1) & 1;
                 const uint64_t dKt = tc::sw128_desc_mn(sb + S_K + ph * TILE, 16384);
+                wait_go(&a_full, ph, limit, abort);
                 wait_go(&v_ready, ph, limit, abort);
                 __syncwarp();
                 tc::fence_after_sync();
 #pragma unroll
                 for (int k = 0; k < 8; ++k)                                        // K^T: tokens are the K rows
-                    tc::mma_f16_ss_elect(tmu + D_KV, dKt + k * (2048 >> 4), dS + k * (2048 >> 4), idt, k > 0);
+                    tc::mma_f16_ss_elect(tmu + D_KV, dKt + k * (2048 >> 4), dR + k * (2048 >> 4), idt, k > 0);
                 tc::mma_commit_elect(&kv_done);
                 tc::mma_commit_elect(&k_empty[ph]);
+                rows(tmu + D_AV, tc::sw128_desc(sb + S_A), sw64_desc_mn(sb + S_V), 1024, id32, false);
+                tc::mma_commit_elect(&av_done);
             }
             if (i < nc) {
                 const uint32_t ph = i & 1;
@@ -758,12 +727,6 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
                 rows(tmu + D_TR, tc::sw128_desc(sb + S_THI), dR, 2048, id64, false);
                 rows(tmu + D_TR, tc::sw128_desc(sb + S_TLO), dR, 2048, id32, true);
                 tc::mma_commit_elect(&tr_done);
-                wait_go(&p_full, ph, limit, abort);
-                if (i > 0) wait_go(&o_free, (i - 1) & 1, limit, abort);            // the last chunk's output rows are through
-                __syncwarp();
-                tc::fence_after_sync();
-                rows(tmu + D_PR, tc::sw128_desc(sb + S_P), dR, 2048, id64, false);
-                tc::mma_commit_elect(&pr_done);
             }
         }
         __syncwarp();
@@ -777,15 +740,19 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
         // ---------------- output rows: one token per thread, 32 columns ----------------
         const int row = tid & 127;
         const uint32_t tl = tm + ((uint32_t)(warp & 3) << 21);
+        if (nc > 0) {
+            tc::mbar_arrive_warp(&r_ready);
+            tc::mbar_arrive_warp(&v_ready);
+        }
 #pragma unroll 1
         for (int c = 0; c < nc; ++c) {
             if ((c & 7) == 7 && any_of_128(*abort != 0)) break;    // all four warps or none: they share barriers
             const uint32_t ph = c & 1;
             const float fw = __ldcg(reinterpret_cast<const float*>(recs + c * rec_step + REC_F + row * 16 + 12));
             float o[32], x[32];
-            // The next P R waits for these rows: a barrier that could run two phases ahead of its reader
-            // (that of Q S) is not waited on here
-            wait_go(&pr_done, ph, limit, abort);
+            // A V' is the chunk's last product, and the next one waits for these rows: a barrier that
+            // could run two phases ahead of its reader (that of Q S) is not waited on here
+            wait_go(&av_done, ph, limit, abort);
             __syncwarp();
             tc::fence_after_sync();
             tc::tmem_ld32(tl + D_QS + 64 * ph, o);
@@ -793,14 +760,14 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
             tc::tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = fw * (o[i] + x[i]);                // scale rq e^g (Q S)
-            tc::tmem_ld32(tl + D_PR, x);
-            tc::tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] += x[i];
-            tc::tmem_ld32(tl + D_PR + 32, x);
-            tc::tmem_ld_wait();
-            tc::fence_before_sync();
+            tc::tmem_ld32(tl + D_AV, x);
             const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(sm + S_V + row * 64 + 16 * i) = zero;   // T's zeros again
+            tc::tmem_ld_wait();
+            tc::fence_proxy_async();
+            tc::fence_before_sync();
+            if (c + 1 < nc) tc::mbar_arrive_warp(&r_ready);
             const bool whole = (c + 1) * C <= T;
             if (a.o) {
 #pragma unroll
@@ -826,7 +793,7 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
                     for (int i = 0; i < 4; ++i) store8_bf16(out + 8 * i, o + 8 * i);
                 }
             }
-            if (c + 1 < nc) tc::mbar_arrive_warp(&o_free);
+            if (c + 1 < nc) tc::mbar_arrive_warp(&v_ready);
             __syncwarp();
         }
         if (tid == 256) tc::bulk_wait_all();
@@ -898,16 +865,26 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
                 const int c = i - 1;
                 const uint32_t ph = c & 1;
                 const bool live = c * C + row < T;
-                // V'' = e^{g_C - g} rk T R in S's place (K S and Q S are done with it; P R still reads R)
+                // V' = T R, and V'' = e^{g_C - g} rk V' over R (T R is done with it)
                 wait_go(&tr_done, ph, limit, abort);
                 __syncwarp();
                 tc::fence_after_sync();
                 tc::tmem_ld16(tl + D_TR, x);
                 tc::tmem_ld16(tl + D_TR + 32, y);
                 tc::tmem_ld_wait();
+                uint32_t vb[8];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) x[e] = live ? f.z * (x[e] + y[e]) : 0.f;
-                store_split(sm + S_S, row, w, x);
+                for (int e = 0; e < 16; e += 2) {
+                    x[e] = live ? x[e] + y[e] : 0.f;
+                    x[e + 1] = live ? x[e + 1] + y[e + 1] : 0.f;
+                    const __nv_bfloat162 hh = __floats2bfloat162_rn(x[e], x[e + 1]);      // for o only
+                    vb[e >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
+                    x[e] *= f.z;
+                    x[e + 1] *= f.z;
+                }
+                *reinterpret_cast<uint4*>(sm + S_V + swz64(row, 2 * w)) = make_uint4(vb[0], vb[1], vb[2], vb[3]);
+                *reinterpret_cast<uint4*>(sm + S_V + swz64(row, 2 * w + 1)) = make_uint4(vb[4], vb[5], vb[6], vb[7]);
+                store_split(sm + S_R, row, w, x);
                 tc::fence_proxy_async();
                 tc::fence_before_sync();
                 tc::mbar_arrive_warp(&v_ready);
