@@ -435,8 +435,9 @@ kda_status kda_kcp_apply(const float* M, float* X, const float* add, int H, int 
  * kda_get_last_device_error.  Every product that reaches a final state splits its
  * float32 operand into two bf16 parts: states are within some 4e-6 of exact ones
  * (relative L2; what S0 left in them takes a float32 rounding, 2^-24 at most, at every
- * chunk, so half a million tokens of slow decay add about 3e-6), o within bf16 roundings
- * of its weights (the masked Q K^T), of the values it weighs and of itself, 2.8e-3 in all.
+ * chunk, so half a million tokens of slow decay add about 3e-6; where keys are all alike
+ * and nothing decays updates cancel from token to token and they are within 1.4e-5).  o
+ * is off by little but its own rounding: its other operands keep 11 bits.
  * float32: the per-token recurrence on CUDA cores, no workspace.
  * kda_gdn_prefill_recurrent: the per-token recurrence for either type.  It rounds the
  * state to float32 at every token, as the step does: over tens of thousands of tokens

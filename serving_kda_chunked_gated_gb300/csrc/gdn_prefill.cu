@@ -14,15 +14,18 @@
 // come out within 4e-6 of exact ones, relative (a third part would need more shared memory than
 // there is); its float32 update adds up to 2^-24 a chunk, which shows where thousands of chunks
 // decay slowly.  Exponents are differences of exact sums (64-bit fixed point) of steps rounded to
-// 2^-41: a decay of e^-600 over the chunk costs the short ones nothing.  Only the product behind o alone, masked Q K^T
-// times V', has both operands rounded to bf16, as attention weights and values are: o is then
-// within 2.8e-3, of which its own rounding is 1.7e-3.  V' in two parts brings 2.2e-3 and
-// costs 14 % (4.30 -> 4.90 ms): that product delays the next K S.
+// 2^-41: a decay of e^-600 over the chunk costs the short ones nothing.  The product behind o alone,
+// masked Q K^T times V', has both operands rounded to fp16, which keeps 11 bits where each is scaled by
+// a power of two into its range: rows of the masked Q K^T by their largest possible entry, V' of a chunk
+// and its 32 columns by the largest there is.  (In bf16 o was within 2.8e-3, where its own rounding is
+// 1.7e-3, and where keys are alike and little decays V' cancels from token to token: 1.1e-2 for a token
+// repeated; fp16 leaves 1.7e-3 and 1.8e-3 for 4.20 -> 4.23 ms.  Forming (masked Q K^T) T in prep and
+// feeding R instead measures 2.2e-3 and 2.1e-3, and 4.63 ms.)
 //
 // prep: one CTA per (chunk, key head) forms K K^T and Q K^T once for all value heads of
 // the key head, then per value head A, its inverse (16 x 16 blocks by substitution, merged
 // by [[X, 0], [B, Z]]^-1 = [[X^-1, 0], [-Z^-1 B X^-1, Z^-1]]), and writes a record: T as two
-// bf16 parts, the masked and scaled Q K^T in bf16, the tokens' factors.
+// bf16 parts, the masked and scaled Q K^T in fp16, the tokens' factors.
 // scan: one CTA per (sequence, value head, 32 value columns) walks the chunks.  Tokens (or
 // key channels) are TMEM lanes, the 32 columns of an operand's hi and lo parts one
 // 128-byte row of 64 MN-major elements: one N = 64 MMA forms both products.
@@ -31,8 +34,8 @@
 // of an SM per chunk and value head), the scan by its chain K S -> R -> T R -> V'' -> K^T V'' -> S,
 // some 4450 cycles a chunk of which 1450 are MMAs, 1600 the rows' arithmetic and 1300 the
 // hand-overs between them; 32 columns rather than 64 or 128 because 32 heads then fill 128 SMs.
-// Measured: 131072 tokens, 16 key and 32 value heads, S0: 4.20 ms (31.2 M tokens/s); 8192
-// tokens, 32 / 32 heads: 0.29 ms, one half prep and one half scan.
+// Measured: 131072 tokens, 16 key and 32 value heads, S0: 4.23 ms (31.0 M tokens/s); 8192
+// tokens, 32 / 32 heads: 0.30 ms, one half prep and one half scan.
 #include <math.h>
 
 #include <algorithm>
@@ -54,7 +57,8 @@ constexpr int TILE = C * DH * 2;              // a K or Q tile: two slabs of 64 
 // half is zero), rows of 128 bytes in the 128-byte swizzle.
 constexpr int TRI = 16384 + 8192;
 constexpr int REC_THI = 0, REC_TLO = TRI, REC_A = 2 * TRI, REC_F = 3 * TRI;
-constexpr int REC = 3 * TRI + C * 16 + 128;   // + four factors per token + e^{g_C} and the record's ERR_ bits
+constexpr int REC_O = REC_F + C * 16 + 128;   // behind four factors per token, e^{g_C} and the record's ERR_ bits
+constexpr int REC = REC_O + C * 4;            // + a factor of the masked product per token
 constexpr int WS_HEAD = 256;                  // the error word's line
 
 // For up to MAX_LISTED sequences the host lays the work out.  Scans of the longest start first: one of
@@ -144,6 +148,11 @@ KDA_DEV void split2(float x0, float x1, uint32_t* hi, uint32_t* lo) {
     *lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
+KDA_DEV uint32_t pack_f16(float x0, float x1) {
+    const __half2 h = __floats2half2_rn(x0, x1);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 // ---------------------------------------------------------------------------
 // prep
 // ---------------------------------------------------------------------------
@@ -208,7 +217,7 @@ gdn_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
     __shared__ __align__(8) uint64_t loaded, done;
     __shared__ uint32_t s_tmem;
     __shared__ int s_err;
-    __shared__ float s_rk[C], s_rq[C], s_beta[C], s_part[4][C];
+    __shared__ float s_rk[C], s_rq[C], s_beta[C], s_part[4][C], s_down[C], s_wmax[4];
     __shared__ long long s_g[C], s_wsum[4];
     const kda_gdn_prefill_args& a = p.a;
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
@@ -338,6 +347,25 @@ gdn_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
             for (int w = 0; w < warp; ++w) g += s_wsum[w];
             s_g[row] = g;
             s_beta[row] = beta;
+            // The largest entry that the masked Q K^T can have in this row, as a power of two: 1 between unit
+            // vectors, else |q_i| max_j e^{g_i - g_j} |k_j|.
+            float up = 1.f;
+            if (!a.qk_l2norm) {
+                const float gi = (float)g * UNFIX;
+                float m = __log2f(s_part[0][row] + s_part[1][row]) * 0.5f - gi;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const float y = __shfl_up_sync(~0u, m, o);
+                    if (lane >= o) m = fmaxf(m, y);
+                }
+                if (lane == 31) s_wmax[warp] = m;
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                for (int w = 0; w < warp; ++w) m = fmaxf(m, s_wmax[w]);
+                m += gi + __log2f(s_part[2][row] + s_part[3][row]) * 0.5f;
+                up = exp2f(fminf(fmaxf(ceilf(m), -100.f), 100.f));
+            }
+            s_down[row] = 1.f / up;
+            *reinterpret_cast<float*>(rec + REC_O + row * 4) = up * a.scale;
         }
         __syncthreads();
         const long long gi = s_g[row], gC = s_g[C - 1];
@@ -366,7 +394,7 @@ gdn_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
         {
             const int b = row >> 4;
             const float u = b ? exp2f((float)(gi - s_g[16 * b - 1]) * UNFIX) : 0.f;     // e^{g_i - g_(16 b - 1)}
-            const float ka = live ? s_beta[row] * s_rk[row] : 0.f, qa = live ? s_rq[row] * a.scale : 0.f;
+            const float ka = live ? s_beta[row] * s_rk[row] : 0.f, qa = live ? s_rq[row] * s_down[row] : 0.f;
             const float kau = ka * u, qau = qa * u;
             const uint32_t lane0 = tm + ((uint32_t)(warp & 3) << 21);
 #pragma unroll 1
@@ -387,10 +415,8 @@ gdn_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
                         const float4 w = *reinterpret_cast<const float4*>(W + b * C + cb * 16 + c);
                         *reinterpret_cast<float4*>(X + row * XS + cb * 16 + c) =
                             make_float4(kau * (w.x * G[c]), kau * (w.y * G[c + 1]), kau * (w.z * G[c + 2]), kau * (w.w * G[c + 3]));
-                        const __nv_bfloat162 h0 = __floats2bfloat162_rn(qau * (w.x * P[c]), qau * (w.y * P[c + 1]));
-                        const __nv_bfloat162 h1 = __floats2bfloat162_rn(qau * (w.z * P[c + 2]), qau * (w.w * P[c + 3]));
-                        q[c >> 1] = *reinterpret_cast<const uint32_t*>(&h0);
-                        q[(c >> 1) + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+                        q[c >> 1] = pack_f16(qau * (w.x * P[c]), qau * (w.y * P[c + 1]));
+                        q[(c >> 1) + 1] = pack_f16(qau * (w.z * P[c + 2]), qau * (w.w * P[c + 3]));
                     }
                 } else if (cb == b) {
                     // masked places by selection, not by a product with 0
@@ -405,9 +431,8 @@ gdn_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
                             y[i] = j <= row && live ? qa * w * P[c + i] : 0.f;
                         }
                         *reinterpret_cast<float4*>(X + row * XS + cb * 16 + c) = make_float4(x[0], x[1], x[2], x[3]);
-                        const __nv_bfloat162 h0 = __floats2bfloat162_rn(y[0], y[1]), h1 = __floats2bfloat162_rn(y[2], y[3]);
-                        q[c >> 1] = *reinterpret_cast<const uint32_t*>(&h0);
-                        q[(c >> 1) + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+                        q[c >> 1] = pack_f16(y[0], y[1]);
+                        q[(c >> 1) + 1] = pack_f16(y[2], y[3]);
                     }
                 }
                 *reinterpret_cast<uint4*>(dst + swz(row, piece)) = make_uint4(q[0], q[1], q[2], q[3]);
@@ -499,7 +524,7 @@ constexpr int S_K = 0, S_Q = 2 * TILE, S_THI = 3 * TILE, S_TLO = S_THI + 32768, 
 constexpr int S_SMEM = S_END + 1024;
 // The zero half-slabs of the triangular operands are lent out while no MMA reads them and
 // zeroed again by their readers (all are 128 rows of 64 bytes, 64-byte swizzle): T's high part
-// takes the chunk's values v until R is formed, its low part V' in bf16 (the masked product's
+// takes the chunk's values v until R is formed, its low part V' in fp16 (the masked product's
 // operand) from T R on, the masked Q K^T the output rows on their way out.
 constexpr int S_VIN = S_THI + 16384, S_V = S_TLO + 16384, S_O = S_A + 16384;
 // TMEM columns (Q S twice: the outputs of a chunk are read while the next one's are formed)
@@ -534,6 +559,13 @@ KDA_DEV bool any_of_128(bool x) {
                  : "=r"(r) : "r"((uint32_t)x) : "memory");
     return r != 0;
 }
+// and of the 256 state threads
+KDA_DEV bool any_of_256(bool x) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 2, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r) : "r"((uint32_t)x) : "memory");
+    return r != 0;
+}
 
 // this thread's 16 columns of a row, hi and lo parts, into the 128-byte row [hi 32 | lo 32]
 KDA_DEV void store_split(uint8_t* base, int row, int w, const float* x) {
@@ -550,10 +582,12 @@ __global__ void __launch_bounds__(ST, 1)
 gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                 const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo) {
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t k_full[2], k_empty[2], q_full, t_full, a_full, v_full, edge, s_ready, r_ready, v_ready,
+    __shared__ __align__(8) uint64_t k_full[2], k_empty[2], q_full, t_full, a_full, v_full, edge, s_ready, r_ready, v_ready, av_ready,
         ks_done, qs_done, tr_done, kv_done, av_done, drained;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
+    __shared__ __align__(16) float s_vmax[8];
+    __shared__ float s_vup[2];
     const kda_gdn_prefill_args& a = p.a;
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -572,7 +606,8 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
         for (uint64_t* b : ones) tc::mbar_init(b, 1);
         tc::mbar_init(&s_ready, 8);         // warps
         tc::mbar_init(&r_ready, 8 + 4);
-        tc::mbar_init(&v_ready, 8 + 4);
+        tc::mbar_init(&v_ready, 8);
+        tc::mbar_init(&av_ready, 8 + 4);
         tc::mbar_fence_init();
         s_abort = 0;
     }
@@ -659,7 +694,7 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
                     if (slice < 2) tc::tma_prefetch_3d(&mk, slice * 64, hk, t2);
                     else tc::tma_prefetch_3d(&mq, (slice - 2) * 64, hk, t2);
                     if (slice < 3) tc::bulk_prefetch(far + slice * TRI, TRI);
-                    else tc::bulk_prefetch(far + REC_F, C * 16 + 128);
+                    else tc::bulk_prefetch(far + REC_F, REC - REC_F);
                 }
             }
             ++na;
@@ -678,7 +713,7 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
         // state to state, Q S and (masked Q K^T) V' in the gaps that the rows' arithmetic leaves.
         const uint32_t tmu = __shfl_sync(~0u, tm, 0), sb = __shfl_sync(~0u, tc::smem_u32(sm), 0);
         const uint32_t id64 = tc::idesc_bf16(128, 64, false, true), id32 = tc::idesc_bf16(128, 32, false, true),
-                       idt = tc::idesc_bf16(128, 64, true, true);
+                       idt = tc::idesc_bf16(128, 64, true, true), idh = tc::idesc_f16(128, 32, false, true);
         const uint64_t dS = tc::sw128_desc_mn(sb + S_S, 16384), dR = tc::sw128_desc_mn(sb + S_R, 16384);
         // D[., cols] = A (K-major tile of two slabs) times B (MN-major, 16 K rows per step)
         auto rows = [&](uint32_t d, uint64_t ad, uint64_t bd, uint32_t step, uint32_t id, bool acc) {
@@ -695,7 +730,6 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
             if (i > 0) {
                 const uint32_t ph = (i - 1) & 1;
                 const uint64_t dKt = tc::sw128_desc_mn(sb + S_K + ph * TILE, 16384);
-                wait_go(&a_full, ph, limit, abort);
                 wait_go(&v_ready, ph, limit, abort);
                 __syncwarp();
                 tc::fence_after_sync();
@@ -704,7 +738,11 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
                     tc::mma_f16_ss_elect(tmu + D_KV, dKt + k * (2048 >> 4), dR + k * (2048 >> 4), idt, k > 0);
                 tc::mma_commit_elect(&kv_done);
                 tc::mma_commit_elect(&k_empty[ph]);
-                rows(tmu + D_AV, tc::sw128_desc(sb + S_A), sw64_desc_mn(sb + S_V), 1024, id32, false);
+                wait_go(&a_full, ph, limit, abort);
+                wait_go(&av_ready, ph, limit, abort);
+                __syncwarp();
+                tc::fence_after_sync();
+                rows(tmu + D_AV, tc::sw128_desc(sb + S_A), sw64_desc_mn(sb + S_V), 1024, idh, false);
                 tc::mma_commit_elect(&av_done);
             }
             if (i < nc) {
@@ -742,13 +780,14 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
         const uint32_t tl = tm + ((uint32_t)(warp & 3) << 21);
         if (nc > 0) {
             tc::mbar_arrive_warp(&r_ready);
-            tc::mbar_arrive_warp(&v_ready);
+            tc::mbar_arrive_warp(&av_ready);
         }
 #pragma unroll 1
         for (int c = 0; c < nc; ++c) {
             if ((c & 7) == 7 && any_of_128(*abort != 0)) break;    // all four warps or none: they share barriers
             const uint32_t ph = c & 1;
             const float fw = __ldcg(reinterpret_cast<const float*>(recs + c * rec_step + REC_F + row * 16 + 12));
+            const float fo = __ldcg(reinterpret_cast<const float*>(recs + c * rec_step + REC_O + row * 4));
             float o[32], x[32];
             // A V' is the chunk's last product, and the next one waits for these rows: a barrier that
             // could run two phases ahead of its reader (that of Q S) is not waited on here
@@ -761,6 +800,7 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = fw * (o[i] + x[i]);                // scale rq e^g (Q S)
             tc::tmem_ld32(tl + D_AV, x);
+            const float fv = fo * s_vup[ph];                                       // undoes both operands' scaling
             const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(sm + S_V + row * 64 + 16 * i) = zero;   // T's zeros again
@@ -771,7 +811,7 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
             const bool whole = (c + 1) * C <= T;
             if (a.o) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] += x[i];
+                for (int i = 0; i < 32; ++i) o[i] += fv * x[i];
                 if (whole) {
                     // through shared memory and one TMA store; the last chunk's rows one by one
 #pragma unroll
@@ -793,7 +833,7 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
                     for (int i = 0; i < 4; ++i) store8_bf16(out + 8 * i, o + 8 * i);
                 }
             }
-            if (c + 1 < nc) tc::mbar_arrive_warp(&v_ready);
+            if (c + 1 < nc) tc::mbar_arrive_warp(&av_ready);
             __syncwarp();
         }
         if (tid == 256) tc::bulk_wait_all();
@@ -860,7 +900,7 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
         // The loop turns over while T R runs: from R of one chunk to R of the next.
 #pragma unroll 1
         for (int i = 0; i <= nc; ++i) {
-            if ((i & 7) == 7 && __any_sync(~0u, *abort)) break;
+            if ((i & 7) == 7 && any_of_256(*abort != 0)) break;    // all eight warps or none: they share a barrier
             if (i > 0) {
                 const int c = i - 1;
                 const uint32_t ph = c & 1;
@@ -872,22 +912,36 @@ gdn_scan_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
                 tc::tmem_ld16(tl + D_TR, x);
                 tc::tmem_ld16(tl + D_TR + 32, y);
                 tc::tmem_ld_wait();
-                uint32_t vb[8];
 #pragma unroll
-                for (int e = 0; e < 16; e += 2) {
+                for (int e = 0; e < 16; ++e) {
                     x[e] = live ? x[e] + y[e] : 0.f;
-                    x[e + 1] = live ? x[e + 1] + y[e + 1] : 0.f;
-                    const __nv_bfloat162 hh = __floats2bfloat162_rn(x[e], x[e + 1]);      // for o only
-                    vb[e >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
-                    x[e] *= f.z;
-                    x[e + 1] *= f.z;
+                    y[e] = x[e] * f.z;
                 }
-                *reinterpret_cast<uint4*>(sm + S_V + swz64(row, 2 * w)) = make_uint4(vb[0], vb[1], vb[2], vb[3]);
-                *reinterpret_cast<uint4*>(sm + S_V + swz64(row, 2 * w + 1)) = make_uint4(vb[4], vb[5], vb[6], vb[7]);
-                store_split(sm + S_R, row, w, x);
+                store_split(sm + S_R, row, w, y);
                 tc::fence_proxy_async();
                 tc::fence_before_sync();
                 tc::mbar_arrive_warp(&v_ready);
+                // V' for o, while K^T V'' runs: fp16, the largest of the chunk's 128 x 32 below 2^15.  (Where
+                // that is infinite nothing is scaled, so that no finite value becomes 0 beside it.)
+                float m = 0.f;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(x[e]));
+                m = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(m)));
+                if (lane == 0) s_vmax[warp] = m;
+                asm volatile("bar.sync 2, 256;" ::: "memory");
+                const float4 m0 = *reinterpret_cast<const float4*>(s_vmax), m1 = *reinterpret_cast<const float4*>(s_vmax + 4);
+                m = fmaxf(fmaxf(fmaxf(m0.x, m0.y), fmaxf(m0.z, m0.w)), fmaxf(fmaxf(m1.x, m1.y), fmaxf(m1.z, m1.w)));
+                int ex = (int)(__float_as_uint(m) >> 23);              // biased exponent: m < 2^(ex - 126)
+                ex = ex == 255 ? 141 : max(ex, 16);
+                const float down = __uint_as_float((uint32_t)(268 - ex) << 23);              // 2^(141 - ex)
+                if (tid == 0) s_vup[ph] = __uint_as_float((uint32_t)(ex - 14) << 23);        // 2^(ex - 141)
+                uint32_t vh[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) vh[e] = pack_f16(x[2 * e] * down, x[2 * e + 1] * down);
+                *reinterpret_cast<uint4*>(sm + S_V + swz64(row, 2 * w)) = make_uint4(vh[0], vh[1], vh[2], vh[3]);
+                *reinterpret_cast<uint4*>(sm + S_V + swz64(row, 2 * w + 1)) = make_uint4(vh[4], vh[5], vh[6], vh[7]);
+                tc::fence_proxy_async();
+                tc::mbar_arrive_warp(&av_ready);
                 // S <- e^{g_C} S + K^T V''
                 wait_go(&kv_done, ph, limit, abort);
                 __syncwarp();

@@ -61,9 +61,11 @@ __host__ __device__ constexpr uint32_t idesc_tf32(int M, int N, bool neg_a = fal
          | ((uint32_t)(M >> 4) << 24);
 }
 
-// Instruction descriptor, kind::f16 with fp16 A and B, FP32 accumulate, both K-major.
-__host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
-    return (1u << 4)                 // D = F32 (A, B = F16: format 0)
+// Instruction descriptor, kind::f16 with fp16 A and B, FP32 accumulate; each operand
+// K-major or MN-major.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn = false, bool b_mn = false) {
+    return (1u << 4)                 // D = F32; A, B = F16
+         | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16)
          | ((uint32_t)(N >> 3) << 17)
          | ((uint32_t)(M >> 4) << 24);
 }

@@ -289,3 +289,86 @@ def test_prefill_float32_long_and_packed(kda_lib, cuda_dev, lens, Hk, Hv, gate):
         o, S = kda.gdn_prefill(**_dev(d, cuda_dev), cu_seqlens=cu.to(cuda_dev), cu_seqlens_host=cu, gate=gate,
                                recurrent=recurrent)
         _check(o, S, ro, rS, lens, tol_o=TOL_S)
+
+
+@pytest.mark.parametrize("keys,beta", [("same", None), ("same", 1.0), ("near", 1.0), ("turned", None)])
+def test_prefill_keys_alike(kda_lib, cuda_dev, keys, beta):
+    """A token repeated, or keys that differ by a few percent, and no decay: what the updates write then cancels
+    from token to token, and an output formed from rounded updates would be off by many of its own roundings.
+
+    Tolerance of the outputs as above.  States: V'' = T R cancels the same way, and each of a chunk's 128 updates
+    is off by 2^-17 of R, uniformly distributed: sqrt(128 / 3) 2^-17 sqrt(2) = 7e-5 at most."""
+    import serving_kda_chunked_gated_gb300.kda as kda
+    d, cu = gdn_inputs([700], 1, 2, z_mean=-30.0, seed=41)
+    g = torch.Generator().manual_seed(41)
+    k = torch.randn(1, 1, 128, generator=g)
+    d["k"] = (k + (0.05 if keys == "near" else 0.0) * torch.randn(700, 1, 128, generator=g)).to(torch.bfloat16)
+    if keys == "turned":
+        d["k"][1::2] *= -1
+    if beta is not None:
+        d["beta"].fill_(beta)
+    ro, rS = gdn_reference(**d, cu=cu)
+    o, S = kda.gdn_prefill(**_dev(d, cuda_dev), cu_seqlens=cu.to(cuda_dev))
+    for h in range(2):
+        assert rel(o[:, h], ro[:, h]) < TOL_O, rel(o[:, h], ro[:, h])
+        assert rel(S[0, h], rS[0, h]) < 7e-5, rel(S[0, h], rS[0, h])
+
+
+ONCE = 2.4e-3    # bf16's own rounding, 2^-8 / sqrt(3) = 2.26e-3 at most in root mean square, and two operands of 11 bits
+
+
+@pytest.mark.parametrize("lens,Hk,Hv,gate", [([700], 1, 2, "softplus"), ([300, 129, 64], 2, 2, "bounded")])
+def test_prefill_outputs_round_once(kda_lib, cuda_dev, lens, Hk, Hv, gate):
+    """Each of the masked product's operands is rounded to 11 bits (2^-11 / sqrt(3) = 2.8e-4), o to 8."""
+    import serving_kda_chunked_gated_gb300.kda as kda
+    d, cu = gdn_inputs(lens, Hk, Hv, seed=43)
+    ro, rS = gdn_reference(**d, cu=cu, gate=gate)
+    o, S = kda.gdn_prefill(**_dev(d, cuda_dev), cu_seqlens=cu.to(cuda_dev), gate=gate)
+    _check(o, S, ro, rS, lens, tol_o=ONCE)
+
+
+@pytest.mark.parametrize("what", ["v tiny", "v huge", "v of all sizes", "zero v", "q, k of all sizes", "k huge", "scale tiny"])
+def test_prefill_sizes_beyond_fp16(kda_lib, cuda_dev, what):
+    """Values, queries and keys (not normalised) far outside fp16's range: nothing of the masked product may be
+    lost.  Sizes change by powers of two up to 2^12 from token to token, where they do."""
+    import serving_kda_chunked_gated_gb300.kda as kda
+    d, cu = gdn_inputs([500], 1, 2, seed=47)
+    g = torch.Generator().manual_seed(47)
+    sizes = torch.exp2(torch.randint(-6, 7, (500, 1, 1), generator=g).float())
+    kw, times = {}, lambda n, x: d.__setitem__(n, (d[n].float() * x).to(torch.bfloat16))          # noqa: E731
+    if what == "v tiny":
+        times("v", 1e-20)
+        d["S0"].mul_(1e-20)
+    elif what == "v huge":
+        times("v", 1e20)
+        d["S0"].mul_(1e20)
+    elif what == "v of all sizes":
+        times("v", sizes)
+    elif what == "zero v":
+        d["v"].zero_()
+        d["S0"].zero_()
+    elif what == "scale tiny":
+        kw["scale"] = 1e-9
+    else:
+        kw["l2"] = False
+        times("k", 0.15)                                     # norms near 1
+        times("q", 1e4 * sizes if what[0] == "q" else 1e-9)
+        if what[0] == "q":
+            # a key's size with a write strength that keeps its update stable
+            s = torch.exp2(torch.randint(-6, 1, (500, 1), generator=g).float())
+            times("k", s[..., None])
+        else:
+            times("k", 2.0 ** 20)
+            d["beta"].mul_(2.0 ** -40)
+    ro, rS = gdn_reference(**d, cu=cu, **kw)
+    o, S = kda.gdn_prefill(**_dev(d, cuda_dev), cu_seqlens=cu.to(cuda_dev), scale=kw.get("scale", 1.0),
+                           qk_l2norm=kw.get("l2", True))
+    if what == "zero v":
+        assert (o == 0).all() and (S == 0).all()
+        return
+    _check(o, S, ro, rS, [500], tol_o=ONCE)
+    # and token by token: no row is off by more than the largest of its chunk's and its own roundings
+    for h in range(2):
+        row = ro[:, h].norm(dim=-1)
+        off = (o[:, h].double().cpu() - ro[:, h]).norm(dim=-1)
+        assert (off <= 2.0 ** -8 * row + 2.0 ** -9 * torch.stack([row[c // 128 * 128:c + 1].max() for c in range(500)])).all()
