@@ -697,12 +697,14 @@ def _cuda_device(t, name):
 
 
 def _cu_pair(cu, cu_host, total, dev, name="cu_seqlens"):
-    """Device and host copy of sequence bounds.  cu None: one sequence.  cu_host None:
-    copied from the device (synchronises); a caller who has the lengths on the host
-    passes both and saves that."""
-    if cu is None:
-        if cu_host is None:
-            cu_host = torch.tensor([0, total], dtype=torch.int32)
+    """Device and host copy of sequence bounds.  Both None: one sequence, written on the
+    device (a copy from here could not be captured).  cu_host None: copied from the device
+    (synchronises); a caller who has the lengths on the host passes both and saves that."""
+    if cu is None and cu_host is None:
+        cu_host = torch.tensor([0, total], dtype=torch.int32)
+        cu = torch.zeros(2, dtype=torch.int32, device=dev)
+        cu[1:].fill_(total)
+    elif cu is None:
         cu = cu_host.to(dev)
     elif cu_host is None:
         cu_host = cu.to("cpu")

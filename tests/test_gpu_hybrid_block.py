@@ -208,3 +208,44 @@ def test_offsets_past_32_bits(kda_lib, cuda_dev):
     assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
     got = kda.window_prefill(heads(0, 16), heads(16, 2), heads(18, 2), 5)
     assert torch.equal(got, kda.window_prefill(*(x.contiguous() for x in (tok[:, :16], tok[:, 16:18], tok[:, 18:])), 5))
+
+
+def test_prompts_captured(kda_lib, cuda_dev):
+    """The prompts' calls in a graph: bounds left out (one sequence) and given, the ring caches filled beside the
+    prefill.  Each replay on new inputs leaves the bits of the same calls outside a graph."""
+    import serving_kda_chunked_gated_gb300.kda as kda
+    g = torch.Generator(device=cuda_dev).manual_seed(53)
+    r = lambda *s: torch.randn(*s, generator=g, device=cuda_dev)                              # noqa: E731
+    bf, T = torch.bfloat16, 700
+    x = dict(q=r(T, 4, 128).to(bf), k=r(T, 2, 128).to(bf), v=r(T, 2, 128).to(bf), z=r(T, 2) - 3, beta=torch.sigmoid(r(T, 2)))
+    A, kc, vc = torch.zeros(2, device=cuda_dev), *(torch.zeros(3, 110, 2, 128, dtype=bf, device=cuda_dev) for _ in "kv")
+    cu = torch.tensor([0, 300, 300, T], dtype=torch.int32)
+    cud, slots = cu.to(cuda_dev), torch.tensor([2, 1, 0], dtype=torch.int32, device=cuda_dev)
+
+    def run():
+        a = kda.gdn_prefill(x["k"], x["k"], x["v"], x["z"], x["beta"], A)
+        w = kda.window_prefill(x["q"], x["k"], x["v"], 100, 10)
+        k0, v0 = kc[:1], vc[:1]
+        u = kda.window_prefill(x["q"], x["k"], x["v"], 60, 3, k_cache=k0, v_cache=v0)
+        t = kda.window_prefill(x["q"], x["k"], x["v"], 100, 10, cud, cu, k_cache=kc, v_cache=vc, slots=slots)
+        return [*a, w, u, t]
+
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = run()
+    for _ in range(2):
+        for n, t in x.items():
+            t.copy_(torch.sigmoid(r(*t.shape)) if n == "beta" else r(*t.shape) - (3 if n == "z" else 0))
+        for c in (kc, vc):
+            c.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in held + [kc, vc]]
+        for c in (kc, vc):
+            c.zero_()
+        want = run() + [kc, vc]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert kda.device_error(None) == kda.KDA_OK
