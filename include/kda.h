@@ -14,7 +14,8 @@
  * Conventions shared by every entry point:
  *  - Every pointer argument is DEVICE memory owned by the caller, unless the
  *    comment says otherwise.  The library never allocates device memory and
- *    keeps no state between calls.
+ *    keeps no state between calls but the error words of its own (see
+ *    kda_get_last_device_error).
  *  - All work is enqueued on the caller's `stream` (cudaStream_t passed as
  *    void*; NULL = legacy default stream).  Calls return as soon as the work
  *    is enqueued; arguments are validated on the host before anything is

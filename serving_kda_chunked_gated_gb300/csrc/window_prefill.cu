@@ -580,7 +580,8 @@ window_prefill_kernel(const __grid_constant__ PfParams p, const __grid_constant_
                         e0 = exp2f(e0);
                         e1 = exp2f(e1);
                         add2(l0, l1, e0, e1);
-                        // weights rounded to bf16 for the product; l keeps float32
+                        // weights rounded to bf16 for the product (its operands share a type, and V is
+                        // bf16; a second part would double P V and the stores of P); l keeps float32
                         const __nv_bfloat162 h = __floats2bfloat162_rn(e0, e1);
                         w[c >> 1] = *reinterpret_cast<const uint32_t*>(&h);
                     }
