@@ -726,8 +726,11 @@ kda_status kda_paged_read(const kda_paged_read_args* args, void* stream);
  * never reaches.
  * workspace: kda_paged_prefill_workspace_size(args) bytes (0: for refused arguments), else
  * KDA_ERR_WORKSPACE.  Its first 4 bytes are the call's error word, read with
- * kda_get_last_device_error (a call with T_total = 0 leaves it as it was).  Calls that may run at the same time need a
- * workspace each.
+ * kda_get_last_device_error; the next call on the workspace overwrites it, read or not (one with T_total = 0 leaves it as
+ * it was).  Calls that may run at the same time need a workspace each.
+ * error: a device word (int32, zero before its first call) or NULL.  It takes the reports of all calls that it is given to and
+ * stays set until kda_get_last_device_error(error, stream) reads it: one read behind a stack of layers, or of calls without a kept
+ * workspace, tells whether any of them gave up.
  */
 typedef struct {
     kda_paged_cache cache;
@@ -742,6 +745,7 @@ typedef struct {
     float* lse;
     void* workspace;
     size_t workspace_bytes;
+    int32_t* error;
 } kda_paged_prefill_args;
 
 size_t kda_paged_prefill_workspace_size(const kda_paged_prefill_args* args);
@@ -787,7 +791,7 @@ kda_status kda_paged_decode(const kda_paged_decode_args* args, void* stream);
  *
  * kda_get_last_device_error waits for the work queued on `stream`, then reads
  * and clears the error word of `workspace` (the workspace the prefill calls
- * used, kda_paged_prefill's among them, or the word given to kda_window_prefill), or, with workspace == NULL,
+ * used, kda_paged_prefill's among them, or the word given to kda_window_prefill or kda_paged_prefill), or, with workspace == NULL,
  * those of the fixed array kda_prefill_noalloc uses on the current device and of the
  * kda_window_prefill calls without a word of their own (it stays set until it is
  * read).  Returns KDA_OK when no wait gave up,

@@ -71,7 +71,9 @@ kda_status check(const kda_paged_prefill_args* a) {
     if (st != KDA_OK) return st;
     if (!a->cu_seqlens || !a->cu_seqlens_host) return KDA_ERR_NULL;
     if (a->T_total > 0 && (!a->q || !a->o)) return KDA_ERR_NULL;
-    if (misaligned(a->cu_seqlens) || misaligned(a->q) || misaligned(a->o) || misaligned(a->lse)) return KDA_ERR_ALIGN;
+    if (misaligned(a->cu_seqlens) || misaligned(a->q) || misaligned(a->o) || misaligned(a->lse) ||
+        misaligned(a->error))
+        return KDA_ERR_ALIGN;
     const int32_t* cu = a->cu_seqlens_host;
     if (cu[0] != 0 || cu[a->cache.num_seqs] != a->T_total) return KDA_ERR_SEQLENS;
     for (int n = 0; n < a->cache.num_seqs; ++n)

@@ -85,7 +85,7 @@ struct PfParams {
     int neg;                                // scale < 0: S = -Q K^T
     int wide;                               // o is 32-byte aligned
     uint32_t wait_limit;
-    int* error;                             // the call's error word
+    int* error;                             // the call's error word (a.error: the caller's, for many calls)
     int* errors;                            // [CTAs]: what each has to report
     Split* split;                           // [CTAs]: of the unit that the range's start splits, where it is the first start in it
     float* parts;                           // [CTAs][2]: 256 rows of O, then m and l
@@ -876,7 +876,10 @@ join_rows_kernel(const __grid_constant__ PfParams p, int ctas) {
         int e = 0;
         for (int i = threadIdx.x; i < ctas; i += 32) e |= p.errors[i];
         e = __reduce_or_sync(~0u, (unsigned)e);
-        if (threadIdx.x == 0) *p.error = e;
+        if (threadIdx.x == 0) {
+            *p.error = e;
+            if (e && p.a.error) atomicOr(p.a.error, e);
+        }
     }
     if ((int)blockIdx.x + 1 >= ctas) return;
     const Split d = p.split[blockIdx.x + 1];

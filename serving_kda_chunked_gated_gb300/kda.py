@@ -174,6 +174,7 @@ class PagedPrefillArgs(ctypes.Structure):
         ("cache", PagedCache), ("T_total", ctypes.c_int), ("Hq", ctypes.c_int), ("dtype", ctypes.c_int),
         ("cu_seqlens", _vp), ("cu_seqlens_host", _vp), ("q", _vp), ("q_stride", ctypes.c_long),
         ("scale", ctypes.c_float), ("o", _vp), ("lse", _vp), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t),
+        ("error", _vp),
     ]
 
 
@@ -264,7 +265,7 @@ def launch_count() -> int:
 def device_error(workspace=None, stream=None) -> int:
     """``kda_get_last_device_error``: waits for ``stream``, then reads and clears
     the error word of ``workspace`` (a prefill workspace tensor, or the ``error`` of
-    ``window_prefill``), or, when ``workspace`` is None, of the array
+    ``window_prefill`` or ``paged_prefill``), or, when ``workspace`` is None, of the array
     ``kda_prefill_noalloc`` uses and of window prefills without one.  Returns
     KDA_OK (0) or KDA_ERR_TIMEOUT (9); raises on any other status."""
     st = load_library().kda_get_last_device_error(_p(workspace), _stream(stream))
@@ -1065,13 +1066,15 @@ def paged_read(k_cache, v_cache, tables, lens, tokens, cu_seqlens=None, k_scale=
 
 @_on_stream
 def paged_prefill(q, k_cache, v_cache, tables, lens, cu_seqlens=None, cu_seqlens_host=None, k_scale=None, v_scale=None,
-                  scale=None, want_lse=False, out=None, workspace=None):
+                  scale=None, want_lse=False, out=None, workspace=None, error=None):
     """Causal attention of packed new tokens over their sequences' pages, through ``kda_paged_prefill``.  The
     tokens' own keys and values are in the pages already (``paged_write``).
 
     q: [T, Hq, d] bf16 (contiguous, or a slice of a packed projection), d = 64 or 128, Hq a multiple of
     Hkv; sequence n's queries, bounded by cu_seqlens (None: one sequence) and its host copy, are its last
-    positions.  scale: d ** -0.5 by default.  workspace as for ``gdn_prefill``.
+    positions.  scale: d ** -0.5 by default.  workspace as for ``gdn_prefill``; ``device_error(workspace)`` tells of the last
+    call on it alone.  error: an int32 tensor of one zero that keeps the reports of all calls it is given to until
+    ``device_error(error)`` reads it (the only way to learn of a wait that gave up in a call with a workspace of its own).
     Returns o, or (o, lse [T, Hq] f32) with want_lse.
     """
     dev = _cuda_device(q, "q")
@@ -1087,7 +1090,7 @@ def paged_prefill(q, k_cache, v_cache, tables, lens, cu_seqlens=None, cu_seqlens
     qp, qs = _heads("q", q, (T, Hq, d), torch.bfloat16, dev)
     a = PagedPrefillArgs(cache, T, Hq, KDA_BF16, cup, cu_host.data_ptr(), qp, qs,
                          d ** -0.5 if scale is None else scale, _dense("out", o, (T, Hq, d), torch.bfloat16, dev),
-                         lse.data_ptr() if want_lse else None, None, 0)
+                         lse.data_ptr() if want_lse else None, None, 0, _dense("error", error, (1,), torch.int32, dev))
     _launch_paged("kda_paged_prefill", a, dev, workspace)
     return (o, lse) if want_lse else o
 
