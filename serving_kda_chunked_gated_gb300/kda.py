@@ -961,17 +961,6 @@ def window_decode(q, k, v, k_cache, v_cache, positions, window, sinks=0, slots=N
 # any word.  Each call takes stream=None beside the arguments shown.
 # ---------------------------------------------------------------------------
 
-def _words(name, x, shape, dev):
-    """int32 words that a scheduler slices out of larger arrays (``lens[1:]``, some rows of a table), and their address:
-    the entry points want 16 bytes' alignment, so what starts elsewhere is copied on the device (a captured call copies it
-    again at every replay).  The caller keeps the tensor until its launch."""
-    p = _dense(name, x, shape, torch.int32, dev)
-    if p is None or p & 15 == 0:
-        return x, p
-    x = x.clone()
-    return x, x.data_ptr()
-
-
 def _paged_cache(k_cache, v_cache, k_scale, v_scale, tables, lens, dev) -> PagedCache:
     shape, width, dt = k_cache.shape, tables.shape, k_cache.dtype
     if len(shape) != 4 or len(width) != 2:
@@ -992,11 +981,14 @@ def _paged_cache(k_cache, v_cache, k_scale, v_scale, tables, lens, dev) -> Paged
     for name, x in (("pages", pages), ("tokens of a page", size), ("sequences", N), ("pages of a sequence", wide)):
         if x >= 2 ** 31:
             raise KDAError(f"the number of {name} must fit 32 bits, got {x}")
-    tables, tp = _words("tables", tables, width, dev)
-    lens, lp = _words("lens", lens, (N,), dev)
+    tp, lp = _dense("tables", tables, width, torch.int32, dev), _dense("lens", lens, (N,), torch.int32, dev)
     cache = PagedCache(_dense("k_cache", k_cache, shape, dt, dev), _dense("v_cache", v_cache, shape, dt, dev), ks, vs, code,
                        pages, size, heads, d, tp, lp, N, wide)
-    cache.words = tables, lens                    # alive until the launch
+    # A scheduler's slices (lens[1:], some rows of a table) start at any word.  The entry points want 16 bytes' alignment, so those
+    # are copied on the device, by a captured call at every replay; the copies live until the call returns.
+    if (tp | lp) & 15:
+        cache.copies = tables, lens = tables.clone(), lens.clone()
+        cache.tables, cache.lens = tables.data_ptr(), lens.data_ptr()
     return cache
 
 
@@ -1042,7 +1034,10 @@ def paged_write(k, v, k_cache, v_cache, tables, lens, cu_seqlens=None, k_scale=N
     T = _int32("the number of tokens", k.shape[0])
     kp, ks = _heads("k", k, (T, cache.Hkv, cache.d), k.dtype, dev)
     vp, vs = _heads("v", v, (T, cache.Hkv, cache.d), k.dtype, dev)
-    cu, cup = _words("cu_seqlens", cu_seqlens, (cache.num_seqs + 1,), dev)
+    cup = _dense("cu_seqlens", cu_seqlens, (cache.num_seqs + 1,), torch.int32, dev)
+    if cup and cup & 15:
+        cu_seqlens = cu_seqlens.clone()
+        cup = cu_seqlens.data_ptr()
     a = PagedWriteArgs(cache, T, _dtype_code(k), cup, kp, vp, ks, vs)
     _launch("kda_paged_write", a, dev)
 
@@ -1058,7 +1053,10 @@ def paged_read(k_cache, v_cache, tables, lens, tokens, cu_seqlens=None, k_scale=
     cache = _paged_cache(k_cache, v_cache, k_scale, v_scale, tables, lens, dev)
     shape = (_int32("the number of tokens", tokens), cache.Hkv, cache.d)
     k, v = [torch.empty(shape, dtype=dtype, device=dev) for _ in "kv"] if out is None else out
-    cu, cup = _words("cu_seqlens", cu_seqlens, (cache.num_seqs + 1,), dev)
+    cup = _dense("cu_seqlens", cu_seqlens, (cache.num_seqs + 1,), torch.int32, dev)
+    if cup and cup & 15:
+        cu_seqlens = cu_seqlens.clone()
+        cup = cu_seqlens.data_ptr()
     a = PagedReadArgs(cache, tokens, _dtype_code(k), cup, _dense("k", k, shape, dtype, dev), _dense("v", v, shape, dtype, dev))
     _launch("kda_paged_read", a, dev)
     return k, v
@@ -1084,11 +1082,12 @@ def paged_prefill(q, k_cache, v_cache, tables, lens, cu_seqlens=None, cu_seqlens
     if cu_host.shape[0] != cache.num_seqs + 1 or d != cache.d:
         raise KDAError(f"cu_seqlens bounds {cu_host.shape[0] - 1} sequences, heads of {d}; the cache has "
                        f"{cache.num_seqs}, heads of {cache.d}")
-    cu, cup = _words("cu_seqlens", cu, cu_host.shape, dev)
+    if cu.data_ptr() & 15:
+        cu = cu.clone()
     o = torch.empty((T, Hq, d), dtype=q.dtype, device=dev) if out is None else out
     lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if want_lse else None
     qp, qs = _heads("q", q, (T, Hq, d), torch.bfloat16, dev)
-    a = PagedPrefillArgs(cache, T, Hq, KDA_BF16, cup, cu_host.data_ptr(), qp, qs,
+    a = PagedPrefillArgs(cache, T, Hq, KDA_BF16, cu.data_ptr(), cu_host.data_ptr(), qp, qs,
                          d ** -0.5 if scale is None else scale, _dense("out", o, (T, Hq, d), torch.bfloat16, dev),
                          lse.data_ptr() if want_lse else None, None, 0, _dense("error", error, (1,), torch.int32, dev))
     _launch_paged("kda_paged_prefill", a, dev, workspace)
