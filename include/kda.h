@@ -659,6 +659,7 @@ kda_status kda_window_decode(const kda_window_decode_args* args, void* stream);
  *  - positions before 0 (more new tokens than lens[n]) do not exist: nothing is
  *    written for them, they read as 0, their queries see nothing;
  *  - a page outside [0, num_pages) reads as zeros and is not written.
+ * tables and lens start on 16 bytes like every pointer (the Python binding copies slices that do not).
  * Table entries past a sequence's last page are not read, and what pages hold past a
  * sequence's last token is not used, whatever it is.
  * Supported: d = 64 or 128, page_size a multiple of 16, num_pages page_size < 2^31 - 256,
@@ -759,6 +760,8 @@ kda_status kda_paged_prefill(const kda_paged_prefill_args* args, void* stream);
  * The new token takes part as it is stored.  Weights keep 16 bits or more, over 8-bit pages 11: o is off by little but its own
  * rounding to bf16.  A sequence of length 0 has o = 0 and lse = -inf.
  * When k and v are given, the place of a sequence's last token is that of no other sequence's token.
+ * Tables no wider than the batch needs are faster where sequences are short: with at most 16 tiles a row (256 tokens, over 8-bit pages 512)
+ * and many units no sequence is cut and nothing joined (256 sequences of 100 tokens: 24.7 us, under tables for 8192 tokens 32.0).
  * workspace: kda_paged_decode_workspace_size(args) bytes, else KDA_ERR_WORKSPACE; its contents need not be kept between
  * calls, and calls that may run at the same time (two streams, two graphs) need one each.
  */

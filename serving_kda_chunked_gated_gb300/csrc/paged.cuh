@@ -92,13 +92,14 @@ KDA_DEV uint32_t half2_of(uint32_t codes) {
     asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(h) : "r"(codes));
     return h;
 }
-// four codes as two bf16 pairs, times s (a power of two: exact), the first code lowest
+// a bf16 pair of the values times s (a power of two: exact), v.x lowest
 KDA_DEV uint32_t scaled2(float2 v, float s) {
     uint32_t r;
     asm("{\n\t.reg .b64 v, s;\n\t.reg .f32 a, b;\n\tmov.b64 v, {%1, %2};\n\tmov.b64 s, {%3, %3};\n\t"
         "mul.rn.ftz.f32x2 v, v, s;\n\tmov.b64 {a, b}, v;\n\tcvt.rn.bf16x2.f32 %0, b, a;\n\t}" : "=r"(r) : "f"(v.x), "f"(v.y), "f"(s));
     return r;
 }
+// four codes as two bf16 pairs, times s, the first code lowest
 KDA_DEV uint2 values4_bf16(uint32_t codes, float s) {
     return make_uint2(scaled2(values2((uint16_t)codes), s), scaled2(values2((uint16_t)(codes >> 16)), s));
 }

@@ -1098,7 +1098,8 @@ def paged_prefill(q, k_cache, v_cache, tables, lens, cu_seqlens=None, cu_seqlens
 def paged_decode(q, k_cache, v_cache, tables, lens, k=None, v=None, k_scale=None, v_scale=None, scale=None,
                  want_lse=False, out=None, workspace=None):
     """One new token of every sequence through ``kda_paged_decode``: q [N, Hq, d] bf16 attends over its
-    sequence's pages; k, v [N, Hkv, d] bf16, when given, are written at the last position first.
+    sequence's pages; k, v [N, Hkv, d] bf16, when given, are written at the last position first.  Tables no wider than the
+    batch needs are faster where all sequences are short.
     Returns o [N, Hq, d], or (o, lse [N, Hq] f32) with want_lse.
     """
     dev = _cuda_device(q, "q")
